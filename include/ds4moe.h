@@ -242,6 +242,93 @@ int ds4moe_set_test_stall(ds4moe_handle* h, int32_t stage);
 /* Frees everything the handle owns. NULL is allowed. Synchronises the device first. */
 void ds4moe_destroy(ds4moe_handle* h);
 
+/* ---------------------------------------------------------------------------------------------
+ * Operators on 16-bit matrices: what stands next to the quantized layer in a model whose other
+ * weights are kept in bf16 or fp16, and in its training. They need no handle: every operand,
+ * result and scratch buffer is the caller's device memory on the calling thread's current device
+ * (DS4MOE_ERR_INVALID_ARG for host memory, DS4MOE_ERR_DEVICE_MISMATCH for another GPU's), they
+ * allocate nothing, launch asynchronously on `stream`, can be captured in a CUDA graph, and may
+ * run on several streams at once as long as these do not share a workspace. Repeated calls are
+ * bitwise identical (fixed summation order, no float atomics).
+ *
+ * Matrices are row-major; `ld...` is the distance in elements from one row to the next (at least
+ * the row's width; 0 means the width itself). Rows need only their element's alignment; operands
+ * whose addresses and row distances are multiples of 16 bytes are read by the TMA unit, others by
+ * ordinary loads (slower). dtype (DS4MOE_BF16 or DS4MOE_FP16) is the type of all 16-bit operands
+ * and results of a call. Products accumulate in fp32 and round once. Results must not overlap
+ * inputs except where said. Widths n, k, d and vocab are 1..2^24, rows 0..2^24. */
+typedef enum ds4moe_dtype { DS4MOE_BF16 = 0, DS4MOE_FP16 = 1, DS4MOE_FP32 = 2 } ds4moe_dtype;
+typedef enum ds4moe_act { DS4MOE_ACT_NONE = 0, DS4MOE_ACT_RELU = 1, DS4MOE_ACT_SILU = 2, DS4MOE_ACT_GELU = 3 } ds4moe_act;
+
+/* Products grouped by expert with ragged sizes. The rows are ordered by group: group g owns rows
+ * offsets[g] .. offsets[g+1]-1 (offsets: device int32 [n_groups + 1], non-decreasing, starting at
+ * 0 and at most `rows`; n_groups 1..1024; a group may be empty). Group g's weights are
+ * W_g = w + g * w_stride, [n x k] with row distance ldw (w_stride 0 means n * ldw).
+ *   ds4moe_grouped_mm      y[t]  = W_g x[t]            x [rows x k], y [rows x n]
+ *   ds4moe_grouped_mm_dx   dx[t] = W_g^T dy[t]         dy [rows x n], dx [rows x k]
+ *   ds4moe_grouped_mm_dw   dW_g  = sum_t dy[t] x[t]^T  dW_g = dw + g * dw_stride, [n x k]; zero for
+ *                          an empty group. dw_dtype is dtype or DS4MOE_FP32; accumulate != 0 adds to
+ *                          what dw holds.
+ * The offsets are read on the device: nothing is synchronised. Offsets out of range are clamped to
+ * [0, rows] and a group whose end lies before its start is empty. Rows that belong to no group
+ * (from offsets[n_groups] on) are neither read nor written. */
+int ds4moe_grouped_mm(const void* x, const void* w, const int32_t* offsets, void* y, int32_t rows, int32_t n,
+                      int32_t k, int32_t n_groups, int32_t dtype, int64_t ldx, int64_t ldw, int64_t w_stride,
+                      int64_t ldy, void* stream);
+int ds4moe_grouped_mm_dx(const void* dy, const void* w, const int32_t* offsets, void* dx, int32_t rows, int32_t n,
+                         int32_t k, int32_t n_groups, int32_t dtype, int64_t lddy, int64_t ldw, int64_t w_stride,
+                         int64_t lddx, void* stream);
+int ds4moe_grouped_mm_dw(const void* dy, const void* x, const int32_t* offsets, void* dw, int32_t rows, int32_t n,
+                         int32_t k, int32_t n_groups, int32_t dtype, int32_t dw_dtype, int32_t accumulate,
+                         int64_t lddy, int64_t ldx, int64_t lddw, int64_t dw_stride, void* stream);
+
+/* Dense product with bias, activation and residual: z = W x + bias, y = act(z) + residual, in fp32,
+ * rounded once. x [rows x k], w [n x k], bias [n] or NULL, residual [rows x n] or NULL (it may be y
+ * itself), y [rows x n]; zout [rows x n] or NULL receives z rounded to dtype, which the gradient of
+ * an activation needs. silu(z) = z / (1 + exp(-z)); gelu is the exact form with erf. */
+int ds4moe_linear(const void* x, const void* w, const void* bias, const void* residual, void* y, void* zout,
+                  int32_t rows, int32_t n, int32_t k, int32_t act, int32_t dtype, int64_t ldx, int64_t ldw,
+                  int64_t ldr, int64_t ldy, int64_t ldz, void* stream);
+
+/* Its gradients, for dy [rows x n]: dz = dy * act'(z), dx = W^T dz [rows x k], dw = sum_t dz[t] x[t]^T
+ * [n x k], db = sum_t dz[t] [n] (the residual's gradient is dy itself). z is what zout received (not
+ * read, may be NULL, for DS4MOE_ACT_NONE). Each of dx, dw, db may be NULL: it is then not computed (w is
+ * read only for dx, x only for dw). rows == 0 writes zeros into dw and db. dz is rounded to dtype
+ * between its computation and the products; db sums the unrounded dz in fp32. workspace: 16-byte
+ * aligned device memory of ds4moe_linear_grad_workspace bytes (DS4MOE_ERR_CAPACITY if less). */
+int64_t ds4moe_linear_grad_workspace(int32_t rows, int32_t n, int32_t act);
+int ds4moe_linear_grad(const void* dy, const void* x, const void* w, const void* z, void* dx, void* dw, void* db,
+                       int32_t rows, int32_t n, int32_t k, int32_t act, int32_t dtype, int64_t lddy, int64_t ldx,
+                       int64_t ldw, int64_t ldz, int64_t lddx, int64_t lddw, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of the logits z[t] = W x[t], without storing them: lse[t] = log sum_v exp z[t][v],
+ * loss[t] = lse[t] - z[t][labels[t]] (fp32 [rows] each). x [rows x d], w [vocab x d], labels device int32
+ * [rows]. A row whose label is ignore_index has loss 0 and no gradient; so has one whose label lies outside
+ * [0, vocab), which also sets bit 0 of ds4moe_ops_status. lse is written for every row.
+ *   ds4moe_cross_entropy_grad: for dloss (fp32 [rows]) and the lse of the forward,
+ *     dz[t][v] = (exp(z[t][v] - lse[t]) - [v == labels[t]]) * dloss[t],
+ *     dx[t] = sum_v dz[t][v] W[v], dw[v] = sum_t dz[t][v] x[t], rounded to dtype. Either may be NULL.
+ *     The logits are computed again one piece of the vocabulary at a time and dz is rounded to dtype
+ *     (relative to the largest |dloss|, so that fp16 does not underflow) in the workspace.
+ * workspace: 16-byte aligned device memory. The gradient takes the largest piece that fits, up to 8192
+ * columns; ds4moe_cross_entropy_workspace returns the bytes that let either call run at full speed, and
+ * less than the smallest usable size returns DS4MOE_ERR_CAPACITY. */
+int64_t ds4moe_cross_entropy_workspace(int32_t rows, int32_t vocab, int32_t d);
+int ds4moe_cross_entropy(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int32_t rows,
+                         int32_t vocab, int32_t d, int32_t dtype, int32_t ignore_index, int64_t ldx, int64_t ldw,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+int ds4moe_cross_entropy_grad(const void* x, const void* w, const int32_t* labels, const float* lse,
+                              const float* dloss, void* dx, void* dw, int32_t rows, int32_t vocab, int32_t d,
+                              int32_t dtype, int32_t ignore_index, int64_t ldx, int64_t ldw, int64_t lddx,
+                              int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Device-side conditions of the 16-bit operators on the current device since the last call of this
+ * function: synchronises the device, copies the flags to the host word and clears them. bit 0: a label
+ * outside the vocabulary; bit 2: a pipeline wait gave up after its time limit (about one second) and the
+ * results of that call are incomplete, one of bits 17..23 names the wait. */
+int ds4moe_ops_status(int32_t* flags);
+
 /* Message of the last failed call on this thread ("" if none). */
 const char* ds4moe_last_error(void);
 

@@ -1,0 +1,129 @@
+// Products of 16-bit matrices (bf16 or fp16, fp32 accumulation) and their epilogues: the shared
+// description of one product and the per-element epilogue arithmetic.
+//
+// Every product of the 16-bit operators is written as
+//   out[c][l] = sum_r A(l, r) B(c, r),   l < lanes (contiguous in the output), c < cols, r < red,
+// where A and B are row-major matrices read along either index:
+//   y  = x W^T    lanes = output features (A = W, r contiguous), cols = rows of x (B = x, r contiguous)
+//   dx = dy W     lanes = input features (A = W, l contiguous),  cols = rows (B = dy, r contiguous)
+//   dW = dy^T x   lanes = input features (A = x, l contiguous),  cols = output features (B = dy, c contiguous)
+#pragma once
+
+#include "common.cuh"
+
+namespace ds4 {
+
+enum MmRag : int {
+  MM_DENSE = 0,
+  MM_RAG_COLS = 1,  // group g owns columns offsets[g] .. offsets[g+1]-1; A moves by its group stride
+  MM_RAG_RED = 2    // group g owns that range of the reduction; the output moves by its group stride
+};
+enum MmEpi : int {
+  MM_EPI_STORE = 0,     // out = act(v + bias) + residual, or v * scale + what is there
+  MM_EPI_STATS = 1,     // per column: max and sum of exponentials over the tile's lanes; the label's value
+  MM_EPI_SOFTGRAD = 2   // out = (exp(v - lse) - [lane is the label]) * g
+};
+enum MmAct : int { MM_ACT_NONE = 0, MM_ACT_RELU = 1, MM_ACT_SILU = 2, MM_ACT_GELU = 3 };
+
+struct MmOperand {
+  const void* p;
+  int64_t ld;            // elements from one row to the next
+  int64_t group_stride;  // A only: elements from one group's matrix to the next
+  int red_major;         // 1: the reduction index is the contiguous one
+};
+
+struct MmEpiArgs {
+  void* out;
+  int64_t ld, group_stride;  // elements
+  int out_f32;               // out is fp32 (else the operands' type)
+  int accumulate;            // out += v (out's own type; read in fp32)
+  const float* acc_in;       // [cols][acc_ld] fp32 added to v, or null
+  int64_t acc_ld;
+  const float* scale;        // device scalar that multiplies the final sum, or null
+  const void* bias;          // [lanes] or null
+  const void* residual;      // [cols][ldr] or null
+  int64_t ldr;
+  void* z;                   // [cols][ldz] or null: v + bias, rounded
+  int64_t ldz;
+  int act;
+  // cross entropy: lanes are a piece of the vocabulary from lane0, columns are tokens
+  int lane0, vocab, ignore;
+  const int* labels;
+  const float* lse;
+  const float* g;        // dloss
+  const float* gscale;   // device scalar: max |g|
+  float2* part;          // [lane tiles][cols] (max, sum)
+  float* zlab;           // [cols] the label's logit
+};
+
+struct MmProblem {
+  MmOperand a, b;
+  int lanes, cols, red;
+  int groups;          // 1 when dense
+  const int* offsets;  // device [groups + 1], null when dense
+  int rag, epi, f16;
+  MmEpiArgs e;
+  int* err;            // error word (bit 2 and a site bit: a pipeline wait gave up)
+};
+
+// Group g's range of the ragged index, clamped so that no offset reaches outside [0, total].
+__device__ __forceinline__ int2 mm_range(const int* offsets, int g, int total) {
+  const int lo = min(max(__ldg(offsets + g), 0), total);
+  const int hi = min(max(__ldg(offsets + g + 1), lo), total);
+  return make_int2(lo, hi);
+}
+
+__device__ __forceinline__ float ld16(const void* p, int64_t i, int f16) {
+  return f16 ? __half2float(static_cast<const __half*>(p)[i]) : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void st16(void* p, int64_t i, float v, int f16) {
+  if (f16)
+    static_cast<__half*>(p)[i] = __float2half_rn(v);
+  else
+    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ float mm_act(float z, int act) {
+  if (act == MM_ACT_RELU) return z > 0.f ? z : z == z ? 0.f : z;  // NaN stays NaN
+  if (act == MM_ACT_SILU) return z / (1.f + __expf(-z));
+  if (act == MM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  return z;
+}
+__device__ __forceinline__ float mm_act_slope(float z, int act) {
+  if (act == MM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  if (act == MM_ACT_SILU) {
+    const float s = 1.f / (1.f + __expf(-z));
+    return s * (1.f + z * (1.f - s));
+  }
+  if (act == MM_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  return 1.f;
+}
+
+// dz of the cross entropy is kept in 16 bits as (exp(z - lse) - [label]) * (g / max |g|) * 2^13. The
+// division makes the label's term of a mean's gradient, -1 + p, a value just below a power of two,
+// which 8 bits hold to about p (kept with g folded in, every label's term carried the same rounding
+// error of up to 2^-9: the gradients were 1.6 times as far off as now); 2^13 keeps p down to 2^-27
+// a normal fp16 number.
+constexpr float kMmGradOne = 8192.f;
+
+// Lanes of one softmax partial: part[] has ceil(lanes / kMmLaneTile) rows of cols entries.
+constexpr int kMmLaneTile = 64;
+
+// Sets kernel attributes on the current device (once per device).
+cudaError_t mm_prepare();
+// Launches one product. Nothing to do (no lanes or columns) is not an error.
+cudaError_t mm_launch(const MmProblem& p, cudaStream_t s);
+
+// dz = dy * act'(z) rounded to 16 bits (dz null: not stored) and, when part is not null, its unrounded
+// column sums over chunks of rows, part[chunk][n]; then db = the sum over the chunks in order.
+int mm_colsum_chunks(int rows);
+cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz, float* part,
+                        void* db, int rows, int n, int act, int f16, cudaStream_t s);
+// Joins the softmax partials of each token: lse, loss, and bit 0 of *err for labels outside the vocabulary.
+cudaError_t mm_softmax_join(const float2* part, int tiles, const float* zlab, const int* labels, int ignore, int vocab,
+                            int rows, float* loss, float* lse, int* err, cudaStream_t s);
+// gs[0] = max |g| over the rows with a label (1 where that is 0 or not finite), gs[1] = gs[0] / kMmGradOne.
+cudaError_t mm_grad_scale(const float* g, const int* labels, int ignore, int vocab, int rows, float* gs, cudaStream_t s);
+
+}  // namespace ds4

@@ -32,8 +32,22 @@ EXPORTED = ("ds4moe_create", "ds4moe_create_subset", "ds4moe_forward", "ds4moe_f
             "ds4moe_get_route", "ds4moe_get_stats", "ds4moe_device_bytes",
             "ds4moe_launches_per_forward", "ds4moe_set_profiling", "ds4moe_get_phase_times", "ds4moe_route_noalloc",
             "ds4moe_set_test_stall",
+            "ds4moe_grouped_mm", "ds4moe_grouped_mm_dx", "ds4moe_grouped_mm_dw",
+            "ds4moe_linear", "ds4moe_linear_grad", "ds4moe_linear_grad_workspace",
+            "ds4moe_cross_entropy", "ds4moe_cross_entropy_grad", "ds4moe_cross_entropy_workspace",
+            "ds4moe_ops_status",
             "ds4moe_destroy", "ds4moe_last_error")
 DS4MOE_NOALLOC_MAX_LOGITS = 262144
+
+DS4MOE_BF16 = 0
+DS4MOE_FP16 = 1
+DS4MOE_FP32 = 2
+DTYPES = {"bf16": DS4MOE_BF16, "fp16": DS4MOE_FP16, "fp32": DS4MOE_FP32}
+DS4MOE_ACT_NONE = 0
+DS4MOE_ACT_RELU = 1
+DS4MOE_ACT_SILU = 2
+DS4MOE_ACT_GELU = 3
+ACTS = {"none": DS4MOE_ACT_NONE, "relu": DS4MOE_ACT_RELU, "silu": DS4MOE_ACT_SILU, "gelu": DS4MOE_ACT_GELU}
 
 
 class ds4moe_shapes(ctypes.Structure):
@@ -99,6 +113,21 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_route_noalloc.restype = ctypes.c_int
         L.ds4moe_set_test_stall.argtypes = [vp, i32]
         L.ds4moe_set_test_stall.restype = ctypes.c_int
+        L.ds4moe_grouped_mm.argtypes = [vp] * 4 + [i32] * 5 + [i64] * 4 + [vp]
+        L.ds4moe_grouped_mm_dx.argtypes = [vp] * 4 + [i32] * 5 + [i64] * 4 + [vp]
+        L.ds4moe_grouped_mm_dw.argtypes = [vp] * 4 + [i32] * 7 + [i64] * 4 + [vp]
+        L.ds4moe_linear.argtypes = [vp] * 6 + [i32] * 5 + [i64] * 5 + [vp]
+        L.ds4moe_linear_grad.argtypes = [vp] * 7 + [i32] * 5 + [i64] * 6 + [vp, i64, vp]
+        L.ds4moe_cross_entropy.argtypes = [vp] * 5 + [i32] * 5 + [i64] * 2 + [vp, i64, vp]
+        L.ds4moe_cross_entropy_grad.argtypes = [vp] * 7 + [i32] * 5 + [i64] * 4 + [vp, i64, vp]
+        L.ds4moe_ops_status.argtypes = [ctypes.POINTER(i32)]
+        for name in ("grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "linear", "linear_grad", "cross_entropy",
+                     "cross_entropy_grad", "ops_status"):
+            getattr(L, "ds4moe_" + name).restype = ctypes.c_int
+        L.ds4moe_linear_grad_workspace.argtypes = [i32, i32, i32]
+        L.ds4moe_linear_grad_workspace.restype = i64
+        L.ds4moe_cross_entropy_workspace.argtypes = [i32, i32, i32]
+        L.ds4moe_cross_entropy_workspace.restype = i64
         L.ds4moe_destroy.argtypes = [vp]
         L.ds4moe_destroy.restype = None
         L.ds4moe_last_error.argtypes = []
@@ -217,6 +246,92 @@ def ds4moe_route_noalloc(router_w, router_b, x, n_tokens: int, d: int, n_experts
 def ds4moe_set_test_stall(h: int, stage: int) -> None:
     """Test hook: the next batched forward's GEMM withholds one arrival and its waits give up (see the header)."""
     _check(lib().ds4moe_set_test_stall(h, stage))
+
+
+def _enum(table: dict, v) -> int:
+    if isinstance(v, str):
+        if v not in table:
+            raise ValueError(f"{v!r} is none of {sorted(table)}")
+        return table[v]
+    return int(v)
+
+
+# Operators on 16-bit matrices (see the header for the mathematics, layouts and limits). dtype and act
+# are names ("bf16", "fp16"; "none", "relu", "silu", "gelu") or the ABI's numbers; a row distance of 0
+# means that the rows lie back to back.
+
+
+def ds4moe_grouped_mm(x, w, offsets, y, rows: int, n: int, k: int, n_groups: int, dtype="bf16", ldx: int = 0,
+                      ldw: int = 0, w_stride: int = 0, ldy: int = 0, stream: int = 0) -> None:
+    """y[t] = W_g x[t] for the rows t of each group g."""
+    _check(lib().ds4moe_grouped_mm(_ptr(x), _ptr(w), _ptr(offsets), _ptr(y), rows, n, k, n_groups,
+                                   _enum(DTYPES, dtype), ldx, ldw, w_stride, ldy, stream))
+
+
+def ds4moe_grouped_mm_dx(dy, w, offsets, dx, rows: int, n: int, k: int, n_groups: int, dtype="bf16", lddy: int = 0,
+                         ldw: int = 0, w_stride: int = 0, lddx: int = 0, stream: int = 0) -> None:
+    """dx[t] = W_g^T dy[t] for the rows t of each group g."""
+    _check(lib().ds4moe_grouped_mm_dx(_ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx), rows, n, k, n_groups,
+                                      _enum(DTYPES, dtype), lddy, ldw, w_stride, lddx, stream))
+
+
+def ds4moe_grouped_mm_dw(dy, x, offsets, dw, rows: int, n: int, k: int, n_groups: int, dtype="bf16", dw_dtype=None,
+                         accumulate: bool = False, lddy: int = 0, ldx: int = 0, lddw: int = 0, dw_stride: int = 0,
+                         stream: int = 0) -> None:
+    """dW_g = sum over the rows t of group g of dy[t] x[t]^T (added to dw with accumulate)."""
+    dt = _enum(DTYPES, dtype)
+    _check(lib().ds4moe_grouped_mm_dw(_ptr(dy), _ptr(x), _ptr(offsets), _ptr(dw), rows, n, k, n_groups, dt,
+                                      dt if dw_dtype is None else _enum(DTYPES, dw_dtype), int(bool(accumulate)),
+                                      lddy, ldx, lddw, dw_stride, stream))
+
+
+def ds4moe_linear(x, w, bias, residual, y, rows: int, n: int, k: int, act="none", dtype="bf16", zout=None,
+                  ldx: int = 0, ldw: int = 0, ldr: int = 0, ldy: int = 0, ldz: int = 0, stream: int = 0) -> None:
+    """y = act(W x + bias) + residual; zout receives W x + bias."""
+    _check(lib().ds4moe_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(zout), rows, n, k,
+                               _enum(ACTS, act), _enum(DTYPES, dtype), ldx, ldw, ldr, ldy, ldz, stream))
+
+
+def ds4moe_linear_grad_workspace(rows: int, n: int, act="none") -> int:
+    return lib().ds4moe_linear_grad_workspace(rows, n, _enum(ACTS, act))
+
+
+def ds4moe_linear_grad(dy, x, w, z, dx, dw, db, rows: int, n: int, k: int, act="none", dtype="bf16",
+                       workspace=None, workspace_bytes: int = 0, lddy: int = 0, ldx: int = 0, ldw: int = 0,
+                       ldz: int = 0, lddx: int = 0, lddw: int = 0, stream: int = 0) -> None:
+    """Gradients of ds4moe_linear: dx, dw and db (each may be None)."""
+    _check(lib().ds4moe_linear_grad(_ptr(dy), _ptr(x), _ptr(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(db), rows, n, k,
+                                    _enum(ACTS, act), _enum(DTYPES, dtype), lddy, ldx, ldw, ldz, lddx, lddw,
+                                    _ptr(workspace), workspace_bytes, stream))
+
+
+def ds4moe_cross_entropy_workspace(rows: int, vocab: int, d: int) -> int:
+    return lib().ds4moe_cross_entropy_workspace(rows, vocab, d)
+
+
+def ds4moe_cross_entropy(x, w, labels, loss, lse, rows: int, vocab: int, d: int, dtype="bf16",
+                         ignore_index: int = -100, workspace=None, workspace_bytes: int = 0, ldx: int = 0,
+                         ldw: int = 0, stream: int = 0) -> None:
+    """loss[t] = lse[t] - z[t][labels[t]] of the logits z = W x, which are not stored."""
+    _check(lib().ds4moe_cross_entropy(_ptr(x), _ptr(w), _ptr(labels), _ptr(loss), _ptr(lse), rows, vocab, d,
+                                      _enum(DTYPES, dtype), ignore_index, ldx, ldw, _ptr(workspace),
+                                      workspace_bytes, stream))
+
+
+def ds4moe_cross_entropy_grad(x, w, labels, lse, dloss, dx, dw, rows: int, vocab: int, d: int, dtype="bf16",
+                              ignore_index: int = -100, workspace=None, workspace_bytes: int = 0, ldx: int = 0,
+                              ldw: int = 0, lddx: int = 0, lddw: int = 0, stream: int = 0) -> None:
+    """Gradients of sum_t dloss[t] loss[t] with respect to x and w (each may be None)."""
+    _check(lib().ds4moe_cross_entropy_grad(_ptr(x), _ptr(w), _ptr(labels), _ptr(lse), _ptr(dloss), _ptr(dx),
+                                           _ptr(dw), rows, vocab, d, _enum(DTYPES, dtype), ignore_index, ldx, ldw,
+                                           lddx, lddw, _ptr(workspace), workspace_bytes, stream))
+
+
+def ds4moe_ops_status() -> int:
+    """Flags that the 16-bit operators raised on the current device since the last call; clears them."""
+    flags = ctypes.c_int32()
+    _check(lib().ds4moe_ops_status(ctypes.byref(flags)))
+    return flags.value
 
 
 def ds4moe_destroy(h: Optional[int]) -> None:
