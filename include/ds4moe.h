@@ -312,8 +312,9 @@ int ds4moe_linear_grad(const void* dy, const void* x, const void* w, const void*
  *     The logits are computed again one piece of the vocabulary at a time and dz is rounded to dtype
  *     (relative to the largest |dloss|, so that fp16 does not underflow) in the workspace.
  * workspace: 16-byte aligned device memory. The gradient takes the largest piece that fits, up to 8192
- * columns; ds4moe_cross_entropy_workspace returns the bytes that let either call run at full speed, and
- * less than the smallest usable size returns DS4MOE_ERR_CAPACITY. */
+ * words; ds4moe_cross_entropy_workspace returns the bytes that let either call run at full speed. The
+ * forward needs 8 bytes per row and 256 words (and 4 per row), the gradient 16 + 4 rows d (rounded up to
+ * 16) + 512 (rows rounded up to 8); less returns DS4MOE_ERR_CAPACITY. */
 int64_t ds4moe_cross_entropy_workspace(int32_t rows, int32_t vocab, int32_t d);
 int ds4moe_cross_entropy(const void* x, const void* w, const int32_t* labels, float* loss, float* lse, int32_t rows,
                          int32_t vocab, int32_t d, int32_t dtype, int32_t ignore_index, int64_t ldx, int64_t ldw,

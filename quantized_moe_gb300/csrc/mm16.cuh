@@ -7,6 +7,11 @@
 //   y  = x W^T    lanes = output features (A = W, r contiguous), cols = rows of x (B = x, r contiguous)
 //   dx = dy W     lanes = input features (A = W, l contiguous),  cols = rows (B = dy, r contiguous)
 //   dW = dy^T x   lanes = input features (A = x, l contiguous),  cols = output features (B = dy, c contiguous)
+// and, of the cross entropy over a vocabulary with weights W, where dz is kept transposed ([v][t]):
+//   z          lanes = tokens (A = x, r contiguous), cols = words (B = W, r contiguous): a thread owns a
+//              token, so that its softmax needs no exchange between threads
+//   dx = dz W  lanes = features (A = W, l contiguous), cols = tokens (B = dz, c contiguous)
+//   dW = dz x  lanes = features (A = x, l contiguous), cols = words (B = dz, r contiguous)
 #pragma once
 
 #include "common.cuh"
@@ -20,8 +25,8 @@ enum MmRag : int {
 };
 enum MmEpi : int {
   MM_EPI_STORE = 0,     // out = act(v + bias) + residual, or v * scale + what is there
-  MM_EPI_STATS = 1,     // per column: max and sum of exponentials over the tile's lanes; the label's value
-  MM_EPI_SOFTGRAD = 2   // out = (exp(v - lse) - [lane is the label]) * g
+  MM_EPI_STATS = 1,     // per lane: max and sum of exponentials over the tile's columns; the label's value
+  MM_EPI_SOFTGRAD = 2   // out = (exp(v - lse) - [column is the label]) * g
 };
 enum MmAct : int { MM_ACT_NONE = 0, MM_ACT_RELU = 1, MM_ACT_SILU = 2, MM_ACT_GELU = 3 };
 
@@ -46,14 +51,14 @@ struct MmEpiArgs {
   void* z;                   // [cols][ldz] or null: v + bias, rounded
   int64_t ldz;
   int act;
-  // cross entropy: lanes are a piece of the vocabulary from lane0, columns are tokens
-  int lane0, vocab, ignore;
+  // cross entropy: lanes are tokens, columns a piece of the vocabulary from word0
+  int word0, vocab, ignore;
   const int* labels;
   const float* lse;
   const float* g;        // dloss
   const float* gscale;   // device scalar: max |g|
-  float2* part;          // [lane tiles][cols] (max, sum)
-  float* zlab;           // [cols] the label's logit
+  float2* part;          // [column tiles][lanes] (max, sum)
+  float* zlab;           // [lanes] the label's logit
 };
 
 struct MmProblem {
@@ -107,8 +112,8 @@ __device__ __forceinline__ float mm_act_slope(float z, int act) {
 // a normal fp16 number.
 constexpr float kMmGradOne = 8192.f;
 
-// Lanes of one softmax partial: part[] has ceil(lanes / kMmLaneTile) rows of cols entries.
-constexpr int kMmLaneTile = 64;
+// Words of one softmax partial: part[] has ceil(vocab / kMmStatTile) rows of one entry per token.
+constexpr int kMmStatTile = 256;
 
 // Sets kernel attributes on the current device (once per device).
 cudaError_t mm_prepare();

@@ -134,8 +134,8 @@ int64_t stride(Check& c, const char* name, int64_t v, int64_t n, int64_t ld) {
 
 // Workspace of the cross entropy: the forward's partials and label logits, or the gradient's scale
 // words, fp32 sum of dx and one piece of dz.
-int64_t ce_forward_bytes(int64_t rows, int64_t vocab) { return up(8 * rows * ((vocab + ds4::kMmLaneTile - 1) / ds4::kMmLaneTile), 16) + 4 * rows; }
-int64_t ce_grad_bytes(int64_t rows, int64_t d, int64_t piece) { return 16 + up(4 * rows * d, 16) + 2 * rows * piece; }
+int64_t ce_forward_bytes(int64_t rows, int64_t vocab) { return up(8 * rows * ((vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile), 16) + 4 * rows; }
+int64_t ce_grad_bytes(int64_t rows, int64_t d, int64_t piece) { return 16 + up(4 * rows * d, 16) + 2 * up(rows, 8) * piece; }
 
 }  // namespace
 
@@ -288,8 +288,8 @@ extern "C" int ds4moe_cross_entropy(const void* x, const void* w, const int32_t*
     int* err = c.err_word();
     if (!c.ok()) return c.code;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int tiles = (vocab + ds4::kMmLaneTile - 1) / ds4::kMmLaneTile;
-    ds4::MmProblem p = product(w, ldw, true, x, ldx, true, vocab, rows, d, dtype, nullptr, 0, err);
+    const int tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile;
+    ds4::MmProblem p = product(x, ldx, true, w, ldw, true, rows, vocab, d, dtype, nullptr, 0, err);
     p.epi = ds4::MM_EPI_STATS;
     p.e.labels = labels, p.e.vocab = vocab, p.e.ignore = ignore_index;
     p.e.part = static_cast<float2*>(workspace);
@@ -312,7 +312,7 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     if (!c.ok() || (!dx && !dw)) return c.code;
     // the largest piece of the vocabulary that the workspace holds
     const int64_t full = std::min<int64_t>(kPieceMax, up(vocab, kPieceMin));
-    int64_t piece = rows ? (workspace_bytes - ce_grad_bytes(rows, d, 0)) / (2 * (int64_t)rows) / kPieceMin * kPieceMin : full;
+    int64_t piece = rows ? (workspace_bytes - ce_grad_bytes(rows, d, 0)) / (2 * up(rows, 8)) / kPieceMin * kPieceMin : full;
     piece = std::min(piece, full);
     if (piece < kPieceMin) {
       c.fail(DS4MOE_ERR_CAPACITY, "workspace_bytes is less than the " + std::to_string(ce_grad_bytes(rows, d, kPieceMin)) + " of the smallest piece of the vocabulary");
@@ -334,24 +334,25 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     float* sum = reinterpret_cast<float*>(ws + 16);
     char* dz = ws + 16 + up(4 * (int64_t)rows * d, 16);
     const char* wb = static_cast<const char*>(w);
+    const int64_t lddz = up(rows, 8);
     cudaError_t e = ds4::mm_grad_scale(dloss, labels, ignore_index, vocab, rows, gs, s);
     for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += piece) {
       const int pv = (int)std::min<int64_t>(piece, vocab - v0);
       const bool last = v0 + pv == vocab;
-      ds4::MmProblem p = product(wb + 2 * v0 * ldw, ldw, true, x, ldx, true, pv, rows, d, dtype, dz, piece, err);
+      ds4::MmProblem p = product(x, ldx, true, wb + 2 * v0 * ldw, ldw, true, rows, pv, d, dtype, dz, lddz, err);
       p.epi = ds4::MM_EPI_SOFTGRAD;
-      p.e.lane0 = (int)v0, p.e.vocab = vocab, p.e.ignore = ignore_index;
+      p.e.word0 = (int)v0, p.e.vocab = vocab, p.e.ignore = ignore_index;
       p.e.labels = labels, p.e.lse = lse, p.e.g = dloss, p.e.gscale = gs;
       e = ds4::mm_launch(p, s);
       if (e == cudaSuccess && dx) {  // the pieces add up in fp32; the last one rounds
-        p = product(wb + 2 * v0 * ldw, ldw, false, dz, piece, true, d, rows, pv, dtype, last ? dx : sum, last ? lddx : d, err);
+        p = product(wb + 2 * v0 * ldw, ldw, false, dz, lddz, false, d, rows, pv, dtype, last ? dx : sum, last ? lddx : d, err);
         p.e.out_f32 = !last;
         p.e.acc_in = v0 ? sum : nullptr, p.e.acc_ld = d;
         p.e.scale = last ? gs + 1 : nullptr;
         e = ds4::mm_launch(p, s);
       }
       if (e == cudaSuccess && dw) {
-        p = product(x, ldx, false, dz, piece, false, d, pv, rows, dtype, static_cast<char*>(dw) + 2 * v0 * lddw, lddw, err);
+        p = product(x, ldx, false, dz, lddz, true, d, pv, rows, dtype, static_cast<char*>(dw) + 2 * v0 * lddw, lddw, err);
         p.e.scale = gs + 1;
         e = ds4::mm_launch(p, s);
       }

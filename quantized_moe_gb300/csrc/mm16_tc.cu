@@ -1,0 +1,724 @@
+// The 16-bit products on the 5th-generation tensor cores: out[c][l] = sum_r A(l, r) B(c, r).
+//
+// Persistent: one CTA (or pair of CTAs) per SM (or two SMs) loops over output tiles of 128 lanes per
+// CTA x up to BN columns. The lanes are the contiguous index of the output, so that a tensor-memory
+// lane is a lane of the output and a warp stores 32 neighbours; the columns are rows of tokens
+// (or of dW), of which a tile takes exactly what its group has, rounded up to the MMA's granule, so
+// that a group's weights cross HBM once however ragged the counts are.
+//
+// Operands are staged by TMA in 128-byte swizzled sub-tiles of 64 of the reduction, read by the MMA
+// in either order: rows with the reduction contiguous (K-major) or with the lane or column index
+// contiguous (MN-major: boxes of 64 lanes x 64 of the reduction). Pairs (cta_group::2): the leader's
+// MMA spans both SMs' tiles, 256 lanes, and each CTA stages half of the columns, which halves
+// the shared-memory and L2 traffic of the column operand.
+//
+// Warp roles: warp 0 issues the TMA loads (its lanes issue the boxes of a stage in parallel), warp 1
+// owns tensor memory and issues the MMAs (the leader's, in a pair), warps 4-7 run the epilogue of one
+// tile while the next one's main loop fills the other accumulator. Where an operand's address or row
+// distance is not a multiple of 16 bytes, eight loader warps (8-15) read it with ordinary loads and
+// write the same swizzled layout.
+//
+// Every wait is bounded (tc::mbar_wait). On a timeout the CTA raises error bit 2, waits for its copies
+// and MMAs in flight, frees its tensor memory and returns.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "mm16.cuh"
+#include "tc_ptx.cuh"
+
+namespace ds4 {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128, BK = 64;          // lanes per CTA; reduction of one stage
+constexpr int A_BYTES = BM * BK * 2;      // 16 KB
+constexpr int kMaxStages = 12;
+constexpr int kMaxGroups = 1024;
+constexpr int kPanel = 8;                 // column tiles that a raster panel spans
+constexpr int kLoaders = 8;               // loader warps of the unaligned form
+constexpr int kSmemMax = 232448;
+
+struct TcArgs {
+  MmProblem p;
+  int bn, stages, b_box;  // column tile, pipeline depth, rows of a column-operand box
+  int lane_tiles;         // of BM * CG lanes
+};
+
+__host__ __device__ constexpr int ctrl_bytes() { return 16 * kMaxStages + 32 + 16 + 4 * (kMaxGroups + 1) + 12; }
+
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Shared-memory descriptor of a 128-byte swizzled operand. K-major: 8-row atoms of 1024 bytes along
+// the rows (stride offset). MN-major: atoms of 64 lanes x 8 of the reduction; the next 8 of the
+// reduction 1024 bytes on (stride offset), the next 64 lanes one 64 x 64 box on (leading offset).
+__device__ __forceinline__ uint64_t op_desc(uint32_t addr, bool red_major) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(red_major ? 1 : 8192 >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// The MMAs of one stage: ks steps of 16 of the reduction, by one elected lane of the converged warp.
+template <int CG>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step, uint64_t b_step,
+                                          uint32_t idesc, uint32_t accumulate, int ks) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < ks) {
+      if (CG == 2)
+        asm volatile(
+            "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate | i)
+            : "memory");
+      else
+        asm volatile(
+            "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(accumulate | i)
+            : "memory");
+    }
+    a += a_step, b += b_step;
+  }
+}
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {  // in a pair: to both CTAs' barriers
+  if (CG == 2)
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::
+            "r"(su32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    tc_commit_elect(bar);
+}
+template <int CG>
+__device__ __forceinline__ void tmem_get(uint32_t* slot, uint32_t cols) {
+  if (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(su32(slot)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  } else {
+    tmem_alloc(slot, cols);
+    tmem_relinquish();
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  if (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(addr), "r"(cols) : "memory");
+  else
+    tmem_dealloc(addr, cols);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// One output tile.
+struct Tile {
+  int g, l0, c0, n, r0, red;  // group, first lane of the CTA (pair), first column, columns, first of the reduction, its length
+};
+
+// pref: running count of the groups' column tiles, [groups + 1] in shared memory.
+template <int CG>
+__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* pref, int t) {
+  const MmProblem& p = a.p;
+  Tile o;
+  int col_tiles, c_lo = 0, c_n = p.cols;
+  o.g = 0, o.r0 = 0, o.red = p.red;
+  if (p.rag == MM_RAG_COLS) {
+    const int ct = t / a.lane_tiles;  // groups take lane_tiles * their column tiles consecutive tiles
+    int lo = 0, hi = p.groups;
+    while (hi - lo > 1) {  // the last group whose running count is at most ct
+      const int mid = (lo + hi) >> 1;
+      if (pref[mid] <= ct) lo = mid; else hi = mid;
+    }
+    o.g = lo;
+    col_tiles = pref[lo + 1] - pref[lo];
+    t -= pref[lo] * a.lane_tiles;
+    const int2 r = mm_range(p.offsets, lo, p.cols);
+    c_lo = r.x, c_n = r.y - r.x;
+  } else {
+    col_tiles = (p.cols + a.bn - 1) / a.bn;
+    if (p.rag == MM_RAG_RED) {
+      o.g = t / (a.lane_tiles * col_tiles);
+      t -= o.g * a.lane_tiles * col_tiles;
+      const int2 r = mm_range(p.offsets, o.g, p.red);
+      o.r0 = r.x, o.red = r.y - r.x;
+    }
+  }
+  const int panel = t / (a.lane_tiles * kPanel);
+  t -= panel * a.lane_tiles * kPanel;
+  const int w = min(kPanel, col_tiles - panel * kPanel);
+  const int lt = t / w, ct = panel * kPanel + t % w;
+  o.l0 = lt * BM * CG;
+  o.c0 = c_lo + ct * a.bn;
+  o.n = min(a.bn, c_n - ct * a.bn);
+  return o;
+}
+
+// Columns of the tile's MMA: its columns rounded up to the granule (16, in a pair 32); whole 64-column
+// boxes where the columns are the contiguous index.
+template <int CG>
+__device__ __forceinline__ int mma_n(const MmProblem& p, int n) {
+  const int q = p.b.red_major ? 16 * CG : 64 * CG;
+  return (n + q - 1) / q * q;
+}
+
+// Eight consecutive elements of a row as one 16-byte chunk, zeros past `valid`; any alignment.
+__device__ __forceinline__ uint4 gather8(const uint16_t* src, int valid) {
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = i < valid ? (uint32_t)__ldg(src + i) : 0u;
+  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+}
+// One operand's stage by ordinary loads: `boxes` boxes of `rows` rows x 64 elements, in the layout that
+// the TMA's 128-byte swizzle gives (chunk index XOR row mod 8). K-major: box rows are lanes or columns
+// from mn0 and elements the reduction from r0; MN-major the other way round.
+__device__ __forceinline__ void load_stage(uint8_t* dst, const uint16_t* base, int64_t ld, bool red_major, int mn0,
+                                           int mn_end, int r0, int r_end, int mn_count, int tid) {
+  const int chunks = red_major ? mn_count * 8 : mn_count / 64 * 512;
+  for (int i = tid; i < chunks; i += kLoaders * 32) {
+    const int row = i >> 3, ch = i & 7;  // row of 128 bytes in the stage, 16-byte chunk in it
+    int64_t at;
+    int valid;
+    if (red_major) {
+      valid = mn0 + row < mn_end ? min(8, max(0, r_end - (r0 + ch * 8))) : 0;
+      at = (int64_t)(mn0 + row) * ld + r0 + ch * 8;
+    } else {
+      const int mn = mn0 + (row >> 6) * 64 + ch * 8, r = r0 + (row & 63);
+      valid = r < r_end ? min(8, max(0, mn_end - mn)) : 0;
+      at = (int64_t)r * ld + mn;
+    }
+    const uint4 v = valid > 0 ? gather8(base + at, valid) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
+  }
+}
+
+// ------------------------------------------------------------------------------------ epilogues
+
+// 32 elements of one lane, nv of them there, `ld` apart: the type is chosen once for all of them.
+__device__ __forceinline__ void store16(void* base, int64_t at, int64_t ld, int nv, const float (&v)[32], int f16) {
+  uint16_t* q = static_cast<uint16_t*>(base) + at;
+  uint16_t h[32];
+  if (f16) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) h[j] = __half_as_ushort(__float2half_rn(v[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) h[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < nv) q[j * ld] = h[j];
+}
+__device__ __forceinline__ void add16(float (&v)[32], const void* base, int64_t at, int64_t ld, int nv, int f16) {
+  const uint16_t* q = static_cast<const uint16_t*>(base) + at;
+  uint16_t h[32];
+#pragma unroll
+  for (int j = 0; j < 32; ++j) h[j] = j < nv ? q[j * ld] : (uint16_t)0;
+  if (f16) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += __half2float(__ushort_as_half(h[j]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += __uint_as_float((uint32_t)h[j] << 16);
+  }
+}
+
+// 32 columns (of which nv exist) of one lane.
+__device__ __forceinline__ void epi_store(const MmProblem& p, int64_t out_base, int l, int c, int nv, float (&v)[32]) {
+  const MmEpiArgs& e = p.e;
+  if (e.acc_in) {
+    const float* q = e.acc_in + (int64_t)c * e.acc_ld + l;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < nv) v[j] += q[j * e.acc_ld];
+  }
+  if (e.scale) {
+    const float s = __ldg(e.scale);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= s;
+  }
+  if (e.bias) {
+    const float b = ld16(e.bias, l, p.f16);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] += b;
+  }
+  if (e.z) store16(e.z, (int64_t)c * e.ldz + l, e.ldz, nv, v, p.f16);
+  if (e.act != MM_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], e.act);
+  }
+  if (e.residual) add16(v, e.residual, (int64_t)c * e.ldr + l, e.ldr, nv, p.f16);
+  const int64_t o = out_base + (int64_t)c * e.ld + l;
+  if (e.out_f32) {
+    float* q = static_cast<float*>(e.out) + o;
+    if (e.accumulate) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < nv) v[j] += q[j * e.ld];
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j < nv) q[j * e.ld] = v[j];
+  } else {
+    if (e.accumulate) add16(v, e.out, o, e.ld, nv, p.f16);
+    store16(e.out, o, e.ld, nv, v, p.f16);
+  }
+}
+
+// Running maximum m and sum s of exp(z - m) of one token over 32 words (nv exist).
+__device__ __forceinline__ void epi_stats(float (&v)[32], int nv, float& m, float& s) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < nv) top = fmaxf(top, v[j]);
+  if (top == -INFINITY) {  // only words of probability zero so far (NaN logits still reach the sum)
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) bad |= j < nv && v[j] != v[j];
+    if (bad) s = NAN;
+    return;
+  }
+  s *= __expf(m - top);
+  float t = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < nv) t += __expf(v[j] - top);
+  s += t;
+  m = top;
+}
+
+template <int CG, int EPI, bool GEN>
+__global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
+    mm_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                 const __grid_constant__ TcArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const MmProblem& p = a.p;
+  // the stages start on a 1024-byte boundary (the swizzle's period); in a pair both CTAs have the same layout
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const int stage_bytes = A_BYTES + a.bn / CG * BK * 2;
+  uint8_t* ctrl = smem + a.stages * stage_bytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* acc_full = empty + kMaxStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* pref = reinterpret_cast<int*>(tmem_slot + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
+  const int acc_stride = max(a.bn, 32);
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < 2u * acc_stride) tmem_cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < a.stages; ++i) {
+      mbar_init(full + i, GEN ? kLoaders : 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(acc_full + i, 1);
+      mbar_init(acc_empty + i, 4 * CG);
+    }
+    *abort_flag = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_get<CG>(tmem_slot, tmem_cols);
+  if (warp == 0 && lane == 0 && !GEN) {
+    tmap_prefetch(&ta);
+    tmap_prefetch(&tb);
+  }
+  if (p.rag == MM_RAG_COLS && warp == 2) {  // running count of the groups' column tiles
+    int run = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int g = g0 + lane;
+      int n = 0;
+      if (g < p.groups) {
+        const int2 r = mm_range(p.offsets, g, p.cols);
+        n = (r.y - r.x + a.bn - 1) / a.bn;
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (g < p.groups) pref[g] = run + inc - n;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) pref[p.groups] = run;
+  }
+  tc_fence_before();
+  if (CG == 2) cluster_sync();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int col_tiles = p.rag == MM_RAG_COLS ? pref[p.groups] : (p.cols + a.bn - 1) / a.bn;
+  const int tiles = a.lane_tiles * col_tiles * (p.rag == MM_RAG_RED ? p.groups : 1);
+  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+  if (warp == 0 && !GEN) {
+    // ------------------------------------------------------------------ TMA producer
+    const bool a_red = p.a.red_major, b_red = p.b.red_major;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int a_boxes = a_red ? 1 : 2;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile o = tile_of<CG>(a, pref, t);
+      const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
+      const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : nb / 64;
+      const int b_box_bytes = b_red ? a.b_box * 128 : 8192;
+      const uint32_t bytes = CG * (A_BYTES + b_boxes * b_box_bytes);
+      const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
+      const int ga = p.rag == MM_RAG_COLS ? o.g : 0;
+      for (int k = 0; k < o.red; k += BK) {
+        if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * stage_bytes;
+        if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);
+        __syncwarp();
+        const uint32_t bar = CG == 2 ? mapa(su32(full + s), 0) : su32(full + s);
+        const int r = o.r0 + k;
+        if (lane < a_boxes) {
+          if (a_red)
+            tma_load_3d<CG>(su32(st), &ta, r, la, ga, bar);
+          else
+            tma_load_3d<CG>(su32(st + lane * 8192), &ta, la + 64 * lane, r, ga, bar);
+        } else if (lane >= 4 && lane < 4 + b_boxes) {
+          const int i = lane - 4;
+          if (b_red)
+            tma_load_3d<CG>(su32(st + A_BYTES + i * b_box_bytes), &tb, r, cb + i * a.b_box, 0, bar);
+          else
+            tma_load_3d<CG>(su32(st + A_BYTES + i * 8192), &tb, cb + 64 * i, r, 0, bar);
+        }
+        __syncwarp();
+        if (++s == a.stages) s = 0, ph ^= 1;
+      }
+    }
+  } else if (GEN && warp >= 8) {
+    // ------------------------------------------------------------------ loaders (any alignment)
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const int tid = threadIdx.x - 256;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile o = tile_of<CG>(a, pref, t);
+      const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
+      const uint16_t* pb = static_cast<const uint16_t*>(p.b.p);
+      const int nb = mma_n<CG>(p, o.n);
+      for (int k = 0; k < o.red; k += BK) {
+        if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * stage_bytes;
+        load_stage(st, pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0 + k, o.r0 + o.red, BM, tid);
+        load_stage(st + A_BYTES, pb, p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0 + k, o.r0 + o.red, nb, tid);
+        asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + s);
+        if (++s == a.stages) s = 0, ph ^= 1;
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------------ MMA
+    int s = 0, local = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    const uint64_t a_step = (p.a.red_major ? 32 : 2048) >> 4, b_step = (p.b.red_major ? 32 : 2048) >> 4;
+    const uint32_t type = p.f16 ? 0u : 1u;
+    for (int t = first; t < tiles && ok; t += step) {
+      const Tile o = tile_of<CG>(a, pref, t);
+      if (o.red <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
+      const int buf = local & 1, n = mma_n<CG>(p, o.n);
+      const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
+                             (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
+      if (!mbar_wait(acc_empty + buf, ((local >> 1) & 1) ^ 1, abort_flag, p.err, 6)) break;
+      tc_fence_after();
+      const uint32_t d = tmem + (uint32_t)(buf * acc_stride);
+      for (int k = 0; k < o.red; k += BK) {
+        if (!mbar_wait(full + s, ph, abort_flag, p.err, 7)) {
+          ok = false;
+          break;
+        }
+        uint8_t* st = smem + s * stage_bytes;
+        const int left = min(BK, o.red - k);
+        if (p.rag == MM_RAG_RED && !GEN && (left & 15)) {
+          // The group ends inside this step of 16: the rows of the next group that the boxes also
+          // brought are cleared in both operands (0 * NaN would not vanish). A row is 128 bytes of a box.
+          const int boxes = 2 + n / 64, rows = 16 - (left & 15);
+          for (int i = lane; i < boxes * rows * 8; i += 32) {
+            const int ch = i & 7, row = left + (i >> 3) % rows, box = (i >> 3) / rows;
+            *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+        }
+        __syncwarp();
+        tc_fence_after();
+        mma_stage<CG>(d, op_desc(su32(st), p.a.red_major), op_desc(su32(st + A_BYTES), p.b.red_major), a_step, b_step,
+                      idesc, k ? 1u : 0u, (left + 15) >> 4);
+        commit<CG>(empty + s);
+        if (++s == a.stages) s = 0, ph ^= 1;
+      }
+      if (!ok) break;
+      commit<CG>(acc_full + buf);
+      ++local;
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    int local = 0;
+    for (int t = first; t < tiles; t += step) {
+      const Tile o = tile_of<CG>(a, pref, t);
+      const int l = o.l0 + BM * rank + 32 * quad + lane;
+      const bool live = l < p.lanes;
+      const bool sum = o.red > 0;
+      const int buf = local & 1;
+      if (sum) {
+        if (!mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5)) break;
+        __syncwarp();
+        tc_fence_after();
+        ++local;
+      }
+      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      const int64_t out_base = p.rag == MM_RAG_RED ? o.g * p.e.group_stride : 0;
+      float m = -INFINITY, total = 0.f, lse = 0.f, gw = 0.f;
+      int lab = -1;
+      if (EPI != MM_EPI_STORE && live) {
+        lab = __ldg(p.e.labels + l);
+        if (EPI == MM_EPI_SOFTGRAD) {
+          const bool skip = lab == p.e.ignore || lab < 0 || lab >= p.e.vocab;
+          lse = __ldg(p.e.lse + l);
+          gw = skip ? 0.f : __ldg(p.e.g + l) / __ldg(p.e.gscale) * kMmGradOne;
+          if (skip) lab = -1;
+        }
+      }
+      for (int c = 0; c < o.n; c += 32) {
+        float v[32];
+        if (sum) {
+          tmem_ld32(taddr + c, v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        const int nv = o.n - c;
+        if (!live) continue;
+        if (EPI == MM_EPI_STORE) {
+          epi_store(p, out_base, l, o.c0 + c, nv, v);
+        } else if (EPI == MM_EPI_STATS) {
+          epi_stats(v, nv, m, total);
+          const int at = lab - (o.c0 + c);
+          if (at >= 0 && at < min(nv, 32)) {
+            float z = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == at) z = v[j];
+            p.e.zlab[l] = z;
+          }
+        } else {
+          // (a row without gradient stays zero even where its logits are not finite)
+          const int at = lab >= 0 ? lab - p.e.word0 - (o.c0 + c) : -1;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = gw == 0.f ? 0.f : (__expf(v[j] - lse) - (j == at ? 1.f : 0.f)) * gw;
+          store16(p.e.out, (int64_t)(o.c0 + c) * p.e.ld + l, p.e.ld, nv, v, p.f16);
+        }
+      }
+      if (EPI == MM_EPI_STATS && live) p.e.part[(int64_t)(o.c0 / a.bn) * p.lanes + l] = make_float2(m, total);
+      if (sum) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {  // the MMA may overwrite this buffer
+          if (CG == 2)
+            mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
+          else
+            mbar_arrive(acc_empty + buf);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (*abort_flag) {  // after a timeout: let the copies and MMAs in flight finish (about a millisecond)
+    const long long t0 = clock64();
+    while (clock64() - t0 < 2000000ll) {
+    }
+  }
+  tc_fence_before();
+  if (CG == 2)
+    cluster_sync();  // no copy, MMA or commit still targets the other CTA
+  else
+    __syncthreads();
+  if (warp == 1) tmem_free<CG>(tmem, tmem_cols);
+}
+
+// ------------------------------------------------------------------------------------ host
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be resident at once
+
+// 3D map (contiguous index, row, group) with boxes of 64 elements x box_rows rows, 128-byte swizzle.
+bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows) {
+  const cuuint64_t dims[3] = {inner, rows, groups};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, groups > 1 ? (cuuint64_t)o.group_stride * 2 : (cuuint64_t)o.ld * 2};
+  const cuuint32_t box[3] = {BK, box_rows, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tma_ready(const MmOperand& o) {
+  return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 38 && o.group_stride < (int64_t)1 << 38;
+}
+
+int smem_bytes(int cg, int bn, int stages) { return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + ctrl_bytes(); }
+
+template <int CG, int EPI, bool GEN>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a, int grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(GEN ? 256 + 32 * kLoaders : 256);
+  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CG > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mm_tc_kernel<CG, EPI, GEN>, ta, tb, a);
+}
+
+template <int CG, bool GEN>
+cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a, int grid, cudaStream_t s) {
+  switch (a.p.epi) {
+    case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_SOFTGRAD: return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
+    default: return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
+  }
+}
+
+template <int CG, int EPI, bool GEN>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(mm_tc_kernel<CG, EPI, GEN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+}
+template <int CG, bool GEN>
+cudaError_t prepare_epi() {
+  cudaError_t e = prepare_one<CG, MM_EPI_STORE, GEN>();
+  if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_STATS, GEN>();
+  if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_SOFTGRAD, GEN>();
+  return e;
+}
+
+}  // namespace
+
+cudaError_t mm_prepare() {
+  if (!g_encode) {
+    cudaDriverEntryPointQueryResult q;
+    void* fn = nullptr;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    if (e != cudaSuccess) return e;
+    if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&g_sms[dev & 63], cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = prepare_epi<1, false>();
+  if (e == cudaSuccess) e = prepare_epi<2, false>();
+  if (e == cudaSuccess) e = prepare_epi<1, true>();
+  if (e == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&g_pairs[dev & 63], mm_tc_kernel<2, MM_EPI_STORE, false>, &cfg);
+  }
+  return e;
+}
+
+cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
+  if (p.lanes <= 0 || p.cols <= 0) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int sms = g_sms[dev & 63], pairs = g_pairs[dev & 63];
+  TcArgs a = {};
+  a.p = p;
+  const bool gen = p.red <= 0 || !tma_ready(p.a) || !tma_ready(p.b);
+  // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
+  // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
+  const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 ? 2 : 1;
+  a.bn = 256;
+  if (p.epi != MM_EPI_STATS) {
+    const int64_t typical = p.rag == MM_RAG_COLS ? 2 * (((int64_t)p.cols + p.groups - 1) / p.groups) : p.cols;
+    while (a.bn > 64 * cg && a.bn / 2 >= std::min<int64_t>(typical, p.cols)) a.bn /= 2;
+  }
+  a.stages = 1;
+  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1) <= kSmemMax) ++a.stages;
+  a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
+  a.b_box = p.rag == MM_RAG_COLS ? 32 : std::min(128, a.bn / cg);
+  const int64_t col_tiles = p.rag == MM_RAG_COLS ? (p.cols + a.bn - 1) / a.bn + p.groups : (p.cols + a.bn - 1) / a.bn;
+  const int64_t tiles = a.lane_tiles * col_tiles * (p.rag == MM_RAG_RED ? p.groups : 1);
+  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  CUtensorMap ta = {}, tb = {};
+  if (!gen) {
+    const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
+    const uint64_t red = p.red;
+    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? p.lanes : red, groups, p.a.red_major ? BM : BK) &&
+                    make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK);
+    if (!ok) return cudaErrorInvalidValue;
+  }
+  const int grid = cg * (int)std::max<int64_t>(1, std::min<int64_t>(cg == 2 ? pairs : sms, tiles));
+  if (gen) return launch_epi<1, true>(ta, tb, a, grid, s);
+  return cg == 2 ? launch_epi<2, false>(ta, tb, a, grid, s) : launch_epi<1, false>(ta, tb, a, grid, s);
+}
+
+}  // namespace ds4
