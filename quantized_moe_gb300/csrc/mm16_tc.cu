@@ -35,18 +35,36 @@ using namespace tc;
 constexpr int BM = 128, BK = 64;          // lanes per CTA; reduction of one stage
 constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
-constexpr int kMaxGroups = 1024;
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
+constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
+constexpr int kFirstLoader = 4 + kEpiWarps;
 constexpr int kLoaders = 8;               // loader warps of the unaligned form
+constexpr int kThreads = 32 * kFirstLoader;
 constexpr int kSmemMax = 232448;
+
+// n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d).
+struct Divider {
+  uint32_t m, l;
+  Divider() = default;
+  explicit Divider(uint32_t d) : l(0) {
+    while (l < 31 && (1u << l) < d) ++l;
+    m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int div(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> l); }
+};
 
 struct TcArgs {
   MmProblem p;
-  int bn, stages, b_box;  // column tile, pipeline depth, rows of a column-operand box
-  int lane_tiles;         // of BM * CG lanes
+  int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
+  int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
+  int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
+  Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
 };
 
-__host__ __device__ constexpr int ctrl_bytes() { return 16 * kMaxStages + 32 + 16 + 4 * (kMaxGroups + 1) + 12; }
+// Barriers, the tensor-memory address and the abort flag, then the group tables (tile_of).
+__host__ __device__ constexpr int ctrl_bytes(int rag, int groups) {
+  return 24 * kMaxStages + 32 + 16 + (rag == MM_DENSE ? 8 * BM : 4 * (groups + 1) * (rag == MM_RAG_COLS ? 2 : 1));
+}
 
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -81,40 +99,32 @@ __device__ __forceinline__ uint64_t op_desc(uint32_t addr, bool red_major) {
          (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// The MMAs of one stage: ks steps of 16 of the reduction, by one elected lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e != 0;
+}
+// One MMA of 16 of the reduction, and the arrival on a barrier (in a pair: on both CTAs' barriers) once all
+// MMAs issued before are complete. One thread of the CTA issues all of them.
 template <int CG>
-__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step, uint64_t b_step,
-                                          uint32_t idesc, uint32_t accumulate, int ks) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i < ks) {
-      if (CG == 2)
-        asm volatile(
-            "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-            " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate | i)
-            : "memory");
-      else
-        asm volatile(
-            "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-            " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(accumulate | i)
-            : "memory");
-    }
-    a += a_step, b += b_step;
-  }
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if (CG == 2)
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
+  else
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+                 : "memory");
 }
 template <int CG>
-__device__ __forceinline__ void commit(uint64_t* bar) {  // in a pair: to both CTAs' barriers
+__device__ __forceinline__ void commit(uint64_t* bar) {
   if (CG == 2)
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::
-            "r"(su32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(su32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
   else
-    tc_commit_elect(bar);
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(su32(bar)) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tmem_get(uint32_t* slot, uint32_t cols) {
@@ -154,15 +164,17 @@ struct Tile {
   int g, l0, c0, n, r0, red;  // group, first lane of the CTA (pair), first column, columns, first of the reduction, its length
 };
 
-// pref: running count of the groups' column tiles, [groups + 1] in shared memory.
+// Tables in shared memory: lo[g], g = 0..groups, the first row of each group, clamped to the matrix (a group
+// ends where the next one begins, or is empty if that lies before it); for ragged columns pref[g], the running
+// count of the groups' column tiles.
 template <int CG>
-__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* pref, int t) {
+__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int t) {
   const MmProblem& p = a.p;
   Tile o;
-  int col_tiles, c_lo = 0, c_n = p.cols;
+  int col_tiles = a.col_tiles, c_lo = 0, c_n = p.cols, part = 0, width = a.bn;
   o.g = 0, o.r0 = 0, o.red = p.red;
   if (p.rag == MM_RAG_COLS) {
-    const int ct = t / a.lane_tiles;  // groups take lane_tiles * their column tiles consecutive tiles
+    const int ct = a.by_lanes.div(t);  // a group takes lane_tiles * its column tiles consecutive tiles
     int lo = 0, hi = p.groups;
     while (hi - lo > 1) {  // the last group whose running count is at most ct
       const int mid = (lo + hi) >> 1;
@@ -171,24 +183,27 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* pref, int t)
     o.g = lo;
     col_tiles = pref[lo + 1] - pref[lo];
     t -= pref[lo] * a.lane_tiles;
-    const int2 r = mm_range(p.offsets, lo, p.cols);
-    c_lo = r.x, c_n = r.y - r.x;
-  } else {
-    col_tiles = (p.cols + a.bn - 1) / a.bn;
-    if (p.rag == MM_RAG_RED) {
-      o.g = t / (a.lane_tiles * col_tiles);
-      t -= o.g * a.lane_tiles * col_tiles;
-      const int2 r = mm_range(p.offsets, o.g, p.red);
-      o.r0 = r.x, o.red = r.y - r.x;
-    }
+    c_lo = lo_of[lo], c_n = max(lo_of[lo + 1] - c_lo, 0);
+  } else if (p.rag == MM_RAG_RED) {
+    o.g = a.by_matrix.div(t);
+    t -= o.g * a.lane_tiles * col_tiles;
+    o.r0 = lo_of[o.g], o.red = max(lo_of[o.g + 1] - o.r0, 0);
+  } else if (t >= a.tail_from) {
+    const int u = t - a.tail_from;
+    part = u & ((1 << a.tail_lg) - 1);
+    width = a.bn >> a.tail_lg;
+    t = a.tail_from + (u >> a.tail_lg);
   }
-  const int panel = t / (a.lane_tiles * kPanel);
-  t -= panel * a.lane_tiles * kPanel;
+  int panel = 0;
+  if (col_tiles > kPanel) {
+    panel = a.by_panel.div(t);
+    t -= panel * a.lane_tiles * kPanel;
+  }
   const int w = min(kPanel, col_tiles - panel * kPanel);
-  const int lt = t / w, ct = panel * kPanel + t % w;
+  const int lt = w == 1 ? t : w == kPanel ? t / kPanel : t / w, ct = panel * kPanel + t - lt * w;
   o.l0 = lt * BM * CG;
-  o.c0 = c_lo + ct * a.bn;
-  o.n = min(a.bn, c_n - ct * a.bn);
+  o.c0 = c_lo + ct * a.bn + part * width;
+  o.n = min(width, c_n - ct * a.bn - part * width);  // (a part past the last column has none)
   return o;
 }
 
@@ -233,25 +248,44 @@ __device__ __forceinline__ void load_stage(uint8_t* dst, const uint16_t* base, i
 // ------------------------------------------------------------------------------------ epilogues
 
 // 32 elements of one lane, nv of them there, `ld` apart: the type is chosen once for all of them.
-__device__ __forceinline__ void store16(void* base, int64_t at, int64_t ld, int nv, const float (&v)[32], int f16) {
-  uint16_t* q = static_cast<uint16_t*>(base) + at;
-  uint16_t h[32];
-  if (f16) {
+__device__ __forceinline__ void to16(const float (&v)[32], uint16_t (&h)[32], int f16) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) h[j] = __half_as_ushort(__float2half_rn(v[j]));
+  for (int j = 0; j < 32; j += 2) {
+    uint32_t u;
+    if (f16) {
+      const __half2 t = __floats2half2_rn(v[j], v[j + 1]);
+      u = *reinterpret_cast<const uint32_t*>(&t);
+    } else {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[j], v[j + 1]);
+      u = *reinterpret_cast<const uint32_t*>(&t);
+    }
+    h[j] = (uint16_t)u, h[j + 1] = (uint16_t)(u >> 16);
+  }
+}
+template <class T>
+__device__ __forceinline__ void store_col(T* q, int64_t ld, int nv, const T (&h)[32]) {
+  if (nv >= 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j, q += ld) *q = h[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) h[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+    for (int j = 0; j < 32; ++j, q += ld)
+      if (j < nv) *q = h[j];
   }
+}
+template <class T>
+__device__ __forceinline__ void load_col(const T* q, int64_t ld, int nv, T (&h)[32]) {
+  if (nv >= 32) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < nv) q[j * ld] = h[j];
+    for (int j = 0; j < 32; ++j, q += ld) h[j] = *q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j, q += ld) h[j] = j < nv ? *q : T(0);
+  }
 }
 __device__ __forceinline__ void add16(float (&v)[32], const void* base, int64_t at, int64_t ld, int nv, int f16) {
-  const uint16_t* q = static_cast<const uint16_t*>(base) + at;
   uint16_t h[32];
-#pragma unroll
-  for (int j = 0; j < 32; ++j) h[j] = j < nv ? q[j * ld] : (uint16_t)0;
+  load_col(static_cast<const uint16_t*>(base) + at, ld, nv, h);
   if (f16) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] += __half2float(__ushort_as_half(h[j]));
@@ -260,46 +294,67 @@ __device__ __forceinline__ void add16(float (&v)[32], const void* base, int64_t 
     for (int j = 0; j < 32; ++j) v[j] += __uint_as_float((uint32_t)h[j] << 16);
   }
 }
-
-// 32 columns (of which nv exist) of one lane.
-__device__ __forceinline__ void epi_store(const MmProblem& p, int64_t out_base, int l, int c, int nv, float (&v)[32]) {
-  const MmEpiArgs& e = p.e;
-  if (e.acc_in) {
-    const float* q = e.acc_in + (int64_t)c * e.acc_ld + l;
+__device__ __forceinline__ void add32(float (&v)[32], const float* q, int64_t ld, int nv) {
+  float h[32];
+  load_col(q, ld, nv, h);
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < nv) v[j] += q[j * e.acc_ld];
+  for (int j = 0; j < 32; ++j) v[j] += h[j];
+}
+
+// silu with the hardware exponential and division: a few units of 2^-22, and 0 instead of a value below 2^-118.
+__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+
+// Writes 32 columns (nv exist for this lane) of lane l.
+__device__ __forceinline__ void put(const MmProblem& p, int g, int l, int c, int nv, const float (&v)[32]) {
+  const MmEpiArgs& e = p.e;
+  if (l >= p.lanes) return;
+  const int64_t o = (p.rag == MM_RAG_RED ? g * e.group_stride : 0) + (int64_t)c * e.ld + l;
+  if (e.out_f32) {
+    store_col(static_cast<float*>(e.out) + o, e.ld, nv, v);
+  } else {
+    uint16_t h[32];
+    to16(v, h, p.f16);
+    store_col(static_cast<uint16_t*>(e.out) + o, e.ld, nv, h);
   }
+}
+
+// The arithmetic of a stored result: 32 columns (nv exist for this lane) of lane l.
+__device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int c, int nv, float (&v)[32]) {
+  const MmEpiArgs& e = p.e;
+  if (l >= p.lanes) nv = 0;
+  if (e.acc_in) add32(v, e.acc_in + (int64_t)c * e.acc_ld + l, e.acc_ld, nv);
   if (e.scale) {
     const float s = __ldg(e.scale);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= s;
   }
   if (e.bias) {
-    const float b = ld16(e.bias, l, p.f16);
+    const float b = nv ? ld16(e.bias, l, p.f16) : 0.f;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] += b;
   }
-  if (e.z) store16(e.z, (int64_t)c * e.ldz + l, e.ldz, nv, v, p.f16);
-  if (e.act != MM_ACT_NONE) {
+  if (e.z) {
+    uint16_t h[32];
+    to16(v, h, p.f16);
+    store_col(static_cast<uint16_t*>(e.z) + (int64_t)c * e.ldz + l, e.ldz, nv, h);
+  }
+  if (e.act == MM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], e.act);
+    for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
+  } else if (e.act == MM_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], MM_ACT_GELU);
+  } else if (e.act == MM_ACT_RELU) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], MM_ACT_RELU);
   }
   if (e.residual) add16(v, e.residual, (int64_t)c * e.ldr + l, e.ldr, nv, p.f16);
-  const int64_t o = out_base + (int64_t)c * e.ld + l;
-  if (e.out_f32) {
-    float* q = static_cast<float*>(e.out) + o;
-    if (e.accumulate) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < nv) v[j] += q[j * e.ld];
-    }
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < nv) q[j * e.ld] = v[j];
-  } else {
-    if (e.accumulate) add16(v, e.out, o, e.ld, nv, p.f16);
-    store16(e.out, o, e.ld, nv, v, p.f16);
+  if (e.accumulate) {
+    const int64_t o = (p.rag == MM_RAG_RED ? g * e.group_stride : 0) + (int64_t)c * e.ld + l;
+    if (e.out_f32)
+      add32(v, static_cast<const float*>(e.out) + o, e.ld, nv);
+    else
+      add16(v, e.out, o, e.ld, nv, p.f16);
   }
 }
 
@@ -326,7 +381,7 @@ __device__ __forceinline__ void epi_stats(float (&v)[32], int nv, float& m, floa
 }
 
 template <int CG, int EPI, bool GEN>
-__global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
+__global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     mm_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
                  const __grid_constant__ TcArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -339,9 +394,12 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
   uint64_t* acc_empty = acc_full + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* clean = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + kMaxStages);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  int* pref = reinterpret_cast<int*>(tmem_slot + 4);
+  float2* exchange = reinterpret_cast<float2*>(tmem_slot + 4);  // [BM], softmax partials only
+  int* lo_of = reinterpret_cast<int*>(tmem_slot + 4);
+  int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
   const int acc_stride = max(a.bn, 32);
@@ -351,11 +409,12 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(full + i, GEN ? kLoaders : 1);
-      mbar_init(empty + i, 1);
+      mbar_init(empty + i, !GEN && p.rag == MM_RAG_RED ? 2 : 1);  // the MMAs' commit, and the cleaner
+      mbar_init(clean + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4 * CG);
+      mbar_init(acc_empty + i, kEpiWarps * CG);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -365,14 +424,16 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
     tmap_prefetch(&ta);
     tmap_prefetch(&tb);
   }
-  if (p.rag == MM_RAG_COLS && warp == 2) {  // running count of the groups' column tiles
+  if (p.rag != MM_DENSE && warp == 2) {
+    const int total = p.rag == MM_RAG_COLS ? p.cols : p.red;
     int run = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+    for (int g0 = 0; g0 <= p.groups; g0 += 32) {
       const int g = g0 + lane;
       int n = 0;
-      if (g < p.groups) {
-        const int2 r = mm_range(p.offsets, g, p.cols);
-        n = (r.y - r.x + a.bn - 1) / a.bn;
+      if (g <= p.groups) {
+        const int lo = min(max(__ldg(p.offsets + g), 0), total);
+        lo_of[g] = lo;
+        if (g < p.groups) n = (max(min(__ldg(p.offsets + g + 1), total) - lo, 0) + a.bn - 1) / a.bn;
       }
       int inc = n;
 #pragma unroll
@@ -380,18 +441,17 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
         const int u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += u;
       }
-      if (g < p.groups) pref[g] = run + inc - n;
+      if (p.rag == MM_RAG_COLS && g <= p.groups) pref[g] = run + inc - n;
       run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    if (lane == 0) pref[p.groups] = run;
   }
   tc_fence_before();
   if (CG == 2) cluster_sync();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int col_tiles = p.rag == MM_RAG_COLS ? pref[p.groups] : (p.cols + a.bn - 1) / a.bn;
-  const int tiles = a.lane_tiles * col_tiles * (p.rag == MM_RAG_RED ? p.groups : 1);
+  int tiles = a.lane_tiles * (p.rag == MM_RAG_COLS ? pref[p.groups] : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
+  if (p.rag == MM_DENSE) tiles += (tiles - a.tail_from) * ((1 << a.tail_lg) - 1);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   if (warp == 0 && !GEN) {
@@ -402,7 +462,8 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
     bool ok = true;
     const int a_boxes = a_red ? 1 : 2;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      if (o.n <= 0) continue;
       const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
       const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : nb / 64;
       const int b_box_bytes = b_red ? a.b_box * 128 : 8192;
@@ -435,14 +496,15 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
         if (++s == a.stages) s = 0, ph ^= 1;
       }
     }
-  } else if (GEN && warp >= 8) {
+  } else if (GEN && warp >= kFirstLoader) {
     // ------------------------------------------------------------------ loaders (any alignment)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int tid = threadIdx.x - 256;
+    const int tid = threadIdx.x - kThreads;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const uint16_t* pb = static_cast<const uint16_t*>(p.b.p);
       const int nb = mma_n<CG>(p, o.n);
@@ -461,32 +523,66 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
       }
     }
   } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------------ MMA
-    int s = 0, local = 0;
+    // ------------------------------------------------------------------ MMA (one thread)
+    if (elect_one()) {
+      int s = 0, local = 0;
+      uint32_t ph = 0, cleaned = 0;
+      bool ok = true;
+      const uint64_t a_step = (p.a.red_major ? 32 : 2048) >> 4, b_step = (p.b.red_major ? 32 : 2048) >> 4;
+      const uint64_t a_desc = op_desc(su32(smem), p.a.red_major), b_desc = op_desc(su32(smem + A_BYTES), p.b.red_major);
+      const uint32_t type = p.f16 ? 0u : 1u;
+      for (int t = first; t < tiles && ok; t += step) {
+        const Tile o = tile_of<CG>(a, lo_of, pref, t);
+        if (o.red <= 0 || o.n <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
+        const int buf = local & 1, n = mma_n<CG>(p, o.n);
+        const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
+                               (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
+        if (!mbar_wait(acc_empty + buf, ((local >> 1) & 1) ^ 1, abort_flag, p.err, 6)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(buf * acc_stride);
+        for (int k = 0; k < o.red; k += BK) {
+          const int left = min(BK, o.red - k);
+          if (!mbar_wait(full + s, ph, abort_flag, p.err, 7) ||
+              (!GEN && p.rag == MM_RAG_RED && (left & 15) && !mbar_wait(clean + s, cleaned >> s & 1, abort_flag, p.err, 2))) {
+            ok = false;
+            break;
+          }
+          if (left & 15) cleaned ^= 1u << s;
+          tc_fence_after();
+          const uint64_t da = a_desc + (uint32_t)(s * stage_bytes >> 4), db = b_desc + (uint32_t)(s * stage_bytes >> 4);
+          if (left > 48) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, k | i);
+          } else {
+            for (int i = 0; 16 * i < left; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, k | i);
+          }
+          commit<CG>(empty + s);
+          if (++s == a.stages) s = 0, ph ^= 1;
+        }
+        if (!ok) break;
+        commit<CG>(acc_full + buf);
+        ++local;
+      }
+    }
+  } else if (warp == 2 && !GEN && p.rag == MM_RAG_RED) {
+    // ------------------------------------------------------------------ cleaner of ragged ends
+    // Where a group ends inside a step of 16, the rows of the next group that the boxes also brought are
+    // cleared in both operands before the MMA reads them (0 * NaN would not vanish). A row is 128 bytes of a box.
+    // The warp passes every stage in turn and arrives on its empty barrier too, so that the ring cannot lap it.
+    int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const uint64_t a_step = (p.a.red_major ? 32 : 2048) >> 4, b_step = (p.b.red_major ? 32 : 2048) >> 4;
-    const uint32_t type = p.f16 ? 0u : 1u;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, pref, t);
-      if (o.red <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
-      const int buf = local & 1, n = mma_n<CG>(p, o.n);
-      const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
-                             (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
-      if (!mbar_wait(acc_empty + buf, ((local >> 1) & 1) ^ 1, abort_flag, p.err, 6)) break;
-      tc_fence_after();
-      const uint32_t d = tmem + (uint32_t)(buf * acc_stride);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t);
       for (int k = 0; k < o.red; k += BK) {
-        if (!mbar_wait(full + s, ph, abort_flag, p.err, 7)) {
+        if (!mbar_wait(full + s, ph, abort_flag, p.err, 2)) {
           ok = false;
           break;
         }
-        uint8_t* st = smem + s * stage_bytes;
         const int left = min(BK, o.red - k);
-        if (p.rag == MM_RAG_RED && !GEN && (left & 15)) {
-          // The group ends inside this step of 16: the rows of the next group that the boxes also
-          // brought are cleared in both operands (0 * NaN would not vanish). A row is 128 bytes of a box.
-          const int boxes = 2 + n / 64, rows = 16 - (left & 15);
+        if (left & 15) {
+          uint8_t* st = smem + s * stage_bytes;
+          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, rows = 16 - (left & 15);
           for (int i = lane; i < boxes * rows * 8; i += 32) {
             const int ch = i & 7, row = left + (i >> 3) % rows, box = (i >> 3) / rows;
             *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
@@ -494,34 +590,26 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         }
         __syncwarp();
-        tc_fence_after();
-        mma_stage<CG>(d, op_desc(su32(st), p.a.red_major), op_desc(su32(st + A_BYTES), p.b.red_major), a_step, b_step,
-                      idesc, k ? 1u : 0u, (left + 15) >> 4);
-        commit<CG>(empty + s);
+        if (lane == 0) {
+          if (left & 15) mbar_arrive(clean + s);
+          mbar_arrive(empty + s);
+        }
         if (++s == a.stages) s = 0, ph ^= 1;
       }
-      if (!ok) break;
-      commit<CG>(acc_full + buf);
-      ++local;
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < kFirstLoader) {
     // ------------------------------------------------------------------ epilogue
-    const int quad = warp & 3;
+    // Two warps per lane quadrant take the tile's 32-column chunks in turn (for the softmax partials each
+    // keeps its own and the pair adds them up through shared memory).
+    const int quad = warp & 3, half = (warp - 4) >> 2;
     int local = 0;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = tile_of<CG>(a, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      if (o.n <= 0) continue;
       const int l = o.l0 + BM * rank + 32 * quad + lane;
       const bool live = l < p.lanes;
       const bool sum = o.red > 0;
       const int buf = local & 1;
-      if (sum) {
-        if (!mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5)) break;
-        __syncwarp();
-        tc_fence_after();
-        ++local;
-      }
-      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
-      const int64_t out_base = p.rag == MM_RAG_RED ? o.g * p.e.group_stride : 0;
       float m = -INFINITY, total = 0.f, lse = 0.f, gw = 0.f;
       int lab = -1;
       if (EPI != MM_EPI_STORE && live) {
@@ -533,7 +621,17 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
           if (skip) lab = -1;
         }
       }
-      for (int c = 0; c < o.n; c += 32) {
+      bool ok = true;
+      if (sum) {
+        ok = mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5);
+        __syncwarp();
+        tc_fence_after();
+        ++local;
+      }
+      // (all warps of the epilogue leave together: the partials' exchange has a barrier)
+      if (!named_bar_all(1, 32 * kEpiWarps, ok)) break;
+      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      for (int c = 32 * half; c < o.n; c += 64) {
         float v[32];
         if (sum) {
           tmem_ld32(taddr + c, v);
@@ -541,14 +639,14 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
-        const int nv = o.n - c;
-        if (!live) continue;
+        const int nv = min(32, o.n - c);
         if (EPI == MM_EPI_STORE) {
-          epi_store(p, out_base, l, o.c0 + c, nv, v);
+          epi_store(p, o.g, l, o.c0 + c, nv, v);
+          put(p, o.g, l, o.c0 + c, nv, v);
         } else if (EPI == MM_EPI_STATS) {
           epi_stats(v, nv, m, total);
           const int at = lab - (o.c0 + c);
-          if (at >= 0 && at < min(nv, 32)) {
+          if (live && at >= 0 && at < nv) {
             float z = 0.f;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -560,10 +658,9 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
           const int at = lab >= 0 ? lab - p.e.word0 - (o.c0 + c) : -1;
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = gw == 0.f ? 0.f : (__expf(v[j] - lse) - (j == at ? 1.f : 0.f)) * gw;
-          store16(p.e.out, (int64_t)(o.c0 + c) * p.e.ld + l, p.e.ld, nv, v, p.f16);
+          put(p, 0, l, o.c0 + c, nv, v);
         }
       }
-      if (EPI == MM_EPI_STATS && live) p.e.part[(int64_t)(o.c0 / a.bn) * p.lanes + l] = make_float2(m, total);
       if (sum) {
         tc_fence_before();
         __syncwarp();
@@ -572,6 +669,18 @@ __global__ void __launch_bounds__(GEN ? 256 + 32 * kLoaders : 256, 1)
             mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
           else
             mbar_arrive(acc_empty + buf);
+        }
+      }
+      if (EPI == MM_EPI_STATS) {
+        float2* x = exchange + 32 * quad + lane;
+        if (half) *x = make_float2(m, total);
+        named_bar(2, 32 * kEpiWarps);
+        if (!half && live) {
+          const float2 q = *x;
+          const float top = fmaxf(m, q.x);
+          // (a half without likely words has m = -inf and adds its sum, 0 or NaN)
+          const float s0 = m == top ? total : total * __expf(m - top), s1 = q.x == top ? q.y : q.y * __expf(q.x - top);
+          p.e.part[(int64_t)(o.c0 / a.bn) * p.lanes + l] = make_float2(top, s0 + s1);
         }
       }
     }
@@ -598,7 +707,7 @@ int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be
 // 3D map (contiguous index, row, group) with boxes of 64 elements x box_rows rows, 128-byte swizzle.
 bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows) {
   const cuuint64_t dims[3] = {inner, rows, groups};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, groups > 1 ? (cuuint64_t)o.group_stride * 2 : (cuuint64_t)o.ld * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)(groups > 1 ? o.group_stride : o.ld) * 2};
   const cuuint32_t box[3] = {BK, box_rows, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p),
@@ -606,18 +715,21 @@ bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint6
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the TMA unit can address a matrix: 16-byte aligned start and row distances.
 bool tma_ready(const MmOperand& o) {
-  return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 38 && o.group_stride < (int64_t)1 << 38;
+  return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 36 && o.group_stride < (int64_t)1 << 36;
 }
 
-int smem_bytes(int cg, int bn, int stages) { return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + ctrl_bytes(); }
+int smem_bytes(int cg, int bn, int stages, const MmProblem& p) {
+  return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + ctrl_bytes(p.rag, p.groups);
+}
 
 template <int CG, int EPI, bool GEN>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(GEN ? 256 + 32 * kLoaders : 256);
-  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages);
+  cfg.blockDim = dim3(GEN ? kThreads + 32 * kLoaders : kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.p);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -670,7 +782,7 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemMax;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -696,18 +808,38 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
   const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 ? 2 : 1;
+  const int units = cg == 2 ? pairs : sms;
+  a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
-  if (p.epi != MM_EPI_STATS) {
-    const int64_t typical = p.rag == MM_RAG_COLS ? 2 * (((int64_t)p.cols + p.groups - 1) / p.groups) : p.cols;
-    while (a.bn > 64 * cg && a.bn / 2 >= std::min<int64_t>(typical, p.cols)) a.bn /= 2;
+  if (p.rag == MM_RAG_COLS) {
+    // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
+    // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
+    const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
+    while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
+  } else if (p.epi != MM_EPI_STATS) {
+    // the width with the shortest schedule: rounds over the SMs times a tile's columns (and what a tile costs
+    // whatever its width, about 24 columns' time). Widths that are no multiple of 64 run at the next larger one's
+    // rate (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us).
+    int64_t best = INT64_MAX;
+    for (int bn = 256; bn >= 64; bn -= 64) {
+      if (bn % (p.b.red_major ? 64 : 64 * cg)) continue;
+      const int64_t tiles = (int64_t)a.lane_tiles * ((p.cols + bn - 1) / bn) * (p.rag == MM_RAG_RED ? p.groups : 1);
+      const int64_t tail = tiles % units;
+      // the last, partial round: its tiles are split while all parts still fit one round
+      int lg = 0;
+      while (p.rag == MM_DENSE && tail && lg < 2 && (tail << (lg + 1)) <= units && (bn >> (lg + 1)) % (p.b.red_major ? 64 : 64 * cg) == 0) ++lg;
+      const int64_t cost = tiles / units * (bn + 24) + (tail ? (bn >> lg) + 24 : 0);
+      if (cost < best) best = cost, a.bn = bn, a.tail_lg = lg, a.tail_from = (int)std::min<int64_t>(tiles - tail, INT32_MAX);
+    }
   }
   a.stages = 1;
-  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1) <= kSmemMax) ++a.stages;
-  a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
-  a.b_box = p.rag == MM_RAG_COLS ? 32 : std::min(128, a.bn / cg);
-  const int64_t col_tiles = p.rag == MM_RAG_COLS ? (p.cols + a.bn - 1) / a.bn + p.groups : (p.cols + a.bn - 1) / a.bn;
-  const int64_t tiles = a.lane_tiles * col_tiles * (p.rag == MM_RAG_RED ? p.groups : 1);
-  if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, p) <= kSmemMax) ++a.stages;
+  a.b_box = p.rag == MM_RAG_COLS || a.bn / cg % 64 ? 32 : 64;  // divides what a CTA stages
+  a.col_tiles = (p.cols + a.bn - 1) / a.bn;
+  const int64_t tiles = a.lane_tiles * (int64_t)(p.rag == MM_RAG_COLS ? a.col_tiles + p.groups : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
+  if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+  if (a.tail_lg == 0) a.tail_from = (int)tiles;
+  a.by_lanes = Divider(a.lane_tiles), a.by_panel = Divider(a.lane_tiles * kPanel), a.by_matrix = Divider(a.lane_tiles * a.col_tiles);
   CUtensorMap ta = {}, tb = {};
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
@@ -716,7 +848,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK);
     if (!ok) return cudaErrorInvalidValue;
   }
-  const int grid = cg * (int)std::max<int64_t>(1, std::min<int64_t>(cg == 2 ? pairs : sms, tiles));
+  const int grid = cg * (int)std::max<int64_t>(1, std::min<int64_t>(units, tiles + (tiles - (p.rag == MM_DENSE ? a.tail_from : tiles)) * ((1 << a.tail_lg) - 1)));
   if (gen) return launch_epi<1, true>(ta, tb, a, grid, s);
   return cg == 2 ? launch_epi<2, false>(ta, tb, a, grid, s) : launch_epi<1, false>(ta, tb, a, grid, s);
 }
