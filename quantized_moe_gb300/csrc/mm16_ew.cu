@@ -7,37 +7,90 @@ namespace {
 
 constexpr int kMaxChunks = 256;
 
-// Column sums run over chunks of at least 16 rows: one block computes a strip of 64 columns of one
-// chunk with four rows of threads, adds these through shared memory and writes one partial per
-// column; the second kernel adds the chunks in order. The order of every sum is fixed.
+// dz = dy * act'(z), and the column sums of dz (unrounded, fp32). A block takes 256 columns of one chunk of rows: each of
+// its eight warps walks every eighth row with one 16-byte load per operand (eight columns a thread), then the warps'
+// sums are added in order through shared memory, one partial per column and chunk. The second kernel adds the chunks
+// in order, 8 rows of threads per column. The order of every sum is fixed. HBM bound: dy, z and dz cross it once
+// (elements that cannot be moved 8 at a time go one by one).
+template <bool VEC>
 __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ dy, int64_t lddy,
                                                        const void* __restrict__ z, int64_t ldz, void* __restrict__ dz,
                                                        int64_t lddz, float* __restrict__ part, int rows, int n,
                                                        int act, int f16, int chunk_rows) {
-  __shared__ float s[4][64];
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + tx;
+  __shared__ float s[8][256 + 8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + lane * 8;
   const int r0 = blockIdx.y * chunk_rows, r1 = min(r0 + chunk_rows, rows);
-  float sum = 0.f;
-  if (c < n)
-    for (int r = r0 + ty; r < r1; r += 4) {
-      float v = ld16(dy, (int64_t)r * lddy + c, f16);
-      if (act != MM_ACT_NONE) v *= mm_act_slope(ld16(z, (int64_t)r * ldz + c, f16), act);
-      if (dz) st16(dz, (int64_t)r * lddz + c, v, f16);
-      sum += v;
+  float sum[8] = {};
+  if (c < n) {
+#pragma unroll 2
+    for (int r = r0 + warp; r < r1; r += 8) {
+      float g[8];
+      uint16_t hy[8], hz[8];
+      const uint16_t* py = static_cast<const uint16_t*>(dy) + (int64_t)r * lddy + c;
+      const uint16_t* pz = static_cast<const uint16_t*>(z) + (int64_t)r * ldz + c;
+      if (VEC) {
+        *reinterpret_cast<uint4*>(hy) = *reinterpret_cast<const uint4*>(py);
+        if (act != MM_ACT_NONE) *reinterpret_cast<uint4*>(hz) = *reinterpret_cast<const uint4*>(pz);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          hy[i] = c + i < n ? py[i] : (uint16_t)0;
+          if (act != MM_ACT_NONE) hz[i] = c + i < n ? pz[i] : (uint16_t)0;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = ld16(hy, i, f16);
+        if (act != MM_ACT_NONE) g[i] *= mm_act_slope(ld16(hz, i, f16), act);
+        sum[i] += g[i];
+      }
+      if (dz) {
+        uint16_t* pd = static_cast<uint16_t*>(dz) + (int64_t)r * lddz + c;
+        uint16_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st16(h, i, g[i], f16);
+        if (VEC) {
+          *reinterpret_cast<uint4*>(pd) = *reinterpret_cast<const uint4*>(h);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < n) pd[i] = h[i];
+        }
+      }
     }
+  }
   if (!part) return;
-  s[ty][tx] = sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = sum[i];
   __syncthreads();
-  if (ty == 0 && c < n) part[(int64_t)blockIdx.y * n + c] = (s[0][tx] + s[1][tx]) + (s[2][tx] + s[3][tx]);
+  const int cc = blockIdx.x * 256 + threadIdx.x;
+  if (cc < n) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s[w][threadIdx.x];
+    part[(int64_t)blockIdx.y * n + cc] = v;
+  }
 }
 
-__global__ void colsum_join_kernel(const float* __restrict__ part, int chunks, int n, void* __restrict__ db, int f16) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= n) return;
+__global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int chunks, int n,
+                                                          void* __restrict__ db, int f16) {
+  __shared__ float s[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
-  for (int i = 0; i < chunks; ++i) v += part[(int64_t)i * n + c];
-  st16(db, c, v, f16);
+  if (c < n) {
+#pragma unroll 8
+    for (int i = warp; i < chunks; i += 8) v += part[(int64_t)i * n + c];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < n) {
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s[w][lane];
+    st16(db, c, v, f16);
+  }
 }
 
 // One warp per token: the tiles' (max, sum) are joined as (M, S) with M = max m_i and
@@ -98,10 +151,14 @@ int mm_colsum_chunks(int rows) {
 
 cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz, void* dz, int64_t lddz, float* part,
                         void* db, int rows, int n, int act, int f16, cudaStream_t s) {
-  const int chunks = mm_colsum_chunks(rows);
-  act_grad_kernel<<<dim3((n + 63) / 64, chunks), 256, 0, s>>>(dy, lddy, z, ldz, dz, lddz, part, rows, n, act, f16,
-                                                              (rows + chunks - 1) / chunks);
-  if (part) colsum_join_kernel<<<(n + 127) / 128, 128, 0, s>>>(part, chunks, n, db, f16);
+  const int chunks = mm_colsum_chunks(rows), chunk_rows = (rows + chunks - 1) / chunks;
+  const auto vec = [](const void* p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0); };
+  const dim3 grid((n + 255) / 256, chunks);
+  if (n % 8 == 0 && vec(dy, lddy) && (act == MM_ACT_NONE || vec(z, ldz)) && vec(dz, lddz))
+    act_grad_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, dz, lddz, part, rows, n, act, f16, chunk_rows);
+  else
+    act_grad_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, dz, lddz, part, rows, n, act, f16, chunk_rows);
+  if (part) colsum_join_kernel<<<(n + 31) / 32, 256, 0, s>>>(part, chunks, n, db, f16);
   return cudaGetLastError();
 }
 

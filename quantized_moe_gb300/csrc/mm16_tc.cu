@@ -40,6 +40,8 @@ constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of
 constexpr int kFirstLoader = 4 + kEpiWarps;
 constexpr int kLoaders = 8;               // loader warps of the unaligned form
 constexpr int kThreads = 32 * kFirstLoader;
+constexpr int kRowBytes = 2 * BM + 16;    // a staged row of 128 lanes: 16 bytes on, so that eight rows' chunks hit all banks
+constexpr int kOutBytes = 32 * kRowBytes;  // 32 columns of 128 lanes on their way out, one per half of the epilogue
 constexpr int kSmemMax = 232448;
 
 // n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d).
@@ -57,13 +59,14 @@ struct TcArgs {
   MmProblem p;
   int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
+  int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
   int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
   Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
 };
 
 // Barriers, the tensor-memory address and the abort flag, then the group tables (tile_of).
 __host__ __device__ constexpr int ctrl_bytes(int rag, int groups) {
-  return 24 * kMaxStages + 32 + 16 + (rag == MM_DENSE ? 8 * BM : 4 * (groups + 1) * (rag == MM_RAG_COLS ? 2 : 1));
+  return 24 * kMaxStages + 32 + 16 + (rag == MM_DENSE ? 0 : 4 * (groups + 1) * (rag == MM_RAG_COLS ? 2 : 1));
 }
 
 __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
@@ -358,6 +361,97 @@ __device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int 
   }
 }
 
+// ---- 16-bit results by rows: the warps hold 32 lanes x 32 columns as fragments (a thread: lanes i/4 + 8 r, columns
+// 8 j + 2 (i % 4) and the next), which stmatrix writes transposed into shared memory, from where whole rows of 128
+// lanes leave as 16-byte stores.
+struct Frag {
+  float v[4][4][2];  // [block of 8 columns][block of 8 lanes][column parity]
+};
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, Frag& f) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + ((uint32_t)(16 * h) << 16))
+        : "memory");
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) f.v[j][2 * h + (q >> 1)][q & 1] = __uint_as_float(r[4 * j + q]);
+  }
+  // (the values may be used only after the wait; it is ordered by the dependence below)
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) asm volatile("" : "+f"(f.v[j][r][0]), "+f"(f.v[j][r][1]));
+}
+__device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
+  if (f16) {
+    const __half2 t = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&t);
+}
+// The address that lane i gives for its row of an 8 x 8 block: block i / 8 of the warp's four, row i % 8.
+__device__ __forceinline__ uint32_t frag_addr(uint32_t stage, int quad, int j, int lane) {
+  return stage + (uint32_t)((8 * j + (lane & 7)) * kRowBytes + quad * 64 + (lane >> 3) * 16);
+}
+__device__ __forceinline__ void frag_out(uint32_t stage, int quad, int lane, const Frag& f, int f16) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(frag_addr(stage, quad, j, lane)),
+                 "r"(pack16(f.v[j][0][0], f.v[j][0][1], f16)), "r"(pack16(f.v[j][1][0], f.v[j][1][1], f16)),
+                 "r"(pack16(f.v[j][2][0], f.v[j][2][1], f16)), "r"(pack16(f.v[j][3][0], f.v[j][3][1], f16))
+                 : "memory");
+}
+__device__ __forceinline__ void frag_add(uint32_t stage, int quad, int lane, Frag& f, int f16) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t r[4];
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(frag_addr(stage, quad, j, lane))
+                 : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (f16) {
+        f.v[j][i][0] += __half2float(__ushort_as_half((uint16_t)r[i]));
+        f.v[j][i][1] += __half2float(__ushort_as_half((uint16_t)(r[i] >> 16)));
+      } else {
+        f.v[j][i][0] += __uint_as_float(r[i] << 16);
+        f.v[j][i][1] += __uint_as_float(r[i] & 0xffff0000u);
+      }
+    }
+  }
+}
+// Rows of 16-byte pieces between shared and global memory: thread i of 128 takes piece i % 16 of rows i / 16 + 8 k.
+struct Rows {
+  uint32_t smem;  // of the thread's first piece
+  int row;
+  bool live;  // the piece lies inside the matrix
+  __device__ __forceinline__ void store(void* base, int64_t at, int64_t ld, int nv) const {
+    uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (live && row + 8 * k < nv) q[k * ld] = lds128(smem + 8 * k * kRowBytes);  // (ld: 8 rows of ld elements, in pieces)
+  }
+  __device__ __forceinline__ void load(const void* base, int64_t at, int64_t ld, int nv, uint4 (&r)[4]) const {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r[k] = live && row + 8 * k < nv ? q[k * ld] : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void stage(const uint4 (&r)[4]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(smem + 8 * k * kRowBytes), "r"(r[k].x), "r"(r[k].y), "r"(r[k].z), "r"(r[k].w) : "memory");
+  }
+};
+
 // Running maximum m and sum s of exp(z - m) of one token over 32 words (nv exist).
 __device__ __forceinline__ void epi_stats(float (&v)[32], int nv, float& m, float& s) {
   float top = m;
@@ -389,7 +483,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   // the stages start on a 1024-byte boundary (the swizzle's period); in a pair both CTAs have the same layout
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int stage_bytes = A_BYTES + a.bn / CG * BK * 2;
-  uint8_t* ctrl = smem + a.stages * stage_bytes;
+  uint8_t* out_stage = smem + a.stages * stage_bytes;  // [2][kOutBytes]
+  uint8_t* ctrl = out_stage + 2 * kOutBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
@@ -397,7 +492,6 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   uint64_t* clean = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + kMaxStages);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  float2* exchange = reinterpret_cast<float2*>(tmem_slot + 4);  // [BM], softmax partials only
   int* lo_of = reinterpret_cast<int*>(tmem_slot + 4);
   int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -599,28 +693,58 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
   } else if (warp >= 4 && warp < kFirstLoader) {
     // ------------------------------------------------------------------ epilogue
-    // Two warps per lane quadrant take the tile's 32-column chunks in turn (for the softmax partials each
-    // keeps its own and the pair adds them up through shared memory).
+    // Two warps per lane quadrant take the tile's 32-column chunks in turn; the four warps of a half work on the same
+    // chunk.
     const int quad = warp & 3, half = (warp - 4) >> 2;
+    const MmEpiArgs& e = p.e;
+    const uint32_t stage = su32(out_stage) + half * kOutBytes;
+    Rows rows;
+    {
+      const int i = threadIdx.x & 127;
+      rows.row = i >> 4;
+      rows.smem = stage + (uint32_t)(rows.row * kRowBytes + (i & 15) * 16);
+      rows.live = false;
+    }
     int local = 0;
     for (int t = first; t < tiles; t += step) {
       const Tile o = tile_of<CG>(a, lo_of, pref, t);
       if (o.n <= 0) continue;
-      const int l = o.l0 + BM * rank + 32 * quad + lane;
-      const bool live = l < p.lanes;
+      const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
       const int buf = local & 1;
-      float m = -INFINITY, total = 0.f, lse = 0.f, gw = 0.f;
-      int lab = -1;
-      if (EPI != MM_EPI_STORE && live) {
-        lab = __ldg(p.e.labels + l);
-        if (EPI == MM_EPI_SOFTGRAD) {
-          const bool skip = lab == p.e.ignore || lab < 0 || lab >= p.e.vocab;
-          lse = __ldg(p.e.lse + l);
-          gw = skip ? 0.f : __ldg(p.e.g + l) / __ldg(p.e.gscale) * kMmGradOne;
-          if (skip) lab = -1;
+      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      // what the tile needs besides its sums is fetched before they are waited for
+      const bool by_rows = EPI != MM_EPI_STATS && a.rows_out;
+      const int64_t group_out = p.rag == MM_RAG_RED ? o.g * e.group_stride : 0;
+      const void* add = e.accumulate ? e.out : e.residual;
+      const int64_t add_ld = e.accumulate ? e.ld : e.ldr;
+      const int piece = l0 + (threadIdx.x & 15) * 8;
+      const int64_t first_row = o.c0 + 32 * half + rows.row;
+      int64_t add_at = (e.accumulate ? group_out : 0) + first_row * add_ld + piece;
+      uint4 next[4];
+      rows.live = piece < p.lanes;
+      if (by_rows && add) rows.load(add, add_at, add_ld, o.n - 32 * half, next);
+      // lanes of the fragments (four per thread) or the thread's own lane
+      float lse[4], gw[4], bias[4];
+      int lab[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int l = l0 + 32 * quad + (by_rows ? (lane >> 2) + 8 * r : lane);
+        lse[r] = 0.f, gw[r] = 0.f, bias[r] = 0.f, lab[r] = -1;
+        if (l >= p.lanes || (!by_rows && r)) continue;
+        if (EPI == MM_EPI_STORE) {
+          if (e.bias) bias[r] = ld16(e.bias, l, p.f16);
+        } else {
+          lab[r] = __ldg(e.labels + l);
+          if (EPI == MM_EPI_SOFTGRAD) {
+            const bool skip = lab[r] == e.ignore || lab[r] < 0 || lab[r] >= e.vocab;
+            lse[r] = __ldg(e.lse + l);
+            gw[r] = skip ? 0.f : __ldg(e.g + l) / __ldg(e.gscale) * kMmGradOne;
+            lab[r] = skip ? -1 : lab[r] - e.word0;
+          }
         }
       }
+      float m = -INFINITY, total = 0.f;
       bool ok = true;
       if (sum) {
         ok = mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5);
@@ -628,37 +752,113 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         tc_fence_after();
         ++local;
       }
-      // (all warps of the epilogue leave together: the partials' exchange has a barrier)
+      // (all warps of the epilogue leave together: what follows has barriers)
       if (!named_bar_all(1, 32 * kEpiWarps, ok)) break;
-      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
-      for (int c = 32 * half; c < o.n; c += 64) {
-        float v[32];
-        if (sum) {
-          tmem_ld32(taddr + c, v);
-        } else {
+      if (by_rows) {
+        for (int c = 32 * half; c < o.n; c += 64) {
+          Frag f;
+          if (sum) {
+            tmem_ld_frag(taddr + c, f);
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        }
-        const int nv = min(32, o.n - c);
-        if (EPI == MM_EPI_STORE) {
-          epi_store(p, o.g, l, o.c0 + c, nv, v);
-          put(p, o.g, l, o.c0 + c, nv, v);
-        } else if (EPI == MM_EPI_STATS) {
-          epi_stats(v, nv, m, total);
-          const int at = lab - (o.c0 + c);
-          if (live && at >= 0 && at < nv) {
-            float z = 0.f;
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == at) z = v[j];
-            p.e.zlab[l] = z;
+              for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
           }
-        } else {
-          // (a row without gradient stays zero even where its logits are not finite)
-          const int at = lab >= 0 ? lab - p.e.word0 - (o.c0 + c) : -1;
+          const int64_t row_at = first_row + (c - 32 * half);
+          if (EPI == MM_EPI_SOFTGRAD) {
+            const int c_first = o.c0 + c + 2 * (lane & 3);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = gw == 0.f ? 0.f : (__expf(v[j] - lse) - (j == at ? 1.f : 0.f)) * gw;
-          put(p, 0, l, o.c0 + c, nv, v);
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  // (a row without gradient stays zero even where its logits are not finite)
+                  const float d = (__expf(f.v[j][r][q] - lse[r]) - (c_first + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
+                  f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
+                }
+          } else {
+            if (e.scale) {
+              const float sc = __ldg(e.scale);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] *= sc, f.v[j][r][1] *= sc;
+            }
+            if (e.bias) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] += bias[r], f.v[j][r][1] += bias[r];
+            }
+            if (e.z) {
+              frag_out(stage, quad, lane, f, p.f16);
+              named_bar(2 + half, 128);
+              rows.store(e.z, row_at * e.ldz + piece, e.ldz, o.n - c);
+              named_bar(2 + half, 128);
+            }
+            if (e.act == MM_ACT_SILU) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] = silu_fast(f.v[j][r][0]), f.v[j][r][1] = silu_fast(f.v[j][r][1]);
+            } else if (e.act == MM_ACT_GELU) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_GELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_GELU);
+            } else if (e.act == MM_ACT_RELU) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_RELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_RELU);
+            }
+            if (add) {
+              rows.stage(next);
+              named_bar(2 + half, 128);
+              add_at += 64 * add_ld;
+              if (c + 64 < o.n) rows.load(add, add_at, add_ld, o.n - c - 64, next);
+              frag_add(stage, quad, lane, f, p.f16);  // (each warp rereads and overwrites its own quarter only)
+              __syncwarp();
+            }
+          }
+          frag_out(stage, quad, lane, f, p.f16);
+          named_bar(2 + half, 128);
+          rows.store(e.out, group_out + row_at * e.ld + piece, e.ld, o.n - c);
+          named_bar(2 + half, 128);
+        }
+      } else {
+        const int l = l0 + 32 * quad + lane;
+        const bool live = l < p.lanes;
+        for (int c = 32 * half; c < o.n; c += 64) {
+          float v[32];
+          if (sum) {
+            tmem_ld32(taddr + c, v);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          const int nv = min(32, o.n - c);
+          if (EPI == MM_EPI_STORE) {
+            epi_store(p, o.g, l, o.c0 + c, nv, v);
+            put(p, o.g, l, o.c0 + c, nv, v);
+          } else if (EPI == MM_EPI_STATS) {
+            epi_stats(v, nv, m, total);
+            const int at = lab[0] - (o.c0 + c);
+            if (live && at >= 0 && at < nv) {
+              float z = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == at) z = v[j];
+              e.zlab[l] = z;
+            }
+          } else {
+            const int at = lab[0] - (o.c0 + c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
+            put(p, 0, l, o.c0 + c, nv, v);
+          }
         }
       }
       if (sum) {
@@ -671,16 +871,17 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             mbar_arrive(acc_empty + buf);
         }
       }
-      if (EPI == MM_EPI_STATS) {
-        float2* x = exchange + 32 * quad + lane;
+      if (EPI == MM_EPI_STATS) {  // the two halves' partials are joined
+        float2* x = reinterpret_cast<float2*>(out_stage) + 32 * quad + lane;
+        const int l = l0 + 32 * quad + lane;
         if (half) *x = make_float2(m, total);
         named_bar(2, 32 * kEpiWarps);
-        if (!half && live) {
+        if (!half && l < p.lanes) {
           const float2 q = *x;
           const float top = fmaxf(m, q.x);
           // (a half without likely words has m = -inf and adds its sum, 0 or NaN)
           const float s0 = m == top ? total : total * __expf(m - top), s1 = q.x == top ? q.y : q.y * __expf(q.x - top);
-          p.e.part[(int64_t)(o.c0 / a.bn) * p.lanes + l] = make_float2(top, s0 + s1);
+          e.part[(int64_t)(o.c0 / a.bn) * p.lanes + l] = make_float2(top, s0 + s1);
         }
       }
     }
@@ -721,7 +922,7 @@ bool tma_ready(const MmOperand& o) {
 }
 
 int smem_bytes(int cg, int bn, int stages, const MmProblem& p) {
-  return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + ctrl_bytes(p.rag, p.groups);
+  return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + 2 * kOutBytes + ctrl_bytes(p.rag, p.groups);
 }
 
 template <int CG, int EPI, bool GEN>
@@ -840,6 +1041,10 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   if (a.tail_lg == 0) a.tail_from = (int)tiles;
   a.by_lanes = Divider(a.lane_tiles), a.by_panel = Divider(a.lane_tiles * kPanel), a.by_matrix = Divider(a.lane_tiles * a.col_tiles);
+  const MmEpiArgs& ep = p.e;
+  const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
+  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
+               by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   CUtensorMap ta = {}, tb = {};
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
