@@ -7,6 +7,25 @@ namespace {
 
 constexpr int kMaxChunks = 256;
 
+// Programmatic dependent launch, as in the products: a kernel sets itself up while its predecessor runs, and touches
+// global memory only after that is complete.
+__device__ __forceinline__ void begin() {
+  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;\n" ::: "memory");
+}
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // dz = dy * act'(z), and the column sums of dz (unrounded, fp32). A block takes 256 columns of one chunk of rows: each of
 // its eight warps walks every eighth row with one 16-byte load per operand (eight columns a thread), then the warps'
 // sums are added in order through shared memory, one partial per column and chunk. The second kernel adds the chunks
@@ -18,6 +37,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ 
                                                        int64_t lddz, float* __restrict__ part, int rows, int n,
                                                        int act, int f16, int chunk_rows) {
   __shared__ float s[8][256 + 8];
+  begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 256 + lane * 8;
   const int r0 = blockIdx.y * chunk_rows, r1 = min(r0 + chunk_rows, rows);
@@ -76,6 +96,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ 
 __global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int chunks, int n,
                                                           void* __restrict__ db, int f16) {
   __shared__ float s[8][32];
+  begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -100,6 +121,7 @@ __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* __restr
                                                            const int* __restrict__ labels, int ignore, int vocab,
                                                            int rows, float* __restrict__ loss,
                                                            float* __restrict__ lse, int* err) {
+  begin();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= rows) return;
   float m = -INFINITY;
@@ -124,6 +146,7 @@ __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* __restr
 __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* __restrict__ g, const int* __restrict__ labels,
                                                           int ignore, int vocab, int rows, float* __restrict__ gs) {
   __shared__ float s[32];
+  begin();
   float m = 0.f;
   for (int i = threadIdx.x; i < rows; i += 1024) {
     const int lab = labels[i];
@@ -154,24 +177,21 @@ cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz
   const int chunks = mm_colsum_chunks(rows), chunk_rows = (rows + chunks - 1) / chunks;
   const auto vec = [](const void* p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0); };
   const dim3 grid((n + 255) / 256, chunks);
-  if (n % 8 == 0 && vec(dy, lddy) && (act == MM_ACT_NONE || vec(z, ldz)) && vec(dz, lddz))
-    act_grad_kernel<true><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, dz, lddz, part, rows, n, act, f16, chunk_rows);
-  else
-    act_grad_kernel<false><<<grid, 256, 0, s>>>(dy, lddy, z, ldz, dz, lddz, part, rows, n, act, f16, chunk_rows);
-  if (part) colsum_join_kernel<<<(n + 31) / 32, 256, 0, s>>>(part, chunks, n, db, f16);
-  return cudaGetLastError();
+  const bool wide = n % 8 == 0 && vec(dy, lddy) && (act == MM_ACT_NONE || vec(z, ldz)) && vec(dz, lddz);
+  cudaError_t e = launch(wide ? act_grad_kernel<true> : act_grad_kernel<false>, grid, 256, s, dy, lddy, z, ldz, dz, lddz, part, rows, n,
+                         act, f16, chunk_rows);
+  if (e == cudaSuccess && part) e = launch(colsum_join_kernel, dim3((n + 31) / 32), 256, s, part, chunks, n, db, f16);
+  return e;
 }
 
 cudaError_t mm_softmax_join(const float2* part, int tiles, const float* zlab, const int* labels, int ignore, int vocab,
                             int rows, float* loss, float* lse, int* err, cudaStream_t s) {
-  softmax_join_kernel<<<(rows + 7) / 8, 256, 0, s>>>(part, tiles, zlab, labels, ignore, vocab, rows, loss, lse, err);
-  return cudaGetLastError();
+  return launch(softmax_join_kernel, dim3((rows + 7) / 8), 256, s, part, tiles, zlab, labels, ignore, vocab, rows, loss, lse, err);
 }
 
 cudaError_t mm_grad_scale(const float* g, const int* labels, int ignore, int vocab, int rows, float* gs,
                           cudaStream_t s) {
-  grad_scale_kernel<<<1, 1024, 0, s>>>(g, labels, ignore, vocab, rows, gs);
-  return cudaGetLastError();
+  return launch(grad_scale_kernel, dim3(1), 1024, s, g, labels, ignore, vocab, rows, gs);
 }
 
 }  // namespace ds4

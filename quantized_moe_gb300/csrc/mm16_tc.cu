@@ -41,6 +41,7 @@ constexpr int kFirstLoader = 4 + kEpiWarps;
 constexpr int kLoaders = 8;               // loader warps of the unaligned form
 constexpr int kThreads = 32 * kFirstLoader;
 constexpr int kRowBytes = 2 * BM + 16;    // a staged row of 128 lanes: 16 bytes on, so that eight rows' chunks hit all banks
+constexpr int kPartLd = BM + 4;           // floats from one column of a partial sum to the next (conflict-free as fragments)
 constexpr int kOutBytes = 32 * kRowBytes;  // 32 columns of 128 lanes on their way out, one per half of the epilogue
 constexpr int kSmemMax = 232448;
 
@@ -60,6 +61,8 @@ struct TcArgs {
   int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
+  int alt;                    // the epilogue's halves take whole tiles in turn instead of halves of each tile
+  int split;                  // CTAs (a cluster) that share a tile's reduction; 1: none
   int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
   Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
 };
@@ -77,6 +80,11 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
+
+// Programmatic dependent launch: the next launch of the stream may set itself up while this one runs; nothing of
+// global memory is read or written before the launches in front are complete.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <int CG>
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -171,7 +179,7 @@ struct Tile {
 // ends where the next one begins, or is empty if that lies before it); for ragged columns pref[g], the running
 // count of the groups' column tiles.
 template <int CG>
-__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int t) {
+__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int t, int share) {
   const MmProblem& p = a.p;
   Tile o;
   int col_tiles = a.col_tiles, c_lo = 0, c_n = p.cols, part = 0, width = a.bn;
@@ -207,6 +215,12 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
   o.l0 = lt * BM * CG;
   o.c0 = c_lo + ct * a.bn + part * width;
   o.n = min(width, c_n - ct * a.bn - part * width);  // (a part past the last column has none)
+  if (CG == 1 && a.split > 1) {  // this CTA's share of the reduction, whole stages
+    const int blocks = (o.red + BK - 1) / BK;
+    const int b0 = blocks * share / a.split * BK, b1 = blocks * (share + 1) / a.split * BK;
+    o.red = min(o.red, b1) - b0;
+    o.r0 += b0;
+  }
   return o;
 }
 
@@ -218,33 +232,60 @@ __device__ __forceinline__ int mma_n(const MmProblem& p, int n) {
   return (n + q - 1) / q * q;
 }
 
-// Eight consecutive elements of a row as one 16-byte chunk, zeros past `valid`; any alignment.
-__device__ __forceinline__ uint4 gather8(const uint16_t* src, int valid) {
-  uint32_t h[8];
+// Eight consecutive elements of a row, any alignment, zeros past `valid`: the aligned 32-bit words that hold them,
+// shifted by an element where the row starts in the middle of a word.
+__device__ __forceinline__ void words_of(const uint16_t* src, int valid, uint32_t (&w)[5]) {
+  const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
+  const uint32_t* q = reinterpret_cast<const uint32_t*>(src - odd);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = i < valid ? (uint32_t)__ldg(src + i) : 0u;
-  return make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+  for (int i = 0; i < 5; ++i) w[i] = 2 * i < valid + (int)odd ? __ldg(q + i) : 0u;  // (a word with a wanted element)
 }
-// One operand's stage by ordinary loads: `boxes` boxes of `rows` rows x 64 elements, in the layout that
-// the TMA's 128-byte swizzle gives (chunk index XOR row mod 8). K-major: box rows are lanes or columns
-// from mn0 and elements the reduction from r0; MN-major the other way round.
+__device__ __forceinline__ uint4 chunk_of(const uint16_t* src, int valid, const uint32_t (&w)[5]) {
+  const uint32_t sh = (reinterpret_cast<uintptr_t>(src) & 2) * 8;
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r[i] = __funnelshift_r(w[i], w[i + 1], sh);
+    const int left = valid - 2 * i;
+    if (left < 2) r[i] = left < 1 ? 0u : r[i] & 0xffffu;
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+// One operand's stage by ordinary loads, in the layout that the TMA's 128-byte swizzle gives (chunk index XOR row mod
+// 8). K-major: the rows of 128 bytes are lanes or columns from mn0 and their elements the reduction from r0; MN-major
+// the other way round, in boxes of 64 x 64. Four chunks a thread are in flight.
 __device__ __forceinline__ void load_stage(uint8_t* dst, const uint16_t* base, int64_t ld, bool red_major, int mn0,
                                            int mn_end, int r0, int r_end, int mn_count, int tid) {
   const int chunks = red_major ? mn_count * 8 : mn_count / 64 * 512;
-  for (int i = tid; i < chunks; i += kLoaders * 32) {
-    const int row = i >> 3, ch = i & 7;  // row of 128 bytes in the stage, 16-byte chunk in it
-    int64_t at;
-    int valid;
-    if (red_major) {
-      valid = mn0 + row < mn_end ? min(8, max(0, r_end - (r0 + ch * 8))) : 0;
-      at = (int64_t)(mn0 + row) * ld + r0 + ch * 8;
-    } else {
-      const int mn = mn0 + (row >> 6) * 64 + ch * 8, r = r0 + (row & 63);
-      valid = r < r_end ? min(8, max(0, mn_end - mn)) : 0;
-      at = (int64_t)r * ld + mn;
+  for (int i0 = tid; i0 < chunks; i0 += 4 * kLoaders * 32) {
+    const uint16_t* src[4];
+    int valid[4];
+    uint32_t w[4][5];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kLoaders * 32, row = i >> 3, ch = i & 7;
+      int64_t at;
+      if (red_major) {
+        valid[u] = i < chunks && mn0 + row < mn_end ? min(8, max(0, r_end - (r0 + ch * 8))) : 0;
+        at = (int64_t)(mn0 + row) * ld + r0 + ch * 8;
+      } else {
+        const int mn = mn0 + (row >> 6) * 64 + ch * 8, r = r0 + (row & 63);
+        valid[u] = i < chunks && r < r_end ? min(8, max(0, mn_end - mn)) : 0;
+        at = (int64_t)r * ld + mn;
+      }
+      src[u] = base + at;
+      if (valid[u] > 0) {
+        words_of(src[u], valid[u], w[u]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 5; ++k) w[u][k] = 0u;
+      }
     }
-    const uint4 v = valid > 0 ? gather8(base + at, valid) : make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u * kLoaders * 32, row = i >> 3, ch = i & 7;
+      if (i < chunks) *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = chunk_of(src[u], valid[u], w[u]);
+    }
   }
 }
 
@@ -484,7 +525,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int stage_bytes = A_BYTES + a.bn / CG * BK * 2;
   uint8_t* out_stage = smem + a.stages * stage_bytes;  // [2][kOutBytes]
-  uint8_t* ctrl = out_stage + 2 * kOutBytes;
+  float* parts = reinterpret_cast<float*>(out_stage + 2 * kOutBytes);  // [split - 1][bn][kPartLd], in the cluster's first CTA
+  uint8_t* ctrl = out_stage + 2 * kOutBytes + (a.split - 1) * a.bn * kPartLd * 4;
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
@@ -508,7 +550,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, kEpiWarps * CG);
+      mbar_init(acc_empty + i, (a.alt ? kEpiWarps / 2 : kEpiWarps) * CG);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -518,25 +560,26 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     tmap_prefetch(&ta);
     tmap_prefetch(&tb);
   }
-  if (p.rag != MM_DENSE && warp == 2) {
+  wait_for_previous();
+  let_next_start();
+  if (p.rag != MM_DENSE) {
     const int total = p.rag == MM_RAG_COLS ? p.cols : p.red;
-    int run = 0;
-    for (int g0 = 0; g0 <= p.groups; g0 += 32) {
-      const int g = g0 + lane;
-      int n = 0;
-      if (g <= p.groups) {
-        const int lo = min(max(__ldg(p.offsets + g), 0), total);
-        lo_of[g] = lo;
-        if (g < p.groups) n = (max(min(__ldg(p.offsets + g + 1), total) - lo, 0) + a.bn - 1) / a.bn;
-      }
-      int inc = n;
+    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) lo_of[g] = min(max(__ldg(p.offsets + g), 0), total);
+    __syncthreads();
+    if (p.rag == MM_RAG_COLS && warp == 2) {
+      int run = 0;
+      for (int g0 = 0; g0 <= p.groups; g0 += 32) {
+        const int g = g0 + lane;
+        const int n = g < p.groups ? (max(lo_of[g + 1] - lo_of[g], 0) + a.bn - 1) / a.bn : 0;
+        int inc = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += u;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += u;
+        }
+        if (g <= p.groups) pref[g] = run + inc - n;
+        run += __shfl_sync(0xffffffffu, inc, 31);
       }
-      if (p.rag == MM_RAG_COLS && g <= p.groups) pref[g] = run + inc - n;
-      run += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   tc_fence_before();
@@ -546,7 +589,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   int tiles = a.lane_tiles * (p.rag == MM_RAG_COLS ? pref[p.groups] : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
   if (p.rag == MM_DENSE) tiles += (tiles - a.tail_from) * ((1 << a.tail_lg) - 1);
-  const int first = blockIdx.x / CG, step = gridDim.x / CG;
+  const int share = CG == 2 ? 2 : a.split;  // CTAs that work on the same tile
+  const int first = blockIdx.x / share, step = gridDim.x / share;
+  const int part = CG == 1 && a.split > 1 ? (int)cluster_ctarank() : 0;
+  if (CG == 1 && a.split > 1) tiles = min(tiles, first + 1);  // one tile a cluster, whatever the offsets say
 
   if (warp == 0 && !GEN) {
     // ------------------------------------------------------------------ TMA producer
@@ -556,7 +602,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     bool ok = true;
     const int a_boxes = a_red ? 1 : 2;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
       const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : nb / 64;
@@ -597,7 +643,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     bool ok = true;
     const int tid = threadIdx.x - kThreads;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const uint16_t* pb = static_cast<const uint16_t*>(p.b.p);
@@ -626,7 +672,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const uint64_t a_desc = op_desc(su32(smem), p.a.red_major), b_desc = op_desc(su32(smem + A_BYTES), p.b.red_major);
       const uint32_t type = p.f16 ? 0u : 1u;
       for (int t = first; t < tiles && ok; t += step) {
-        const Tile o = tile_of<CG>(a, lo_of, pref, t);
+        const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
         if (o.red <= 0 || o.n <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
         const int buf = local & 1, n = mma_n<CG>(p, o.n);
         const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
@@ -667,7 +713,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       for (int k = 0; k < o.red; k += BK) {
         if (!mbar_wait(full + s, ph, abort_flag, p.err, 2)) {
           ok = false;
@@ -705,13 +751,18 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.smem = stage + (uint32_t)(rows.row * kRowBytes + (i & 15) * 16);
       rows.live = false;
     }
+    const int c_first = a.alt ? 0 : 32 * half, c_step = a.alt ? 32 : 64;
     int local = 0;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t);
+      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
       const int buf = local & 1;
+      if (a.alt) {  // (an empty sum takes no accumulator: the second half leaves it to the first)
+        if (sum) ++local;
+        if (half != (sum ? buf : 0)) continue;
+      }
       const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
       // what the tile needs besides its sums is fetched before they are waited for
       const bool by_rows = EPI != MM_EPI_STATS && a.rows_out;
@@ -719,11 +770,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const void* add = e.accumulate ? e.out : e.residual;
       const int64_t add_ld = e.accumulate ? e.ld : e.ldr;
       const int piece = l0 + (threadIdx.x & 15) * 8;
-      const int64_t first_row = o.c0 + 32 * half + rows.row;
+      const int64_t first_row = o.c0 + c_first + rows.row;
       int64_t add_at = (e.accumulate ? group_out : 0) + first_row * add_ld + piece;
       uint4 next[4];
       rows.live = piece < p.lanes;
-      if (by_rows && add) rows.load(add, add_at, add_ld, o.n - 32 * half, next);
+      if (by_rows && add && part == 0) rows.load(add, add_at, add_ld, o.n - c_first, next);
       // lanes of the fragments (four per thread) or the thread's own lane
       float lse[4], gw[4], bias[4];
       int lab[4];
@@ -747,15 +798,37 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       float m = -INFINITY, total = 0.f;
       bool ok = true;
       if (sum) {
-        ok = mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5);
+        ok = mbar_wait(acc_full + buf, ((a.alt ? local - 1 : local) >> 1) & 1, abort_flag, p.err, 5);
         __syncwarp();
         tc_fence_after();
-        ++local;
+        if (!a.alt) ++local;
       }
-      // (all warps of the epilogue leave together: what follows has barriers)
-      if (!named_bar_all(1, 32 * kEpiWarps, ok)) break;
+      // (the warps that share barriers in what follows leave together)
+      ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
+      if (CG == 1 && a.split > 1) {
+        // the CTAs of a cluster have each summed a share of the reduction: the others hand theirs to the first one's
+        // shared memory, which adds them in order
+        if (part > 0 && ok) {
+          for (int c = c_first; c < o.n; c += c_step) {
+            float v[32];
+            if (sum) {
+              tmem_ld32(taddr + c, v);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+            const uint32_t to = mapa(su32(parts + ((part - 1) * a.bn + c) * kPartLd + 32 * quad + lane), 0);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + j * kPartLd * 4), "f"(v[j]) : "memory");
+          }
+        }
+        cluster_sync();
+        if (part > 0) break;
+      }
+      if (!ok) break;
       if (by_rows) {
-        for (int c = 32 * half; c < o.n; c += 64) {
+        for (int c = c_first; c < o.n; c += c_step) {
           Frag f;
           if (sum) {
             tmem_ld_frag(taddr + c, f);
@@ -765,9 +838,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 #pragma unroll
               for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
           }
-          const int64_t row_at = first_row + (c - 32 * half);
+          if (CG == 1) {
+            for (int k = 1; k < a.split; ++k) {
+              const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
+                  f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
+                }
+            }
+          }
+          const int64_t row_at = first_row + (c - c_first);
           if (EPI == MM_EPI_SOFTGRAD) {
-            const int c_first = o.c0 + c + 2 * (lane & 3);
+            const int word = o.c0 + c + 2 * (lane & 3);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -775,7 +860,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                   // (a row without gradient stays zero even where its logits are not finite)
-                  const float d = (__expf(f.v[j][r][q] - lse[r]) - (c_first + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
+                  const float d = (__expf(f.v[j][r][q] - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
                   f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
                 }
           } else {
@@ -817,8 +902,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             if (add) {
               rows.stage(next);
               named_bar(2 + half, 128);
-              add_at += 64 * add_ld;
-              if (c + 64 < o.n) rows.load(add, add_at, add_ld, o.n - c - 64, next);
+              add_at += c_step * add_ld;
+              if (c + c_step < o.n) rows.load(add, add_at, add_ld, o.n - c - c_step, next);
               frag_add(stage, quad, lane, f, p.f16);  // (each warp rereads and overwrites its own quarter only)
               __syncwarp();
             }
@@ -831,13 +916,20 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       } else {
         const int l = l0 + 32 * quad + lane;
         const bool live = l < p.lanes;
-        for (int c = 32 * half; c < o.n; c += 64) {
+        for (int c = c_first; c < o.n; c += c_step) {
           float v[32];
           if (sum) {
             tmem_ld32(taddr + c, v);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = 0.f;
+          }
+          if (CG == 1) {
+            for (int k = 1; k < a.split; ++k) {
+              const float* q = parts + ((k - 1) * a.bn + c) * kPartLd + 32 * quad + lane;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += q[j * kPartLd];
+            }
           }
           const int nv = min(32, o.n - c);
           if (EPI == MM_EPI_STORE) {
@@ -887,6 +979,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
   }
   __syncwarp();
+  if (CG == 1 && a.split > 1 && first < tiles && (warp < 4 || warp >= kFirstLoader)) cluster_sync();
   if (*abort_flag) {  // after a timeout: let the copies and MMAs in flight finish (about a millisecond)
     const long long t0 = clock64();
     while (clock64() - t0 < 2000000ll) {
@@ -921,8 +1014,8 @@ bool tma_ready(const MmOperand& o) {
   return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 36 && o.group_stride < (int64_t)1 << 36;
 }
 
-int smem_bytes(int cg, int bn, int stages, const MmProblem& p) {
-  return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + 2 * kOutBytes + ctrl_bytes(p.rag, p.groups);
+int smem_bytes(int cg, int bn, int stages, int split, const MmProblem& p) {
+  return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + 2 * kOutBytes + (split - 1) * bn * kPartLd * 4 + ctrl_bytes(p.rag, p.groups);
 }
 
 template <int CG, int EPI, bool GEN>
@@ -930,15 +1023,17 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(GEN ? kThreads + 32 * kLoaders : kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.p);
+  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.split, a.p);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG == 2 ? 2 : a.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
+  cfg.numAttrs = CG == 2 || a.split > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, mm_tc_kernel<CG, EPI, GEN>, ta, tb, a);
 }
 
@@ -1006,13 +1101,24 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   TcArgs a = {};
   a.p = p;
   const bool gen = p.red <= 0 || !tma_ready(p.a) || !tma_ready(p.b);
+  // Few tiles: the reduction of a tile is split over a cluster of CTAs, as many as keep every SM busy once, with four
+  // stages each at least.
+  a.split = 1;
+  const int64_t lanes128 = (p.lanes + BM - 1) / BM;
+  const int blocks = (p.red + BK - 1) / BK;
+  const int64_t few = lanes128 * std::min(p.groups, p.cols);  // tiles, where each group has one column tile
+  const int split_bn = p.cols <= 32 && p.b.red_major ? 32 : 64;
+  if (p.rag != MM_RAG_RED && p.epi == MM_EPI_STORE && p.cols <= 64 && 2 * few <= sms)
+    a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 4, split_bn == 32 ? 8 : 4}));
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
-  const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 ? 2 : 1;
+  const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
   const int units = cg == 2 ? pairs : sms;
   a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
-  if (p.rag == MM_RAG_COLS) {
+  if (a.split > 1) {
+    a.bn = split_bn;  // one column tile
+  } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
     // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
     const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
@@ -1034,7 +1140,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     }
   }
   a.stages = 1;
-  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, p) <= kSmemMax) ++a.stages;
+  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.split, p) <= kSmemMax) ++a.stages;
   a.b_box = p.rag == MM_RAG_COLS || a.bn / cg % 64 ? 32 : 64;  // divides what a CTA stages
   a.col_tiles = (p.cols + a.bn - 1) / a.bn;
   const int64_t tiles = a.lane_tiles * (int64_t)(p.rag == MM_RAG_COLS ? a.col_tiles + p.groups : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
@@ -1052,6 +1158,14 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? p.lanes : red, groups, p.a.red_major ? BM : BK) &&
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK);
     if (!ok) return cudaErrorInvalidValue;
+  }
+  // a tile with few stages spends more on its epilogue: the halves take whole tiles in turn there (the last tile's
+  // epilogue takes twice as long, which many tiles hide)
+  const int64_t red = p.rag == MM_RAG_RED ? p.red / p.groups : p.red;
+  a.alt = p.epi != MM_EPI_STATS && a.split == 1 && red <= 512 && tiles >= 8 * units;
+  if (a.split > 1) {
+    const int64_t most = a.lane_tiles * (p.rag == MM_RAG_COLS ? (int64_t)std::min(p.groups, p.cols) : a.col_tiles);
+    return gen ? launch_epi<1, true>(ta, tb, a, (int)most * a.split, s) : launch_epi<1, false>(ta, tb, a, (int)most * a.split, s);
   }
   const int grid = cg * (int)std::max<int64_t>(1, std::min<int64_t>(units, tiles + (tiles - (p.rag == MM_DENSE ? a.tail_from : tiles)) * ((1 << a.tail_lg) - 1)));
   if (gen) return launch_epi<1, true>(ta, tb, a, grid, s);

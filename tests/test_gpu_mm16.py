@@ -464,3 +464,51 @@ def test_pointers_that_are_not_this_devices_memory_are_refused():
         with pytest.raises(api.Ds4MoeError) as ei:
             api.ds4moe_linear(x, bad, None, None, x, 4, 8, 8, stream=stream())
         assert ei.value.code == api.DS4MOE_ERR_INVALID_ARG and "w is not device memory" in str(ei.value)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,n,k,pad", [(1, 4096, 4096, 0), (3, 256, 2048, 0), (32, 384, 1096, 8), (33, 200, 4104, 0),
+                                          (64, 1000, 520, 0), (7, 130, 1001, 0), (64, 513, 2001, 0)])
+def test_few_rows_split_over_the_reduction(dtype, rows, n, k, pad):
+    """Few tiles share out the reduction among the CTAs of a cluster; whole numbers stay exact."""
+    x, w, b, r = whole((rows, k), dtype, 1), whole((n, k), dtype, 2), whole((n,), dtype, 3), whole((rows, n), dtype, 4)
+    y, z = torch.empty((rows, n), dtype=x.dtype, device="cuda"), torch.empty((rows, n), dtype=x.dtype, device="cuda")
+    api.ds4moe_linear(strided(x, k + pad)[0], strided(w, k + pad)[0], b, r, y, rows, n, k, "relu", dtype, z, ldx=k + pad, ldw=k + pad, stream=stream())
+    ref = x.double() @ w.double().T + b.double()
+    assert torch.equal(z, ref.to(x.dtype))
+    assert torch.equal(y, (ref.clamp(min=0) + r.double()).to(x.dtype))
+    counts = [0, rows // 2, 0, rows - rows // 2]
+    wg = whole((4, n, k), dtype, 5)
+    api.ds4moe_grouped_mm(x, wg, offsets(counts), y, rows, n, k, 4, dtype, stream=stream())
+    want = torch.cat([x[lo:hi].double() @ wg[g].double().T for g, lo, hi in groups_of(counts)])
+    assert torch.equal(y, want.to(x.dtype))
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("counts,n,k", [([128] * 40, 1024, 1024), ([5, 0, 64, 200, 0, 33] * 12, 520, 1304), ([700] * 9, 2048, 640)])
+def test_many_small_weight_gradients(counts, n, k):
+    """Enough output tiles that the two halves of the epilogue take whole tiles in turn, empty groups among them."""
+    rows, g = sum(counts), len(counts)
+    x, dy = whole((rows, k), "bf16", 1), whole((rows, n), "bf16", 2)
+    for out_dtype in ("bf16", "fp32"):
+        dw = torch.full((g, n, k), 7.0, dtype=DT[out_dtype], device="cuda")
+        api.ds4moe_grouped_mm_dw(dy, x, offsets(counts), dw, rows, n, k, g, "bf16", out_dtype, stream=stream())
+        for e, lo, hi in groups_of(counts):
+            assert torch.equal(dw[e], (dy[lo:hi].double().T @ x[lo:hi].double()).to(DT[out_dtype])), e
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,n,k", [(1100, 4000, 264), (2500, 2056, 64), (4096, 520, 200)])
+def test_uneven_schedules(rows, n, k):
+    """Sizes whose last round of tiles is partial, so that it is split over its columns."""
+    x, w, dy = whole((rows, k), "bf16", 1), whole((n, k), "bf16", 2), whole((rows, n), "bf16", 3)
+    y = torch.empty((rows, n), dtype=x.dtype, device="cuda")
+    api.ds4moe_linear(x, w, None, None, y, rows, n, k, stream=stream())
+    assert torch.equal(y, (x.double() @ w.double().T).to(x.dtype))
+    dx, dw, db = torch.empty_like(x), torch.empty_like(w), torch.empty(n, dtype=x.dtype, device="cuda")
+    size = api.ds4moe_linear_grad_workspace(rows, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    api.ds4moe_linear_grad(dy, x, w, None, dx, dw, db, rows, n, k, workspace=ws, workspace_bytes=size, stream=stream())
+    assert torch.equal(dx, (dy.double() @ w.double()).to(x.dtype))
+    assert torch.equal(dw, (dy.double().T @ x.double()).to(x.dtype))
+    assert torch.equal(db, dy.double().sum(0).to(x.dtype))
