@@ -117,6 +117,8 @@ constexpr int kMmStatTile = 256;
 
 // Sets kernel attributes on the current device (once per device).
 cudaError_t mm_prepare();
+// An estimate of a dense product's time (columns of a tile times stages of the reduction, by rounds over the SMs).
+int64_t mm_cost(int lanes, int cols, int red, bool b_red);
 // Launches one product. Nothing to do (no lanes or columns) is not an error.
 cudaError_t mm_launch(const MmProblem& p, cudaStream_t s);
 

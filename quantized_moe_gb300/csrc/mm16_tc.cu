@@ -1058,7 +1058,36 @@ cudaError_t prepare_epi() {
   return e;
 }
 
+// The column tile with the shortest schedule: rounds over the SMs times a tile's columns (and what a tile costs
+// whatever its width, about 24 columns' time). Widths that are no multiple of 64 run at the next larger one's rate
+// (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us).
+struct Schedule {
+  int64_t cost;  // columns' time
+  int bn, tail_lg, tail_from;
+};
+Schedule schedule(int64_t lane_tiles, int cols, bool b_red, int groups, int cg, int units) {
+  Schedule best = {INT64_MAX, 256, 0, 0};
+  const int grain = b_red ? 64 : 64 * cg;
+  for (int bn = 256; bn >= grain; bn -= grain) {
+    const int64_t tiles = lane_tiles * ((cols + bn - 1) / bn) * groups;
+    const int64_t tail = tiles % units;
+    // the last, partial round of a dense product: its tiles are split while all parts still fit one round
+    int lg = 0;
+    while (groups == 1 && tail && lg < 2 && (tail << (lg + 1)) <= units && (bn >> (lg + 1)) % grain == 0) ++lg;
+    const int64_t cost = tiles / units * (bn + 24) + (tail ? (bn >> lg) + 24 : 0);
+    if (cost < best.cost) best = {cost, bn, lg, (int)std::min<int64_t>(tiles - tail, INT32_MAX)};
+  }
+  return best;
+}
+
 }  // namespace
+
+int64_t mm_cost(int lanes, int cols, int red, bool b_red) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  const int cg = lanes > BM && g_pairs[dev & 63] > 0 ? 2 : 1, units = std::max(1, cg == 2 ? g_pairs[dev & 63] : g_sms[dev & 63]);
+  return schedule((lanes + BM * cg - 1) / (BM * cg), cols, b_red, 1, cg, units).cost * ((red + BK - 1) / BK + 4);
+}
 
 cudaError_t mm_prepare() {
   if (!g_encode) {
@@ -1106,10 +1135,11 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   a.split = 1;
   const int64_t lanes128 = (p.lanes + BM - 1) / BM;
   const int blocks = (p.red + BK - 1) / BK;
-  const int64_t few = lanes128 * std::min(p.groups, p.cols);  // tiles, where each group has one column tile
   const int split_bn = p.cols <= 32 && p.b.red_major ? 32 : 64;
-  if (p.rag != MM_RAG_RED && p.epi == MM_EPI_STORE && p.cols <= 64 && 2 * few <= sms)
-    a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 4, split_bn == 32 ? 8 : 4}));
+  // tiles of that width (ragged columns: where they all fit one, each group with rows has one)
+  const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
+  if (p.rag != MM_RAG_RED && p.epi == MM_EPI_STORE && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
+    a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / (gen ? 2 : 4), split_bn == 32 ? 8 : 4}));
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
   const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
@@ -1117,27 +1147,15 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
   if (a.split > 1) {
-    a.bn = split_bn;  // one column tile
+    a.bn = split_bn;
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
     // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
     const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
   } else if (p.epi != MM_EPI_STATS) {
-    // the width with the shortest schedule: rounds over the SMs times a tile's columns (and what a tile costs
-    // whatever its width, about 24 columns' time). Widths that are no multiple of 64 run at the next larger one's
-    // rate (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us).
-    int64_t best = INT64_MAX;
-    for (int bn = 256; bn >= 64; bn -= 64) {
-      if (bn % (p.b.red_major ? 64 : 64 * cg)) continue;
-      const int64_t tiles = (int64_t)a.lane_tiles * ((p.cols + bn - 1) / bn) * (p.rag == MM_RAG_RED ? p.groups : 1);
-      const int64_t tail = tiles % units;
-      // the last, partial round: its tiles are split while all parts still fit one round
-      int lg = 0;
-      while (p.rag == MM_DENSE && tail && lg < 2 && (tail << (lg + 1)) <= units && (bn >> (lg + 1)) % (p.b.red_major ? 64 : 64 * cg) == 0) ++lg;
-      const int64_t cost = tiles / units * (bn + 24) + (tail ? (bn >> lg) + 24 : 0);
-      if (cost < best) best = cost, a.bn = bn, a.tail_lg = lg, a.tail_from = (int)std::min<int64_t>(tiles - tail, INT32_MAX);
-    }
+    const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 1, cg, units);
+    a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;
   }
   a.stages = 1;
   while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.split, p) <= kSmemMax) ++a.stages;

@@ -146,16 +146,17 @@ def _check(rc: int) -> None:
 
 
 def _ptr(a) -> Optional[int]:
-    if a is None:
-        return None
+    if a is None or type(a) is int:
+        return a
+    address = getattr(a, "data_ptr", None)
+    if address is not None:
+        return address()
     if isinstance(a, int):
         return a
     if isinstance(a, np.ndarray):
         if not a.flags["C_CONTIGUOUS"]:
             raise ValueError("arrays must be C-contiguous")
         return a.ctypes.data
-    if hasattr(a, "data_ptr"):
-        return a.data_ptr()
     raise TypeError(f"cannot take the address of {type(a)}")
 
 
@@ -249,10 +250,11 @@ def ds4moe_set_test_stall(h: int, stage: int) -> None:
 
 
 def _enum(table: dict, v) -> int:
+    n = table.get(v)
+    if n is not None:
+        return n
     if isinstance(v, str):
-        if v not in table:
-            raise ValueError(f"{v!r} is none of {sorted(table)}")
-        return table[v]
+        raise ValueError(f"{v!r} is none of {sorted(table)}")
     return int(v)
 
 

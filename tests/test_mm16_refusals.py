@@ -59,7 +59,7 @@ INVALID, FORMAT, CAPACITY = api.DS4MOE_ERR_INVALID_ARG, api.DS4MOE_ERR_UNSUPPORT
     (linear, dict(ldz=7), INVALID, "ldz=7"), (linear, dict(k=(1 << 24) + 1), INVALID, "k="),
     (linear_grad, dict(workspace_bytes=15), CAPACITY, "workspace_bytes"), (linear_grad, dict(lddx=7), INVALID, "lddx=7"),
     (linear_grad, dict(act=9), INVALID, "act=9"), (linear_grad, dict(rows=-2), INVALID, "rows=-2"),
-    (loss, dict(vocab=0), INVALID, "vocab=0"), (loss, dict(d=0), INVALID, "d=0"), (loss, dict(workspace_bytes=60), CAPACITY, "workspace_bytes"),
+    (loss, dict(vocab=0), INVALID, "vocab=0"), (loss, dict(d=0), INVALID, "d=0"), (loss, dict(workspace_bytes=47), CAPACITY, "workspace_bytes"),
     (loss, dict(dtype=2), FORMAT, "dtype=2"), (loss_grad, dict(workspace_bytes=2000), CAPACITY, "smallest piece"),
     (loss_grad, dict(lddw=7), INVALID, "lddw=7"), (loss_grad, dict(workspace_bytes=-1), CAPACITY, "workspace_bytes"),
 ])
