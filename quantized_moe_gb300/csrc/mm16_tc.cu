@@ -232,62 +232,68 @@ __device__ __forceinline__ int mma_n(const MmProblem& p, int n) {
   return (n + q - 1) / q * q;
 }
 
-// Eight consecutive elements of a row, any alignment, zeros past `valid`: the aligned 32-bit words that hold them,
-// shifted by an element where the row starts in the middle of a word.
-__device__ __forceinline__ void words_of(const uint16_t* src, int valid, uint32_t (&w)[5]) {
-  const uint32_t odd = (uint32_t)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(src - odd);
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = 2 * i < valid + (int)odd ? __ldg(q + i) : 0u;  // (a word with a wanted element)
-}
-__device__ __forceinline__ uint4 chunk_of(const uint16_t* src, int valid, const uint32_t (&w)[5]) {
-  const uint32_t sh = (reinterpret_cast<uintptr_t>(src) & 2) * 8;
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[i] = __funnelshift_r(w[i], w[i + 1], sh);
-    const int left = valid - 2 * i;
-    if (left < 2) r[i] = left < 1 ? 0u : r[i] & 0xffffu;
+// One operand's stages by ordinary loads, in the layout that the TMA's 128-byte swizzle gives (16-byte chunk index XOR
+// row mod 8). K-major: the rows of 64 elements are lanes or columns and their elements the reduction; MN-major the other
+// way round, in boxes of 64 x 64. A thread owns one 16-byte chunk of every 32nd row, so that neither its chunk nor the
+// parity of its addresses changes: it reads the aligned words that hold its eight elements and, where the row starts in
+// the middle of a word, shifts them by an element. Elements outside the matrix are zeros; their words are not read.
+struct Loader {
+  const uint16_t* src;  // of the thread's chunk in its first row
+  int64_t step;         // elements to the chunk 32 rows on
+  int odd, red_major, row, ch;
+  int mn_left, r_left;  // lanes or columns, and reduction, from the thread's first element to their ends
+  __device__ __forceinline__ void start(const uint16_t* base, int64_t ld, int red, int mn0, int mn_end, int r0, int r_end, int tid) {
+    red_major = red;
+    row = tid >> 3, ch = tid & 7;
+    const int mn = red ? mn0 + row : mn0 + ch * 8, r = red ? r0 + ch * 8 : r0 + row;
+    src = base + (red ? (int64_t)mn * ld + r : (int64_t)r * ld + mn);
+    step = 32 * ld;
+    odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
+    mn_left = mn_end - mn, r_left = r_end - r;
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-// One operand's stage by ordinary loads, in the layout that the TMA's 128-byte swizzle gives (chunk index XOR row mod
-// 8). K-major: the rows of 128 bytes are lanes or columns from mn0 and their elements the reduction from r0; MN-major
-// the other way round, in boxes of 64 x 64. Four chunks a thread are in flight.
-__device__ __forceinline__ void load_stage(uint8_t* dst, const uint16_t* base, int64_t ld, bool red_major, int mn0,
-                                           int mn_end, int r0, int r_end, int mn_count, int tid) {
-  const int chunks = red_major ? mn_count * 8 : mn_count / 64 * 512;
-  for (int i0 = tid; i0 < chunks; i0 += 4 * kLoaders * 32) {
-    const uint16_t* src[4];
-    int valid[4];
-    uint32_t w[4][5];
+  __device__ __forceinline__ int valid(int u) const {
+    if (red_major) return mn_left > 32 * u ? min(8, r_left) : 0;
+    return r_left > 32 * (u & 1) ? min(8, mn_left - 64 * (u >> 1)) : 0;
+  }
+  // 32 u rows of a stage, then on to the next stage
+  __device__ __forceinline__ void stage(uint8_t* dst, int units, int64_t next) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(src - odd);
+    const uint32_t sh = odd * 16;
+    uint8_t* to = dst + row * 128 + ((ch ^ (row & 7)) << 4);
+    for (int u0 = 0; u0 < units; u0 += 4) {
+      uint32_t w[4][5];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * kLoaders * 32, row = i >> 3, ch = i & 7;
-      int64_t at;
-      if (red_major) {
-        valid[u] = i < chunks && mn0 + row < mn_end ? min(8, max(0, r_end - (r0 + ch * 8))) : 0;
-        at = (int64_t)(mn0 + row) * ld + r0 + ch * 8;
-      } else {
-        const int mn = mn0 + (row >> 6) * 64 + ch * 8, r = r0 + (row & 63);
-        valid[u] = i < chunks && r < r_end ? min(8, max(0, mn_end - mn)) : 0;
-        at = (int64_t)r * ld + mn;
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + i, v = u < units ? valid(u) : 0;
+        const uint32_t* qu = q + (red_major ? u * step : (u & 1) * step + 64 * (u >> 1)) / 2;
+        if (v >= 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[i][k] = __ldg(qu + k);
+          w[i][4] = odd ? __ldg(qu + 4) : 0u;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? __ldg(qu + k) : 0u;  // (a word with a wanted element)
+        }
       }
-      src[u] = base + at;
-      if (valid[u] > 0) {
-        words_of(src[u], valid[u], w[u]);
-      } else {
 #pragma unroll
-        for (int k = 0; k < 5; ++k) w[u][k] = 0u;
+      for (int i = 0; i < 4; ++i) {
+        const int u = u0 + i;
+        if (u >= units) break;
+        uint32_t r[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[i][k], w[i][k + 1], sh);
+        const int v = valid(u);
+        if (v < 8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = v - 2 * k < 1 ? 0u : v - 2 * k < 2 ? r[k] & 0xffffu : r[k];
+        }
+        *reinterpret_cast<uint4*>(to + u * 4096) = make_uint4(r[0], r[1], r[2], r[3]);
       }
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + u * kLoaders * 32, row = i >> 3, ch = i & 7;
-      if (i < chunks) *reinterpret_cast<uint4*>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = chunk_of(src[u], valid[u], w[u]);
-    }
+    src += next;
+    r_left -= BK;
   }
-}
+};
 
 // ------------------------------------------------------------------------------------ epilogues
 
@@ -646,16 +652,18 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
-      const uint16_t* pb = static_cast<const uint16_t*>(p.b.p);
       const int nb = mma_n<CG>(p, o.n);
+      Loader la, lb;
+      la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
+      lb.start(static_cast<const uint16_t*>(p.b.p), p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0, o.r0 + o.red, tid);
       for (int k = 0; k < o.red; k += BK) {
         if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
           ok = false;
           break;
         }
         uint8_t* st = smem + s * stage_bytes;
-        load_stage(st, pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0 + k, o.r0 + o.red, BM, tid);
-        load_stage(st + A_BYTES, pb, p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0 + k, o.r0 + o.red, nb, tid);
+        la.stage(st, BM / 32, p.a.red_major ? BK : BK * p.a.ld);
+        lb.stage(st + A_BYTES, (nb + 31) / 32, p.b.red_major ? BK : BK * p.b.ld);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s);
@@ -1139,7 +1147,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   // tiles of that width (ragged columns: where they all fit one, each group with rows has one)
   const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
   if (p.rag != MM_RAG_RED && p.epi == MM_EPI_STORE && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
-    a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / (gen ? 2 : 4), split_bn == 32 ? 8 : 4}));
+    a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
   const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
