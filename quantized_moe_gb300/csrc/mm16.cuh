@@ -112,6 +112,10 @@ __device__ __forceinline__ float mm_act_slope(float z, int act) {
 // a normal fp16 number.
 constexpr float kMmGradOne = 8192.f;
 
+// Whether the TMA unit can address a matrix: 16-byte aligned start and row distances.
+inline bool mm_aligned(const MmOperand& o) {
+  return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 36 && o.group_stride < (int64_t)1 << 36;
+}
 // Words of one softmax partial: part[] has ceil(vocab / kMmStatTile) rows of one entry per token.
 constexpr int kMmStatTile = 256;
 

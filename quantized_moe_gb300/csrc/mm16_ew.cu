@@ -5,7 +5,7 @@
 namespace ds4 {
 namespace {
 
-constexpr int kMaxChunks = 256;
+constexpr int kMaxChunks = 128;
 
 // Programmatic dependent launch, as in the products: a kernel sets itself up while its predecessor runs, and touches
 // global memory only after that is complete.
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ 
   const int r0 = blockIdx.y * chunk_rows, r1 = min(r0 + chunk_rows, rows);
   float sum[8] = {};
   if (c < n) {
-#pragma unroll 2
+#pragma unroll 4
     for (int r = r0 + warp; r < r1; r += 8) {
       float g[8];
       uint16_t hy[8], hz[8];
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* __restric
 }  // namespace
 
 int mm_colsum_chunks(int rows) {
-  const int c = (rows + 15) / 16;
+  const int c = (rows + 31) / 32;
   return c < 1 ? 1 : c > kMaxChunks ? kMaxChunks : c;
 }
 

@@ -306,9 +306,9 @@ extern "C" int ds4moe_cross_entropy(const void* x, const void* w, const int32_t*
     int* err = c.err_word();
     if (!c.ok()) return c.code;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile;
     ds4::MmProblem p = product(x, ldx, true, w, ldw, true, rows, vocab, d, dtype, nullptr, 0, err);
     p.epi = ds4::MM_EPI_STATS;
+    const int tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile;
     p.e.labels = labels, p.e.vocab = vocab, p.e.ignore = ignore_index;
     p.e.part = static_cast<float2*>(workspace);
     p.e.zlab = reinterpret_cast<float*>(static_cast<char*>(workspace) + up(8 * (int64_t)rows * tiles, 16));

@@ -35,6 +35,7 @@ using namespace tc;
 constexpr int BM = 128, BK = 64;          // lanes per CTA; reduction of one stage
 constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
+constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulator where the result is fp32
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -61,7 +62,8 @@ struct TcArgs {
   int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
-  int alt;                    // the epilogue's halves take whole tiles in turn instead of halves of each tile
+  int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
+  int accs;                   // accumulators of one tile that lie side by side in tensor memory (1: two take turns; 2: none is left to)
   int split;                  // CTAs (a cluster) that share a tile's reduction; 1: none
   int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
   Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
@@ -369,7 +371,7 @@ __device__ __forceinline__ void put(const MmProblem& p, int g, int l, int c, int
 }
 
 // The arithmetic of a stored result: 32 columns (nv exist for this lane) of lane l.
-__device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int c, int nv, float (&v)[32]) {
+__device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int c, int nv, bool accumulate, float (&v)[32]) {
   const MmEpiArgs& e = p.e;
   if (l >= p.lanes) nv = 0;
   if (e.acc_in) add32(v, e.acc_in + (int64_t)c * e.acc_ld + l, e.acc_ld, nv);
@@ -399,7 +401,7 @@ __device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int 
     for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], MM_ACT_RELU);
   }
   if (e.residual) add16(v, e.residual, (int64_t)c * e.ldr + l, e.ldr, nv, p.f16);
-  if (e.accumulate) {
+  if (accumulate) {
     const int64_t o = (p.rag == MM_RAG_RED ? g * e.group_stride : 0) + (int64_t)c * e.ld + l;
     if (e.out_f32)
       add32(v, static_cast<const float*>(e.out) + o, e.ld, nv);
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
   const int acc_stride = max(a.bn, 32);
   uint32_t tmem_cols = 32;
-  while (tmem_cols < 2u * acc_stride) tmem_cols *= 2;
+  while (tmem_cols < 2u * max(a.bn, 32)) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, (a.alt ? kEpiWarps / 2 : kEpiWarps) * CG);
+      mbar_init(acc_empty + i, kEpiWarps * CG);
     }
     *abort_flag = 0;
     mbar_init_fence();
@@ -682,13 +684,25 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       for (int t = first; t < tiles && ok; t += step) {
         const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
         if (o.red <= 0 || o.n <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
-        const int buf = local & 1, n = mma_n<CG>(p, o.n);
+        const int n = mma_n<CG>(p, o.n);
         const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
                                (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
-        if (!mbar_wait(acc_empty + buf, ((local >> 1) & 1) ^ 1, abort_flag, p.err, 6)) break;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(buf * acc_stride);
+        uint32_t d = 0;
+        int in_seg = 0;  // reduction already in this accumulator
         for (int k = 0; k < o.red; k += BK) {
+          const int buf = a.accs == 1 ? local & 1 : 0;
+          if (in_seg == 0) {
+            if (a.accs == 1 || k == 0) {
+              if (!mbar_wait(acc_empty + buf, ((a.accs == 1 ? local >> 1 : local) & 1) ^ 1, abort_flag, p.err, 6)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d = tmem + (uint32_t)(buf * acc_stride);
+            } else {
+              d += acc_stride;  // the next accumulator of the same tile
+            }
+          }
           const int left = min(BK, o.red - k);
           if (!mbar_wait(full + s, ph, abort_flag, p.err, 7) ||
               (!GEN && p.rag == MM_RAG_RED && (left & 15) && !mbar_wait(clean + s, cleaned >> s & 1, abort_flag, p.err, 2))) {
@@ -700,16 +714,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           const uint64_t da = a_desc + (uint32_t)(s * stage_bytes >> 4), db = b_desc + (uint32_t)(s * stage_bytes >> 4);
           if (left > 48) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, k | i);
+            for (int i = 0; i < 4; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, in_seg | i);
           } else {
-            for (int i = 0; 16 * i < left; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, k | i);
+            for (int i = 0; 16 * i < left; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, in_seg | i);
           }
           commit<CG>(empty + s);
           if (++s == a.stages) s = 0, ph ^= 1;
+          in_seg += BK;
+          if (in_seg == a.seg || k + BK >= o.red) {
+            if (a.accs == 1 || k + BK >= o.red) {
+              commit<CG>(acc_full + buf);
+              ++local;
+            }
+            in_seg = 0;
+          }
         }
-        if (!ok) break;
-        commit<CG>(acc_full + buf);
-        ++local;
       }
     }
   } else if (warp == 2 && !GEN && p.rag == MM_RAG_RED) {
@@ -759,19 +778,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.smem = stage + (uint32_t)(rows.row * kRowBytes + (i & 15) * 16);
       rows.live = false;
     }
-    const int c_first = a.alt ? 0 : 32 * half, c_step = a.alt ? 32 : 64;
+    const int c_first = 32 * half, c_step = 64;
     int local = 0;
     for (int t = first; t < tiles; t += step) {
       const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
-      const int buf = local & 1;
-      if (a.alt) {  // (an empty sum takes no accumulator: the second half leaves it to the first)
-        if (sum) ++local;
-        if (half != (sum ? buf : 0)) continue;
-      }
-      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
       // what the tile needs besides its sums is fetched before they are waited for
       const bool by_rows = EPI != MM_EPI_STATS && a.rows_out;
       const int64_t group_out = p.rag == MM_RAG_RED ? o.g * e.group_stride : 0;
@@ -804,12 +817,17 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
       }
       float m = -INFINITY, total = 0.f;
+      constexpr bool kHold = EPI == MM_EPI_STATS && CG == 2;  // sums over accumulators are held in registers
+      float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       bool ok = true;
+      for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
+      const int buf = a.accs == 1 ? local & 1 : 0;
+      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
       if (sum) {
-        ok = mbar_wait(acc_full + buf, ((a.alt ? local - 1 : local) >> 1) & 1, abort_flag, p.err, 5);
+        ok = mbar_wait(acc_full + buf, (a.accs == 1 ? local >> 1 : local) & 1, abort_flag, p.err, 5);
         __syncwarp();
         tc_fence_after();
-        if (!a.alt) ++local;
+        ++local;
       }
       // (the warps that share barriers in what follows leave together)
       ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
@@ -832,10 +850,38 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         }
         cluster_sync();
-        if (part > 0) break;
+        if (part > 0) ok = false;
       }
       if (!ok) break;
-      if (by_rows) {
+      if (EPI == MM_EPI_STATS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c_first + i * c_step;
+          if (c >= o.n || l0 + 32 * quad >= p.lanes) break;  // (no words, or no tokens)
+          float v[32];
+          float(&y)[32] = kHold ? z[kHold ? i : 0] : v;
+          tmem_ld32(taddr + c, v);
+          if (kHold) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = k ? y[j] + v[j] : v[j];
+            if (k + a.seg < o.red) continue;
+          } else if (a.accs > 1 && o.red > a.seg) {
+            float more[32];
+            tmem_ld32(taddr + acc_stride + c, more);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += more[j];
+          }
+          const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
+          epi_stats(y, nv, m, total);
+          if (at >= 0 && at < nv) {  // (the label of a lane that exists)
+            float own = 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (j == at) own = y[j];
+            e.zlab[l0 + 32 * quad + lane] = own;
+          }
+        }
+      } else if (by_rows) {
         for (int c = c_first; c < o.n; c += c_step) {
           Frag f;
           if (sum) {
@@ -923,7 +969,6 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
       } else {
         const int l = l0 + 32 * quad + lane;
-        const bool live = l < p.lanes;
         for (int c = c_first; c < o.n; c += c_step) {
           float v[32];
           if (sum) {
@@ -941,18 +986,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
           const int nv = min(32, o.n - c);
           if (EPI == MM_EPI_STORE) {
-            epi_store(p, o.g, l, o.c0 + c, nv, v);
+            epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || k, v);
             put(p, o.g, l, o.c0 + c, nv, v);
-          } else if (EPI == MM_EPI_STATS) {
-            epi_stats(v, nv, m, total);
-            const int at = lab[0] - (o.c0 + c);
-            if (live && at >= 0 && at < nv) {
-              float z = 0.f;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (j == at) z = v[j];
-              e.zlab[l] = z;
-            }
           } else {
             const int at = lab[0] - (o.c0 + c);
 #pragma unroll
@@ -971,6 +1006,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             mbar_arrive(acc_empty + buf);
         }
       }
+      }
+      if (!ok) break;
       if (EPI == MM_EPI_STATS) {  // the two halves' partials are joined
         float2* x = reinterpret_cast<float2*>(out_stage) + 32 * quad + lane;
         const int l = l0 + 32 * quad + lane;
@@ -1015,11 +1052,6 @@ bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint6
   return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p),
                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Whether the TMA unit can address a matrix: 16-byte aligned start and row distances.
-bool tma_ready(const MmOperand& o) {
-  return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && o.group_stride % 8 == 0 && o.ld < (int64_t)1 << 36 && o.group_stride < (int64_t)1 << 36;
 }
 
 int smem_bytes(int cg, int bn, int stages, int split, const MmProblem& p) {
@@ -1137,7 +1169,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const int sms = g_sms[dev & 63], pairs = g_pairs[dev & 63];
   TcArgs a = {};
   a.p = p;
-  const bool gen = p.red <= 0 || !tma_ready(p.a) || !tma_ready(p.b);
+  const bool gen = p.red <= 0 || !mm_aligned(p.a) || !mm_aligned(p.b);
   // Few tiles: the reduction of a tile is split over a cluster of CTAs, as many as keep every SM busy once, with four
   // stages each at least.
   a.split = 1;
@@ -1185,10 +1217,18 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK);
     if (!ok) return cudaErrorInvalidValue;
   }
-  // a tile with few stages spends more on its epilogue: the halves take whole tiles in turn there (the last tile's
-  // epilogue takes twice as long, which many tiles hide)
-  const int64_t red = p.rag == MM_RAG_RED ? p.red / p.groups : p.red;
-  a.alt = p.epi != MM_EPI_STATS && a.split == 1 && red <= 512 && tiles >= 8 * units;
+  // The tensor cores' fp32 accumulation cuts instead of rounding: over 256 steps of 16 the sums lose about 1e-5 of their
+  // size towards zero, which a 16-bit result does not show. Results in fp32 take several accumulators, added up with
+  // ordinary additions: weight gradients one for every 512 rows (added to what the tile has stored), losses one for
+  // every 2048 of d (their relative error at d 4096: 9.3e-7 with one accumulator, 4.6e-7 with two; four, 1.6e-7, cost
+  // the 2048-row forward 7 % for their hand-overs, two 1 %). Pairs hold the sums in registers; single CTAs, where
+  // that many registers keep the next launch from starting early (16 rows: 195 us, 174 without), keep both
+  // accumulators, all of tensor memory, until the epilogue has read them: the loads in flight bridge that.
+  a.seg = INT32_MAX / BK * BK;
+  a.accs = 1;
+  if (p.epi == MM_EPI_STATS && cg == 2) a.seg = kSegStats;
+  if (p.epi == MM_EPI_STATS && cg == 1 && p.red > kSegStats) a.seg = (p.red + 2 * BK - 1) / (2 * BK) * BK, a.accs = 2;
+  if (ep.out_f32 && !ep.acc_in && p.rag == MM_RAG_RED) a.seg = kSegStore;
   if (a.split > 1) {
     const int64_t most = a.lane_tiles * (p.rag == MM_RAG_COLS ? (int64_t)std::min(p.groups, p.cols) : a.col_tiles);
     return gen ? launch_epi<1, true>(ta, tb, a, (int)most * a.split, s) : launch_epi<1, false>(ta, tb, a, (int)most * a.split, s);
