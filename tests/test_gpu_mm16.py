@@ -512,3 +512,25 @@ def test_uneven_schedules(rows, n, k):
     assert torch.equal(dx, (dy.double() @ w.double()).to(x.dtype))
     assert torch.equal(dw, (dy.double().T @ x.double()).to(x.dtype))
     assert torch.equal(db, dy.double().sum(0).to(x.dtype))
+
+
+@pytest.mark.parametrize("rows,n,k", [(3100, 1536, 3400), (2600, 4096, 2312)])
+def test_larger_gradients(rows, n, k):
+    """Several rounds of tiles over the SMs, whole numbers exact."""
+    x, w, dy = whole((rows, k), "bf16", 1), whole((n, k), "bf16", 2), whole((rows, n), "bf16", 3)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    size = api.ds4moe_linear_grad_workspace(rows, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    api.ds4moe_linear_grad(dy, x, w, None, dx, dw, None, rows, n, k, workspace=ws, workspace_bytes=size, stream=stream())
+    assert torch.equal(dx, (dy.double() @ w.double()).to(x.dtype))
+    assert torch.equal(dw, (dy.double().T @ x.double()).to(x.dtype))
+    assert api.ds4moe_ops_status() == 0
+
+
+def test_larger_cross_entropy_gradients_in_pieces():
+    rows, vocab, d = 2100, 5000, 2304
+    x, w = normal((rows, d), "bf16", 1), normal((vocab, d), "bf16", 2, d ** -0.5)
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    dloss = torch.full((rows,), 1.0 / rows, device="cuda")
+    small = 16 + 4 * rows * d + 2 * ((rows + 7) // 8 * 8) * 2048  # several pieces
+    _ce_check(x, w, labels, dloss, "bf16", _ce(x, w, labels, dloss, "bf16", ws_bytes=small))
