@@ -247,9 +247,10 @@ void ds4moe_destroy(ds4moe_handle* h);
  * weights are kept in bf16 or fp16, and in its training. They need no handle: every operand,
  * result and scratch buffer is the caller's device memory on the calling thread's current device
  * (DS4MOE_ERR_INVALID_ARG for host memory, DS4MOE_ERR_DEVICE_MISMATCH for another GPU's), they
- * allocate nothing, launch asynchronously on `stream`, can be captured in a CUDA graph, and may
- * run on several streams at once as long as these do not share a workspace. Repeated calls are
- * bitwise identical (fixed summation order, no float atomics).
+ * allocate nothing, launch asynchronously on `stream`, can be captured in a CUDA graph (the first
+ * call of any of them on a device sets its kernels up: make it before a capture), and may run on
+ * several streams at once as long as these do not share a workspace. Repeated calls are bitwise
+ * identical (fixed summation order, no float atomics).
  *
  * Matrices are row-major; `ld...` is the distance in elements from one row to the next (at least
  * the row's width; 0 means the width itself). Rows need only their element's alignment; operands
@@ -327,7 +328,9 @@ int ds4moe_cross_entropy_grad(const void* x, const void* w, const int32_t* label
 /* Device-side conditions of the 16-bit operators on the current device since the last call of this
  * function: synchronises the device, copies the flags to the host word and clears them. bit 0: a label
  * outside the vocabulary; bit 2: a pipeline wait gave up after its time limit (about one second) and the
- * results of that call are incomplete, one of bits 17..23 names the wait. */
+ * results of that call are incomplete. One of bits 17..23 names the wait: 17 loads (stage free), 18 the
+ * clearing of a ragged end (stage loaded), 21 epilogue (accumulator full), 22 MMA (accumulator free), 23 MMA
+ * (stage loaded). */
 int ds4moe_ops_status(int32_t* flags);
 
 /* Message of the last failed call on this thread ("" if none). */

@@ -71,13 +71,8 @@ struct MmProblem {
   int* err;            // error word (bit 2 and a site bit: a pipeline wait gave up)
 };
 
-// Group g's range of the ragged index, clamped so that no offset reaches outside [0, total].
-__device__ __forceinline__ int2 mm_range(const int* offsets, int g, int total) {
-  const int lo = min(max(__ldg(offsets + g), 0), total);
-  const int hi = min(max(__ldg(offsets + g + 1), lo), total);
-  return make_int2(lo, hi);
-}
-
+// Loads of what earlier launches wrote are plain ones throughout, never through the non-coherent path: a launch may
+// start before those are complete (programmatic dependent launch) and must not meet lines cached before.
 __device__ __forceinline__ float ld16(const void* p, int64_t i, int f16) {
   return f16 ? __half2float(static_cast<const __half*>(p)[i]) : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
@@ -97,7 +92,7 @@ __device__ __forceinline__ float mm_act(float z, int act) {
 __device__ __forceinline__ float mm_act_slope(float z, int act) {
   if (act == MM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   if (act == MM_ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
     return s * (1.f + z * (1.f - s));
   }
   if (act == MM_ACT_GELU)

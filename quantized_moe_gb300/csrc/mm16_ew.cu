@@ -31,11 +31,11 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s,
 // sums are added in order through shared memory, one partial per column and chunk. The second kernel adds the chunks
 // in order, 8 rows of threads per column. The order of every sum is fixed. HBM bound: dy, z and dz cross it once
 // (elements that cannot be moved 8 at a time go one by one).
-template <bool VEC>
-__global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ dy, int64_t lddy,
-                                                       const void* __restrict__ z, int64_t ldz, void* __restrict__ dz,
-                                                       int64_t lddz, float* __restrict__ part, int rows, int n,
-                                                       int act, int f16, int chunk_rows) {
+template <bool VEC, int ACT>
+__global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t lddy,
+                                                       const void* z, int64_t ldz, void* dz,
+                                                       int64_t lddz, float* part, int rows, int n,
+                                                       int f16, int chunk_rows) {
   __shared__ float s[8][256 + 8];
   begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -43,39 +43,45 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ 
   const int r0 = blockIdx.y * chunk_rows, r1 = min(r0 + chunk_rows, rows);
   float sum[8] = {};
   if (c < n) {
-#pragma unroll 4
-    for (int r = r0 + warp; r < r1; r += 8) {
-      float g[8];
-      uint16_t hy[8], hz[8];
-      const uint16_t* py = static_cast<const uint16_t*>(dy) + (int64_t)r * lddy + c;
-      const uint16_t* pz = static_cast<const uint16_t*>(z) + (int64_t)r * ldz + c;
-      if (VEC) {
-        *reinterpret_cast<uint4*>(hy) = *reinterpret_cast<const uint4*>(py);
-        if (act != MM_ACT_NONE) *reinterpret_cast<uint4*>(hz) = *reinterpret_cast<const uint4*>(pz);
-      } else {
+    for (int r = r0 + warp; r < r1; r += 16) {  // two rows in flight
+      uint16_t hy[2][8], hz[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          hy[i] = c + i < n ? py[i] : (uint16_t)0;
-          if (act != MM_ACT_NONE) hz[i] = c + i < n ? pz[i] : (uint16_t)0;
+      for (int k = 0; k < 2; ++k) {
+        const int rk = r + 8 * k;
+        const uint16_t* py = static_cast<const uint16_t*>(dy) + (int64_t)rk * lddy + c;
+        const uint16_t* pz = static_cast<const uint16_t*>(z) + (int64_t)rk * ldz + c;
+        if (VEC) {
+          *reinterpret_cast<uint4*>(hy[k]) = rk < r1 ? *reinterpret_cast<const uint4*>(py) : make_uint4(0, 0, 0, 0);
+          if (ACT != MM_ACT_NONE) *reinterpret_cast<uint4*>(hz[k]) = rk < r1 ? *reinterpret_cast<const uint4*>(pz) : make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            hy[k][i] = rk < r1 && c + i < n ? py[i] : (uint16_t)0;
+            if (ACT != MM_ACT_NONE) hz[k][i] = rk < r1 && c + i < n ? pz[i] : (uint16_t)0;
+          }
         }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] = ld16(hy, i, f16);
-        if (act != MM_ACT_NONE) g[i] *= mm_act_slope(ld16(hz, i, f16), act);
-        sum[i] += g[i];
-      }
-      if (dz) {
-        uint16_t* pd = static_cast<uint16_t*>(dz) + (int64_t)r * lddz + c;
+      for (int k = 0; k < 2; ++k) {
+        const int rk = r + 8 * k;
+        if (rk >= r1) break;
         uint16_t h[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) st16(h, i, g[i], f16);
-        if (VEC) {
-          *reinterpret_cast<uint4*>(pd) = *reinterpret_cast<const uint4*>(h);
-        } else {
+        for (int i = 0; i < 8; ++i) {
+          float g = ld16(hy[k], i, f16);
+          if (ACT != MM_ACT_NONE) g *= mm_act_slope(ld16(hz[k], i, f16), ACT);
+          sum[i] += g;
+          st16(h, i, g, f16);
+        }
+        if (dz) {
+          uint16_t* pd = static_cast<uint16_t*>(dz) + (int64_t)rk * lddz + c;
+          if (VEC) {
+            *reinterpret_cast<uint4*>(pd) = *reinterpret_cast<const uint4*>(h);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < n) pd[i] = h[i];
+            for (int i = 0; i < 8; ++i)
+              if (c + i < n) pd[i] = h[i];
+          }
         }
       }
     }
@@ -93,8 +99,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* __restrict__ 
   }
 }
 
-__global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restrict__ part, int chunks, int n,
-                                                          void* __restrict__ db, int f16) {
+__global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int chunks, int n,
+                                                          void* db, int f16) {
   __shared__ float s[8][32];
   begin();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -116,11 +122,11 @@ __global__ void __launch_bounds__(256) colsum_join_kernel(const float* __restric
 
 // One warp per token: the tiles' (max, sum) are joined as (M, S) with M = max m_i and
 // S = sum s_i exp(m_i - M); lse = M + log S.
-__global__ void __launch_bounds__(256) softmax_join_kernel(const float2* __restrict__ part, int tiles,
-                                                           const float* __restrict__ zlab,
-                                                           const int* __restrict__ labels, int ignore, int vocab,
-                                                           int rows, float* __restrict__ loss,
-                                                           float* __restrict__ lse, int* err) {
+__global__ void __launch_bounds__(256) softmax_join_kernel(const float2* part, int tiles,
+                                                           const float* zlab,
+                                                           const int* labels, int ignore, int vocab,
+                                                           int rows, float* loss,
+                                                           float* lse, int* err) {
   begin();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= rows) return;
@@ -143,8 +149,8 @@ __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* __restr
   }
 }
 
-__global__ void __launch_bounds__(1024) grad_scale_kernel(const float* __restrict__ g, const int* __restrict__ labels,
-                                                          int ignore, int vocab, int rows, float* __restrict__ gs) {
+__global__ void __launch_bounds__(1024) grad_scale_kernel(const float* g, const int* labels,
+                                                          int ignore, int vocab, int rows, float* gs) {
   __shared__ float s[32];
   begin();
   float m = 0.f;
@@ -178,8 +184,14 @@ cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz
   const auto vec = [](const void* p, int64_t ld) { return !p || ((uintptr_t)p % 16 == 0 && ld % 8 == 0); };
   const dim3 grid((n + 255) / 256, chunks);
   const bool wide = n % 8 == 0 && vec(dy, lddy) && (act == MM_ACT_NONE || vec(z, ldz)) && vec(dz, lddz);
-  cudaError_t e = launch(wide ? act_grad_kernel<true> : act_grad_kernel<false>, grid, 256, s, dy, lddy, z, ldz, dz, lddz, part, rows, n,
-                         act, f16, chunk_rows);
+  const auto run = [&](auto kernel) { return launch(kernel, grid, 256, s, dy, lddy, z, ldz, dz, lddz, part, rows, n, f16, chunk_rows); };
+  cudaError_t e;
+  switch (act) {  // (one kernel for each: all activations in one overflow the instruction cache, 4096 x 2048 silu 27 us instead of 12)
+    case MM_ACT_RELU: e = run(wide ? act_grad_kernel<true, MM_ACT_RELU> : act_grad_kernel<false, MM_ACT_RELU>); break;
+    case MM_ACT_SILU: e = run(wide ? act_grad_kernel<true, MM_ACT_SILU> : act_grad_kernel<false, MM_ACT_SILU>); break;
+    case MM_ACT_GELU: e = run(wide ? act_grad_kernel<true, MM_ACT_GELU> : act_grad_kernel<false, MM_ACT_GELU>); break;
+    default: e = run(wide ? act_grad_kernel<true, MM_ACT_NONE> : act_grad_kernel<false, MM_ACT_NONE>);
+  }
   if (e == cudaSuccess && part) e = launch(colsum_join_kernel, dim3((n + 31) / 32), 256, s, part, chunks, n, db, f16);
   return e;
 }

@@ -74,7 +74,10 @@ struct Check {
     if (at.device != dev && at.type == cudaMemoryTypeDevice) fail(DS4MOE_ERR_DEVICE_MISMATCH, std::string(name) + " lives on another device than the current one");
   }
   int cuda(cudaError_t e) {
-    if (e != cudaSuccess) fail(DS4MOE_ERR_CUDA, cudaGetErrorString(e));
+    if (e != cudaSuccess) {
+      cudaGetLastError();  // reported here, not at the caller's next check
+      fail(DS4MOE_ERR_CUDA, cudaGetErrorString(e));
+    }
     return code;
   }
   // The current device's error word.

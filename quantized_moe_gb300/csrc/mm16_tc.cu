@@ -270,11 +270,11 @@ struct Loader {
         const uint32_t* qu = q + (red_major ? u * step : (u & 1) * step + 64 * (u >> 1)) / 2;
         if (v >= 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[i][k] = __ldg(qu + k);
-          w[i][4] = odd ? __ldg(qu + 4) : 0u;
+          for (int k = 0; k < 4; ++k) w[i][k] = *(qu + k);
+          w[i][4] = odd ? *(qu + 4) : 0u;
         } else {
 #pragma unroll
-          for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? __ldg(qu + k) : 0u;  // (a word with a wanted element)
+          for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? *(qu + k) : 0u;  // (a word with a wanted element)
         }
       }
 #pragma unroll
@@ -376,7 +376,7 @@ __device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int 
   if (l >= p.lanes) nv = 0;
   if (e.acc_in) add32(v, e.acc_in + (int64_t)c * e.acc_ld + l, e.acc_ld, nv);
   if (e.scale) {
-    const float s = __ldg(e.scale);
+    const float s = *e.scale;
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= s;
   }
@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   let_next_start();
   if (p.rag != MM_DENSE) {
     const int total = p.rag == MM_RAG_COLS ? p.cols : p.red;
-    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) lo_of[g] = min(max(__ldg(p.offsets + g), 0), total);
+    for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) lo_of[g] = min(max(*(p.offsets + g), 0), total);
     __syncthreads();
     if (p.rag == MM_RAG_COLS && warp == 2) {
       int run = 0;
@@ -807,11 +807,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (EPI == MM_EPI_STORE) {
           if (e.bias) bias[r] = ld16(e.bias, l, p.f16);
         } else {
-          lab[r] = __ldg(e.labels + l);
+          lab[r] = *(e.labels + l);
           if (EPI == MM_EPI_SOFTGRAD) {
             const bool skip = lab[r] == e.ignore || lab[r] < 0 || lab[r] >= e.vocab;
-            lse[r] = __ldg(e.lse + l);
-            gw[r] = skip ? 0.f : __ldg(e.g + l) / __ldg(e.gscale) * kMmGradOne;
+            lse[r] = *(e.lse + l);
+            gw[r] = skip ? 0.f : *(e.g + l) / *e.gscale * kMmGradOne;
             lab[r] = skip ? -1 : lab[r] - e.word0;
           }
         }
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
                 }
           } else {
             if (e.scale) {
-              const float sc = __ldg(e.scale);
+              const float sc = *e.scale;
 #pragma unroll
               for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -534,3 +534,69 @@ def test_larger_cross_entropy_gradients_in_pieces():
     dloss = torch.full((rows,), 1.0 / rows, device="cuda")
     small = 16 + 4 * rows * d + 2 * ((rows + 7) // 8 * 8) * 2048  # several pieces
     _ce_check(x, w, labels, dloss, "bf16", _ce(x, w, labels, dloss, "bf16", ws_bytes=small))
+
+
+def test_offsets_past_32_bits():
+    """Rows and matrices that lie further apart than 2^31 elements."""
+    rows, n, k, ld = 2200, 72, 64, 1 << 20
+    x = whole((rows, k), "bf16", 1)
+    far = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
+    far.view(rows, ld)[:, :k] = x
+    w = whole((2, n, k), "bf16", 2)
+    counts = [1000, rows - 1000]
+    out = torch.empty(rows * ld, dtype=torch.bfloat16, device="cuda")
+    want = torch.cat([x[lo:hi].double() @ w[g].double().T for g, lo, hi in groups_of(counts)]).to(x.dtype)
+    for skew in (0, 1):  # by the TMA unit, and by ordinary loads and stores
+        src = far if skew == 0 else torch.cat([far[:skew], far])[:rows * ld]
+        api.ds4moe_grouped_mm(src.data_ptr() + 2 * skew, w, offsets(counts), out.data_ptr() + 2 * skew, rows - skew, n, k, 2, ldx=ld, ldy=ld, stream=stream())
+        got = out[skew:skew + (rows - skew - 1) * ld + n].as_strided((rows - skew, n), (ld, 1))
+        assert torch.equal(got, want[:rows - skew])
+    del far, out
+    stride = (1 << 31) + 64
+    wide = torch.empty(stride + n * k, dtype=torch.bfloat16, device="cuda")
+    wide[:n * k], wide[stride:] = w[0].flatten(), w[1].flatten()
+    y = torch.empty((rows, n), dtype=x.dtype, device="cuda")
+    api.ds4moe_grouped_mm(x, wide, offsets(counts), y, rows, n, k, 2, w_stride=stride, stream=stream())
+    assert torch.equal(y, want)
+    dw = torch.empty(stride + n * k, dtype=torch.bfloat16, device="cuda")
+    api.ds4moe_grouped_mm_dw(y, x, offsets(counts), dw, rows, n, k, 2, dw_stride=stride, stream=stream())
+    for g, lo, hi in groups_of(counts):
+        assert torch.equal(dw[g * stride:g * stride + n * k].view(n, k), (y[lo:hi].double().T @ x[lo:hi].double()).to(x.dtype))
+
+
+@pytest.mark.parametrize("direction", ["y", "dw"])
+def test_a_thousand_groups(direction):
+    g, n, k = 1024, 40, 72
+    counts = torch.randint(0, 4, (g,), generator=torch.Generator().manual_seed(1)).tolist()
+    rows = sum(counts)
+    x, dy, w = whole((rows, k), "fp16", 1), whole((rows, n), "fp16", 2), whole((g, n, k), "fp16", 3)
+    if direction == "y":
+        y = torch.empty((rows, n), dtype=x.dtype, device="cuda")
+        api.ds4moe_grouped_mm(x, w, offsets(counts), y, rows, n, k, g, "fp16", stream=stream())
+        of = torch.repeat_interleave(torch.arange(g), torch.tensor(counts)).cuda()
+        assert torch.equal(y, torch.einsum("tk,tnk->tn", x.double(), w[of].double()).to(x.dtype))
+    else:
+        dw = torch.empty_like(w)
+        api.ds4moe_grouped_mm_dw(dy, x, offsets(counts), dw, rows, n, k, g, "fp16", stream=stream())
+        want = torch.stack([dy[lo:hi].double().T @ x[lo:hi].double() for _, lo, hi in groups_of(counts)])
+        assert torch.equal(dw, want.to(x.dtype))
+
+
+def test_cross_entropy_of_no_rows():
+    dw = torch.ones((30, 16), dtype=torch.bfloat16, device="cuda")
+    api.ds4moe_cross_entropy_grad(None, None, None, None, None, None, dw, 0, 30, 16, stream=stream())
+    assert not bool(dw.any())
+
+
+def test_a_chain_of_calls_sees_each_others_results():
+    """Launches may overlap their set-up; every one still reads what the one before it wrote, in place too."""
+    rows, n = 96, 256
+    w = (torch.eye(n, device="cuda") * 2).to(torch.bfloat16)
+    a, b = whole((rows, n), "bf16", 1), torch.zeros((rows, n), dtype=torch.bfloat16, device="cuda")
+    want = a.clone()
+    for _ in range(8):
+        api.ds4moe_linear(a, w, None, None, b, rows, n, n, stream=stream())  # b = 2 a
+        api.ds4moe_linear(b, w, None, a, a, rows, n, n, stream=stream())     # a = 4 a + a
+        want = (want.double() * 5).to(torch.bfloat16)
+    # (5^8 times small whole numbers is rounded on the way, by both alike)
+    assert torch.equal(a, want)
