@@ -60,6 +60,7 @@ struct Divider {
 struct TcArgs {
   MmProblem p;
   int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
+  int a_blocks, b_blocks;     // boxes of 64 x 64 that one copy of an MN-major operand brings
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
   int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
@@ -89,18 +90,18 @@ __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontr
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
 template <int CG>
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int g, uint32_t bar) {
   if (CG == 2)
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3, %4}], [%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5}], [%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(g), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(g), "r"(bar)
         : "memory");
 }
 
@@ -608,13 +609,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int a_boxes = a_red ? 1 : 2;
+    const int a_boxes = a_red ? 1 : 2 / a.a_blocks;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
       if (o.n <= 0) continue;
       const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
-      const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : nb / 64;
-      const int b_box_bytes = b_red ? a.b_box * 128 : 8192;
+      const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
+      const int b_box_bytes = b_red ? a.b_box * 128 : a.b_blocks * 8192;
       const uint32_t bytes = CG * (A_BYTES + b_boxes * b_box_bytes);
       const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
       const int ga = p.rag == MM_RAG_COLS ? o.g : 0;
@@ -630,15 +631,20 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         const int r = o.r0 + k;
         if (lane < a_boxes) {
           if (a_red)
-            tma_load_3d<CG>(su32(st), &ta, r, la, ga, bar);
+            tma_load<CG>(su32(st), &ta, r, la, 0, ga, bar);
+          else if (a.a_blocks > 1)
+            tma_load<CG>(su32(st), &ta, 0, r, la / 64, ga, bar);
           else
-            tma_load_3d<CG>(su32(st + lane * 8192), &ta, la + 64 * lane, r, ga, bar);
+            tma_load<CG>(su32(st + lane * 8192), &ta, la + 64 * lane, r, 0, ga, bar);
         } else if (lane >= 4 && lane < 4 + b_boxes) {
           const int i = lane - 4;
+          const uint32_t to = su32(st + A_BYTES + i * b_box_bytes);
           if (b_red)
-            tma_load_3d<CG>(su32(st + A_BYTES + i * b_box_bytes), &tb, r, cb + i * a.b_box, 0, bar);
+            tma_load<CG>(to, &tb, r, cb + i * a.b_box, 0, 0, bar);
+          else if (a.b_blocks > 1)
+            tma_load<CG>(to, &tb, 0, r, cb / 64 + i * a.b_blocks, 0, bar);
           else
-            tma_load_3d<CG>(su32(st + A_BYTES + i * 8192), &tb, cb + 64 * i, r, 0, bar);
+            tma_load<CG>(to, &tb, cb + 64 * i, r, 0, 0, bar);
         }
         __syncwarp();
         if (++s == a.stages) s = 0, ph ^= 1;
@@ -1043,13 +1049,16 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be resident at once
 
-// 3D map (contiguous index, row, group) with boxes of 64 elements x box_rows rows, 128-byte swizzle.
-bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows) {
-  const cuuint64_t dims[3] = {inner, rows, groups};
-  const cuuint64_t strides[2] = {(cuuint64_t)o.ld * 2, (cuuint64_t)(groups > 1 ? o.group_stride : o.ld) * 2};
-  const cuuint32_t box[3] = {BK, box_rows, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(o.p),
+// 4D map with boxes of 64 contiguous elements, 128-byte swizzle: (contiguous index, row, -, group) with box_rows rows;
+// or, for an MN-major operand whose width is a multiple of 64, (index in a block of 64, row, block, group) with
+// `blocks` blocks of BK rows, which one copy lays one after the other.
+bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows, int blocks) {
+  const cuuint64_t row = (cuuint64_t)o.ld * 2;
+  const cuuint64_t dims[4] = {blocks > 1 ? 64 : inner, rows, blocks > 1 ? inner / 64 : 1, groups};
+  const cuuint64_t strides[3] = {row, blocks > 1 ? 128 : row, groups > 1 ? (cuuint64_t)o.group_stride * 2 : row};
+  const cuuint32_t box[4] = {BK, box_rows, (cuuint32_t)blocks, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(o.p),
                   dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1199,7 +1208,12 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   }
   a.stages = 1;
   while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.split, p) <= kSmemMax) ++a.stages;
-  a.b_box = p.rag == MM_RAG_COLS || a.bn / cg % 64 ? 32 : 64;  // divides what a CTA stages
+  // the rows of a copy divide what a CTA stages; large copies where the columns are not ragged (4096^3 with copies of
+  // 128 rows 81.7 us, of 64 rows 83.8)
+  const int staged = a.bn / cg;
+  a.b_box = p.rag == MM_RAG_COLS || staged % 64 ? 32 : staged % 128 ? 64 : 128;
+  a.a_blocks = !p.a.red_major && p.lanes % 64 == 0 ? 2 : 1;
+  a.b_blocks = !p.b.red_major && p.cols % 64 == 0 && (staged == 256 || staged == 128) ? staged / 64 : 1;
   a.col_tiles = (p.cols + a.bn - 1) / a.bn;
   const int64_t tiles = a.lane_tiles * (int64_t)(p.rag == MM_RAG_COLS ? a.col_tiles + p.groups : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
@@ -1213,8 +1227,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
     const uint64_t red = p.red;
-    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? p.lanes : red, groups, p.a.red_major ? BM : BK) &&
-                    make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK);
+    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? p.lanes : red, groups, p.a.red_major ? BM : BK, a.a_blocks) &&
+                    make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK, a.b_blocks);
     if (!ok) return cudaErrorInvalidValue;
   }
   // The tensor cores' fp32 accumulation cuts instead of rounding: over 256 steps of 16 the sums lose about 1e-5 of their
