@@ -36,6 +36,7 @@ constexpr int BM = 128, BK = 64;          // lanes per CTA; reduction of one sta
 constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulator where the result is fp32
+constexpr int kEpiPlain = 3;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -755,11 +756,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         const int left = min(BK, o.red - k);
         if (left & 15) {
           uint8_t* st = smem + s * stage_bytes;
-          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, rows = 16 - (left & 15);
-          for (int i = lane; i < boxes * rows * 8; i += 32) {
-            const int ch = i & 7, row = left + (i >> 3) % rows, box = (i >> 3) / rows;
-            *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + ch * 16) = make_uint4(0, 0, 0, 0);
-          }
+          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, end = (left + 15) & ~15;
+          for (int box = 0; box < boxes; ++box)
+            for (int row = left + (lane >> 3); row < end; row += 4)
+              *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         }
         __syncwarp();
@@ -770,7 +770,63 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (++s == a.stages) s = 0, ph ^= 1;
       }
     }
-  } else if (warp >= 4 && warp < kFirstLoader) {
+  } else if (EPI == kEpiPlain && warp >= 4 && warp < kFirstLoader) {
+    // ------------------------------------------------------------------ epilogue without anything to add
+    const int quad = warp & 3, half = (warp - 4) >> 2, piece = threadIdx.x & 15, row = (threadIdx.x & 127) >> 4;
+    const uint32_t stage = su32(out_stage) + half * kOutBytes, from = stage + (uint32_t)(row * kRowBytes + piece * 16);
+    const int64_t ld = p.e.ld;
+    int local = 0;
+    for (int t = first; t < tiles; t += step) {
+      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      if (o.n <= 0) continue;
+      const bool sum = o.red > 0;
+      const int buf = local & 1, l = o.l0 + BM * rank + 8 * piece;
+      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      int left = l < p.lanes ? o.n - 32 * half - row : 0;  // rows from the thread's first to the tile's end
+      uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.out) + (p.rag == MM_RAG_RED ? o.g * p.e.group_stride : 0) +
+                                          (o.c0 + 32 * half + row) * ld + l);
+      bool ok = true;
+      if (sum) {
+        ok = mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5);
+        __syncwarp();
+        tc_fence_after();
+        ++local;
+      }
+      if (!named_bar_all(2 + half, 128, ok)) break;  // (the warps that share barriers leave together)
+      for (int c = 32 * half; c < o.n; c += 64) {
+        Frag f;
+        if (sum) {
+          tmem_ld_frag(taddr + c, f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
+        }
+        frag_out(stage, quad, lane, f, p.f16);
+        named_bar(2 + half, 128);
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = lds128(from + 8 * k * kRowBytes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (8 * k < left) q[k * ld] = w[k];  // (8 rows of ld elements are ld pieces)
+        left -= 64;
+        q += 8 * ld;
+        named_bar(2 + half, 128);
+      }
+      if (sum) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {  // the MMA may overwrite this buffer
+          if (CG == 2)
+            mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
+          else
+            mbar_arrive(acc_empty + buf);
+        }
+      }
+    }
+  } else if (EPI != kEpiPlain && warp >= 4 && warp < kFirstLoader) {
     // ------------------------------------------------------------------ epilogue
     // Two warps per lane quadrant take the tile's 32-column chunks in turn; the four warps of a half work on the same
     // chunk.
@@ -1091,8 +1147,12 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   switch (a.p.epi) {
     case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SOFTGRAD: return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
-    default: return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
+    default: break;
   }
+  const MmEpiArgs& e = a.p.e;
+  const bool plain = a.rows_out && a.split == 1 && !e.scale && !e.bias && !e.z && !e.residual && !e.accumulate && e.act == MM_ACT_NONE;
+  if (!GEN && plain) return launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
+  return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
 }
 
 template <int CG, int EPI, bool GEN>
@@ -1153,6 +1213,8 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_epi<1, false>();
   if (e == cudaSuccess) e = prepare_epi<2, false>();
   if (e == cudaSuccess) e = prepare_epi<1, true>();
+  if (e == cudaSuccess) e = prepare_one<1, kEpiPlain, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiPlain, false>();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
