@@ -1,10 +1,10 @@
 // The 16-bit products on the 5th-generation tensor cores: out[c][l] = sum_r A(l, r) B(c, r).
 //
 // Persistent: one CTA (or pair of CTAs) per SM (or two SMs) loops over output tiles of 128 lanes per
-// CTA x up to BN columns. The lanes are the contiguous index of the output, so that a tensor-memory
-// lane is a lane of the output and a warp stores 32 neighbours; the columns are rows of tokens
-// (or of dW), of which a tile takes exactly what its group has, rounded up to the MMA's granule, so
-// that a group's weights cross HBM once however ragged the counts are.
+// CTA x up to 256 columns. The lanes are the contiguous index of the output, so that a tensor-memory
+// lane is a lane of the output; the columns are rows of tokens (or of dW), of which a tile takes
+// exactly what its group has, rounded up to the MMA's granule, so that a group's weights cross HBM
+// once however ragged the counts are.
 //
 // Operands are staged by TMA in 128-byte swizzled sub-tiles of 64 of the reduction, read by the MMA
 // in either order: rows with the reduction contiguous (K-major) or with the lane or column index
@@ -12,11 +12,20 @@
 // MMA spans both SMs' tiles, 256 lanes, and each CTA stages half of the columns, which halves
 // the shared-memory and L2 traffic of the column operand.
 //
-// Warp roles: warp 0 issues the TMA loads (its lanes issue the boxes of a stage in parallel), warp 1
-// owns tensor memory and issues the MMAs (the leader's, in a pair), warps 4-7 run the epilogue of one
-// tile while the next one's main loop fills the other accumulator. Where an operand's address or row
-// distance is not a multiple of 16 bytes, eight loader warps (8-15) read it with ordinary loads and
-// write the same swizzled layout.
+// Warp roles: warp 0 issues the TMA loads (its lanes issue the copies of a stage in parallel); one
+// thread of warp 1 issues the MMAs (the leader's, in a pair); warp 2 clears what a ragged end of the
+// reduction leaves in a stage; warps 4-11 run the epilogue of one tile while the next one's main loop
+// fills the other accumulator. Where an operand's address or row distance is not a multiple of 16
+// bytes, eight loader warps (12-19) read it with ordinary loads and write the same swizzled layout.
+// Few tiles share their reduction out over a cluster of CTAs, which join their sums in shared memory.
+//
+// What bounds it (GB300, measured): the experts' products stream their weights (256 experts, 32768
+// rows, n 2048, k 4096: 0.70-0.72 ms = 6.5-6.8 TB/s, 96-99 % of the copy bandwidth, for y and dx; the
+// weight gradients, 4.3 GB of results, 0.90 ms = 5.2 TB/s, bound by the epilogue's instructions);
+// large dense products the tensor pipe and the SMs' L2 reads (2048 x 129280 x 4096: 1.12 ms = 1.94
+// PFLOP/s, the rate of a large library product; 4096^3 with its epilogue 94 us = 1.46 PFLOP/s, of
+// which a seventh is the last, partial round and the launch); single tokens the launch and one pass of
+// loads (1 x 4096 x 4096: 9.8 us a launch in a graph, against 4.9 us of HBM time).
 //
 // Every wait is bounded (tc::mbar_wait). On a timeout the CTA raises error bit 2, waits for its copies
 // and MMAs in flight, frees its tensor memory and returns.
@@ -419,26 +428,19 @@ struct Frag {
   float v[4][4][2];  // [block of 8 columns][block of 8 lanes][column parity]
 };
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, Frag& f) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr + ((uint32_t)(16 * h) << 16))
-        : "memory");
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) f.v[j][2 * h + (q >> 1)][q & 1] = __uint_as_float(r[4 * j + q]);
-  }
-  // (the values may be used only after the wait; it is ordered by the dependence below)
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) asm volatile("" : "+f"(f.v[j][r][0]), "+f"(f.v[j][r][1]));
+  for (int i = 0; i < 32; ++i) f.v[(i >> 2) & 3][2 * (i >> 4) + ((i >> 1) & 1)][i & 1] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
   if (f16) {
