@@ -708,8 +708,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
               }
               tc_fence_after();
               d = tmem + (uint32_t)(buf * acc_stride);
-            } else {
-              d += acc_stride;  // the next accumulator of the same tile
+            } else {  // the second accumulator of the same tile
+              if (!mbar_wait(acc_empty + 1, (local & 1) ^ 1, abort_flag, p.err, 6)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d = tmem + acc_stride;
             }
           }
           const int left = min(BK, o.red - k);
@@ -917,23 +922,35 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (part > 0) ok = false;
       }
       if (!ok) break;
+      const bool two = EPI == MM_EPI_STATS && !kHold && a.accs > 1;
+      if (two) {  // fold the first accumulator into the second and hand it back: the next tile's first half needs it soon
+        for (int c = c_first; o.red > a.seg && c < o.n && l0 + 32 * quad < p.lanes; c += c_step) {
+          float v[32], more[32];
+          tmem_ld32(taddr + c, v);
+          tmem_ld32(taddr + acc_stride + c, more);
+          uint32_t w[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] + more[j]);
+          tmem_st32(taddr + acc_stride + c, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+      }
       if (EPI == MM_EPI_STATS) {
+        const uint32_t sums = two && o.red > a.seg ? taddr + acc_stride : taddr;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = c_first + i * c_step;
           if (c >= o.n || l0 + 32 * quad >= p.lanes) break;  // (no words, or no tokens)
           float v[32];
           float(&y)[32] = kHold ? z[kHold ? i : 0] : v;
-          tmem_ld32(taddr + c, v);
+          tmem_ld32(sums + c, v);
           if (kHold) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) y[j] = k ? y[j] + v[j] : v[j];
             if (k + a.seg < o.red) continue;
-          } else if (a.accs > 1 && o.red > a.seg) {
-            float more[32];
-            tmem_ld32(taddr + acc_stride + c, more);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += more[j];
           }
           const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
           epi_stats(y, nv, m, total);
@@ -1067,7 +1084,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (CG == 2)
             mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
           else
-            mbar_arrive(acc_empty + buf);
+            mbar_arrive(acc_empty + (two ? 1 : buf));
         }
       }
       }
@@ -1300,8 +1317,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   // ordinary additions: weight gradients one for every 512 rows (added to what the tile has stored), losses one for
   // every 2048 of d (their relative error at d 4096: 9.3e-7 with one accumulator, 4.6e-7 with two; four, 1.6e-7, cost
   // the 2048-row forward 7 % for their hand-overs, two 1 %). Pairs hold the sums in registers; single CTAs, where
-  // that many registers keep the next launch from starting early (16 rows: 195 us, 174 without), keep both
-  // accumulators, all of tensor memory, until the epilogue has read them: the loads in flight bridge that.
+  // that many registers keep the next launch from starting early (16 rows: 195 us, 174 without), use all of
+  // tensor memory for the two of a tile, and the epilogue folds the first into the second at once and hands it back.
   a.seg = INT32_MAX / BK * BK;
   a.accs = 1;
   if (p.epi == MM_EPI_STATS && cg == 2) a.seg = kSegStats;
