@@ -271,7 +271,8 @@ typedef enum ds4moe_act { DS4MOE_ACT_NONE = 0, DS4MOE_ACT_RELU = 1, DS4MOE_ACT_S
  *                          an empty group. dw_dtype is dtype or DS4MOE_FP32; accumulate != 0 adds to
  *                          what dw holds.
  * The offsets are read on the device: nothing is synchronised. Offsets out of range are clamped to
- * [0, rows] and a group whose end lies before its start is empty. Rows that belong to no group
+ * [0, rows] and a group whose end lies before its start is empty, so that no offsets reach outside the
+ * matrices; which rows are computed for decreasing offsets is otherwise unspecified. Rows that belong to no group
  * (from offsets[n_groups] on) are neither read nor written. */
 int ds4moe_grouped_mm(const void* x, const void* w, const int32_t* offsets, void* y, int32_t rows, int32_t n,
                       int32_t k, int32_t n_groups, int32_t dtype, int64_t ldx, int64_t ldw, int64_t w_stride,

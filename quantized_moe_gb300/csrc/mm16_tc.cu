@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
   }
   tc_fence_before();
-  if (CG == 2) cluster_sync();
+  if (CG == 2 || a.split > 1) cluster_sync();  // every CTA of the cluster runs and has set its barriers up
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (EPI == MM_EPI_STORE) {
           if (e.bias) bias[r] = ld16(e.bias, l, p.f16);
         } else {
-          lab[r] = *(e.labels + l);
+          lab[r] = max(*(e.labels + l), -1);
           if (EPI == MM_EPI_SOFTGRAD) {
             const bool skip = lab[r] == e.ignore || lab[r] < 0 || lab[r] >= e.vocab;
             lse[r] = *(e.lse + l);
@@ -890,20 +890,166 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       bool ok = true;
       for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
-      const int buf = a.accs == 1 ? local & 1 : 0;
-      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
-      if (sum) {
-        ok = mbar_wait(acc_full + buf, (a.accs == 1 ? local >> 1 : local) & 1, abort_flag, p.err, 5);
-        __syncwarp();
-        tc_fence_after();
-        ++local;
-      }
-      // (the warps that share barriers in what follows leave together)
-      ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
-      if (CG == 1 && a.split > 1) {
-        // the CTAs of a cluster have each summed a share of the reduction: the others hand theirs to the first one's
-        // shared memory, which adds them in order
-        if (part > 0 && ok) {
+        const int buf = a.accs == 1 ? local & 1 : 0;
+        const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+        if (sum) {
+          ok = mbar_wait(acc_full + buf, (a.accs == 1 ? local >> 1 : local) & 1, abort_flag, p.err, 5);
+          __syncwarp();
+          tc_fence_after();
+          ++local;
+        }
+        // (the warps that share barriers in what follows leave together)
+        ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
+        if (CG == 1 && a.split > 1) {
+          // the CTAs of a cluster have each summed a share of the reduction: the others hand theirs to the first one's
+          // shared memory, which adds them in order
+          if (part > 0 && ok) {
+            for (int c = c_first; c < o.n; c += c_step) {
+              float v[32];
+              if (sum) {
+                tmem_ld32(taddr + c, v);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              }
+              const uint32_t to = mapa(su32(parts + ((part - 1) * a.bn + c) * kPartLd + 32 * quad + lane), 0);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + j * kPartLd * 4), "f"(v[j]) : "memory");
+            }
+          }
+          cluster_sync();
+          if (part > 0) ok = false;
+        }
+        if (!ok) break;
+        const bool two = EPI == MM_EPI_STATS && !kHold && a.accs > 1;
+        if (two) {  // fold the first accumulator into the second and hand it back: the next tile's first half needs it soon
+          for (int c = c_first; o.red > a.seg && c < o.n && l0 + 32 * quad < p.lanes; c += c_step) {
+            float v[32], more[32];
+            tmem_ld32(taddr + c, v);
+            tmem_ld32(taddr + acc_stride + c, more);
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] + more[j]);
+            tmem_st32(taddr + acc_stride + c, w);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(acc_empty);
+        }
+        if (EPI == MM_EPI_STATS) {
+          const uint32_t sums = two && o.red > a.seg ? taddr + acc_stride : taddr;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = c_first + i * c_step;
+            if (c >= o.n || l0 + 32 * quad >= p.lanes) break;  // (no words, or no tokens)
+            float v[32];
+            float(&y)[32] = kHold ? z[kHold ? i : 0] : v;
+            tmem_ld32(sums + c, v);
+            if (kHold) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = k ? y[j] + v[j] : v[j];
+              if (k + a.seg < o.red) continue;
+            }
+            const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
+            epi_stats(y, nv, m, total);
+            if (at >= 0 && at < nv) {  // (the label of a lane that exists)
+              float own = 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j == at) own = y[j];
+              e.zlab[l0 + 32 * quad + lane] = own;
+            }
+          }
+        } else if (by_rows) {
+          for (int c = c_first; c < o.n; c += c_step) {
+            Frag f;
+            if (sum) {
+              tmem_ld_frag(taddr + c, f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
+            }
+            if (CG == 1) {
+              for (int k = 1; k < a.split; ++k) {
+                const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
+                    f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
+                  }
+              }
+            }
+            const int64_t row_at = first_row + (c - c_first);
+            if (EPI == MM_EPI_SOFTGRAD) {
+              const int word = o.c0 + c + 2 * (lane & 3);
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) {
+                    // (a row without gradient stays zero even where its logits are not finite)
+                    const float d = (__expf(f.v[j][r][q] - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
+                    f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
+                  }
+            } else {
+              if (e.scale) {
+                const float sc = *e.scale;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] *= sc, f.v[j][r][1] *= sc;
+              }
+              if (e.bias) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] += bias[r], f.v[j][r][1] += bias[r];
+              }
+              if (e.z) {
+                frag_out(stage, quad, lane, f, p.f16);
+                named_bar(2 + half, 128);
+                rows.store(e.z, row_at * e.ldz + piece, e.ldz, o.n - c);
+                named_bar(2 + half, 128);
+              }
+              if (e.act == MM_ACT_SILU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = silu_fast(f.v[j][r][0]), f.v[j][r][1] = silu_fast(f.v[j][r][1]);
+              } else if (e.act == MM_ACT_GELU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_GELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_GELU);
+              } else if (e.act == MM_ACT_RELU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_RELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_RELU);
+              }
+              if (add) {
+                rows.stage(next);
+                named_bar(2 + half, 128);
+                add_at += c_step * add_ld;
+                if (c + c_step < o.n) rows.load(add, add_at, add_ld, o.n - c - c_step, next);
+                frag_add(stage, quad, lane, f, p.f16);  // (each warp rereads and overwrites its own quarter only)
+                __syncwarp();
+              }
+            }
+            frag_out(stage, quad, lane, f, p.f16);
+            named_bar(2 + half, 128);
+            rows.store(e.out, group_out + row_at * e.ld + piece, e.ld, o.n - c);
+            named_bar(2 + half, 128);
+          }
+        } else {
+          const int l = l0 + 32 * quad + lane;
           for (int c = c_first; c < o.n; c += c_step) {
             float v[32];
             if (sum) {
@@ -912,181 +1058,35 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.f;
             }
-            const uint32_t to = mapa(su32(parts + ((part - 1) * a.bn + c) * kPartLd + 32 * quad + lane), 0);
+            if (CG == 1) {
+              for (int k = 1; k < a.split; ++k) {
+                const float* q = parts + ((k - 1) * a.bn + c) * kPartLd + 32 * quad + lane;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + j * kPartLd * 4), "f"(v[j]) : "memory");
+                for (int j = 0; j < 32; ++j) v[j] += q[j * kPartLd];
+              }
+            }
+            const int nv = min(32, o.n - c);
+            if (EPI == MM_EPI_STORE) {
+              epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || k, v);
+              put(p, o.g, l, o.c0 + c, nv, v);
+            } else {
+              const int at = lab[0] - (o.c0 + c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
+              put(p, 0, l, o.c0 + c, nv, v);
+            }
           }
         }
-        cluster_sync();
-        if (part > 0) ok = false;
-      }
-      if (!ok) break;
-      const bool two = EPI == MM_EPI_STATS && !kHold && a.accs > 1;
-      if (two) {  // fold the first accumulator into the second and hand it back: the next tile's first half needs it soon
-        for (int c = c_first; o.red > a.seg && c < o.n && l0 + 32 * quad < p.lanes; c += c_step) {
-          float v[32], more[32];
-          tmem_ld32(taddr + c, v);
-          tmem_ld32(taddr + acc_stride + c, more);
-          uint32_t w[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j] + more[j]);
-          tmem_st32(taddr + acc_stride + c, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-      }
-      if (EPI == MM_EPI_STATS) {
-        const uint32_t sums = two && o.red > a.seg ? taddr + acc_stride : taddr;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = c_first + i * c_step;
-          if (c >= o.n || l0 + 32 * quad >= p.lanes) break;  // (no words, or no tokens)
-          float v[32];
-          float(&y)[32] = kHold ? z[kHold ? i : 0] : v;
-          tmem_ld32(sums + c, v);
-          if (kHold) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = k ? y[j] + v[j] : v[j];
-            if (k + a.seg < o.red) continue;
-          }
-          const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
-          epi_stats(y, nv, m, total);
-          if (at >= 0 && at < nv) {  // (the label of a lane that exists)
-            float own = 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j == at) own = y[j];
-            e.zlab[l0 + 32 * quad + lane] = own;
+        if (sum) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {  // the MMA may overwrite this buffer
+            if (CG == 2)
+              mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
+            else
+              mbar_arrive(acc_empty + (two ? 1 : buf));
           }
         }
-      } else if (by_rows) {
-        for (int c = c_first; c < o.n; c += c_step) {
-          Frag f;
-          if (sum) {
-            tmem_ld_frag(taddr + c, f);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
-          }
-          if (CG == 1) {
-            for (int k = 1; k < a.split; ++k) {
-              const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
-                  f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
-                }
-            }
-          }
-          const int64_t row_at = first_row + (c - c_first);
-          if (EPI == MM_EPI_SOFTGRAD) {
-            const int word = o.c0 + c + 2 * (lane & 3);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  // (a row without gradient stays zero even where its logits are not finite)
-                  const float d = (__expf(f.v[j][r][q] - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
-                  f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
-                }
-          } else {
-            if (e.scale) {
-              const float sc = *e.scale;
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] *= sc, f.v[j][r][1] *= sc;
-            }
-            if (e.bias) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] += bias[r], f.v[j][r][1] += bias[r];
-            }
-            if (e.z) {
-              frag_out(stage, quad, lane, f, p.f16);
-              named_bar(2 + half, 128);
-              rows.store(e.z, row_at * e.ldz + piece, e.ldz, o.n - c);
-              named_bar(2 + half, 128);
-            }
-            if (e.act == MM_ACT_SILU) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] = silu_fast(f.v[j][r][0]), f.v[j][r][1] = silu_fast(f.v[j][r][1]);
-            } else if (e.act == MM_ACT_GELU) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_GELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_GELU);
-            } else if (e.act == MM_ACT_RELU) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_RELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_RELU);
-            }
-            if (add) {
-              rows.stage(next);
-              named_bar(2 + half, 128);
-              add_at += c_step * add_ld;
-              if (c + c_step < o.n) rows.load(add, add_at, add_ld, o.n - c - c_step, next);
-              frag_add(stage, quad, lane, f, p.f16);  // (each warp rereads and overwrites its own quarter only)
-              __syncwarp();
-            }
-          }
-          frag_out(stage, quad, lane, f, p.f16);
-          named_bar(2 + half, 128);
-          rows.store(e.out, group_out + row_at * e.ld + piece, e.ld, o.n - c);
-          named_bar(2 + half, 128);
-        }
-      } else {
-        const int l = l0 + 32 * quad + lane;
-        for (int c = c_first; c < o.n; c += c_step) {
-          float v[32];
-          if (sum) {
-            tmem_ld32(taddr + c, v);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.f;
-          }
-          if (CG == 1) {
-            for (int k = 1; k < a.split; ++k) {
-              const float* q = parts + ((k - 1) * a.bn + c) * kPartLd + 32 * quad + lane;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += q[j * kPartLd];
-            }
-          }
-          const int nv = min(32, o.n - c);
-          if (EPI == MM_EPI_STORE) {
-            epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || k, v);
-            put(p, o.g, l, o.c0 + c, nv, v);
-          } else {
-            const int at = lab[0] - (o.c0 + c);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
-            put(p, 0, l, o.c0 + c, nv, v);
-          }
-        }
-      }
-      if (sum) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {  // the MMA may overwrite this buffer
-          if (CG == 2)
-            mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
-          else
-            mbar_arrive(acc_empty + (two ? 1 : buf));
-        }
-      }
       }
       if (!ok) break;
       if (EPI == MM_EPI_STATS) {  // the two halves' partials are joined
