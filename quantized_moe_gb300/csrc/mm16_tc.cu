@@ -268,42 +268,44 @@ struct Loader {
     if (red_major) return mn_left > 32 * u ? min(8, r_left) : 0;
     return r_left > 32 * (u & 1) ? min(8, mn_left - 64 * (u >> 1)) : 0;
   }
-  // 32 u rows of a stage, then on to the next stage
-  __device__ __forceinline__ void stage(uint8_t* dst, int units, int64_t next) {
+  // The words of the chunks in rows 32 u0 .. 32 u0 + 96 of the current stage, and their way into the stage: other work
+  // goes in between, while they are in flight.
+  __device__ __forceinline__ void load(int u0, int units, uint32_t (&w)[4][5]) const {
     const uint32_t* q = reinterpret_cast<const uint32_t*>(src - odd);
-    const uint32_t sh = odd * 16;
-    uint8_t* to = dst + row * 128 + ((ch ^ (row & 7)) << 4);
-    for (int u0 = 0; u0 < units; u0 += 4) {
-      uint32_t w[4][5];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = u0 + i, v = u < units ? valid(u) : 0;
-        const uint32_t* qu = q + (red_major ? u * step : (u & 1) * step + 64 * (u >> 1)) / 2;
-        if (v >= 8) {
+    for (int i = 0; i < 4; ++i) {
+      const int u = u0 + i, v = u < units ? valid(u) : 0;
+      const uint32_t* qu = q + (red_major ? u * step : (u & 1) * step + 64 * (u >> 1)) / 2;
+      if (v >= 8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[i][k] = *(qu + k);
-          w[i][4] = odd ? *(qu + 4) : 0u;
-        } else {
+        for (int k = 0; k < 4; ++k) w[i][k] = qu[k];
+        w[i][4] = odd ? qu[4] : 0u;
+      } else {
 #pragma unroll
-          for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? *(qu + k) : 0u;  // (a word with a wanted element)
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int u = u0 + i;
-        if (u >= units) break;
-        uint32_t r[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[i][k], w[i][k + 1], sh);
-        const int v = valid(u);
-        if (v < 8) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) r[k] = v - 2 * k < 1 ? 0u : v - 2 * k < 2 ? r[k] & 0xffffu : r[k];
-        }
-        *reinterpret_cast<uint4*>(to + u * 4096) = make_uint4(r[0], r[1], r[2], r[3]);
+        for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? qu[k] : 0u;  // (a word with a wanted element)
       }
     }
-    src += next;
+  }
+  __device__ __forceinline__ void put(uint8_t* dst, int u0, int units, const uint32_t (&w)[4][5]) const {
+    const uint32_t sh = odd * 16;
+    uint8_t* to = dst + row * 128 + ((ch ^ (row & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = u0 + i;
+      if (u >= units) break;
+      uint32_t r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[i][k], w[i][k + 1], sh);
+      const int v = valid(u);
+      if (v < 8) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] = v - 2 * k < 1 ? 0u : v - 2 * k < 2 ? r[k] & 0xffffu : r[k];
+      }
+      *reinterpret_cast<uint4*>(to + u * 4096) = make_uint4(r[0], r[1], r[2], r[3]);
+    }
+  }
+  __device__ __forceinline__ void next_stage(int64_t elements) {
+    src += elements;
     r_left -= BK;
   }
 };
@@ -667,14 +669,25 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       Loader la, lb;
       la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
       lb.start(static_cast<const uint16_t*>(p.b.p), p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0, o.r0 + o.red, tid);
+      const int b_units = (nb + 31) / 32;
+      uint32_t wa[4][5], wb[4][5];
+      if (o.red > 0) la.load(0, BM / 32, wa);
       for (int k = 0; k < o.red; k += BK) {
+        lb.load(0, b_units, wb);
         if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
           ok = false;
           break;
         }
         uint8_t* st = smem + s * stage_bytes;
-        la.stage(st, BM / 32, p.a.red_major ? BK : BK * p.a.ld);
-        lb.stage(st + A_BYTES, (nb + 31) / 32, p.b.red_major ? BK : BK * p.b.ld);
+        la.put(st, 0, BM / 32, wa);
+        la.next_stage(p.a.red_major ? BK : BK * p.a.ld);
+        if (k + BK < o.red) la.load(0, BM / 32, wa);  // in flight over the next stage's wait
+        lb.put(st + A_BYTES, 0, b_units, wb);
+        if (b_units > 4) {
+          lb.load(4, b_units, wb);
+          lb.put(st + A_BYTES, 4, b_units, wb);
+        }
+        lb.next_stage(p.b.red_major ? BK : BK * p.b.ld);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s);
