@@ -12,16 +12,16 @@
 // MMA spans both SMs' tiles, 256 lanes, and each CTA stages half of the columns, which halves
 // the shared-memory and L2 traffic of the column operand.
 //
-// Warp roles: warp 0 issues the TMA loads (its lanes issue the copies of a stage in parallel); one
-// thread of warp 1 issues the MMAs (the leader's, in a pair); warp 2 clears what a ragged end of the
-// reduction leaves in a stage; warps 4-11 run the epilogue of one tile while the next one's main loop
+// Warp roles: warps 0 and 3 issue the TMA loads of one operand each (their lanes issue the copies of a
+// stage in parallel); one thread of warp 1 issues the MMAs (the leader's, in a pair); warp 2 clears what a
+// ragged end of the reduction leaves in a stage; warps 4-11 run the epilogue of one tile while the next one's main loop
 // fills the other accumulator. Where an operand's address or row distance is not a multiple of 16
 // bytes, eight loader warps (12-19) read it with ordinary loads and write the same swizzled layout.
 // Few tiles share their reduction out over a cluster of CTAs, which join their sums in shared memory.
 //
 // What bounds it (GB300, measured): the experts' products stream their weights (256 experts, 32768
 // rows, n 2048, k 4096: 0.70-0.72 ms = 6.5-6.8 TB/s, 96-99 % of the copy bandwidth, for y and dx; the
-// weight gradients, 4.3 GB of results, 0.90 ms = 5.2 TB/s, bound by the epilogue's instructions);
+// weight gradients, 4.3 GB of results, 0.86 ms = 5.5 TB/s, bound by the roles' work per tile of two stages);
 // large dense products the tensor pipe and the SMs' L2 reads (2048 x 129280 x 4096: 1.12 ms = 1.94
 // PFLOP/s, the rate of a large library product; 4096^3 with its epilogue 94 us = 1.46 PFLOP/s, of
 // which a seventh is the last, partial round and the launch); single tokens the launch and one pass of
@@ -236,6 +236,29 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
   }
   return o;
 }
+
+// The tiles of a warp in turn, every `step`-th one from `first`: tile_of takes a few hundred cycles of dependent
+// arithmetic, so the lanes work out 32 tiles at once and hand them round (weight gradients of 256 experts, 128 rows
+// each, where a tile has two or three stages: 910 -> 857 us with this and the cleaner's stores unrolled).
+template <int CG>
+struct Walk {
+  Tile mine;
+  int i = 31;
+  __device__ __forceinline__ Tile next(const TcArgs& a, const int* lo_of, const int* pref, int t, int step, int tiles, int share, int lane) {
+    if (++i == 32) {
+      i = 0;
+      mine = tile_of<CG>(a, lo_of, pref, min(t + lane * step, tiles - 1), share);
+    }
+    Tile o;
+    o.g = __shfl_sync(0xffffffffu, mine.g, i);
+    o.l0 = __shfl_sync(0xffffffffu, mine.l0, i);
+    o.c0 = __shfl_sync(0xffffffffu, mine.c0, i);
+    o.n = __shfl_sync(0xffffffffu, mine.n, i);
+    o.r0 = __shfl_sync(0xffffffffu, mine.r0, i);
+    o.red = __shfl_sync(0xffffffffu, mine.red, i);
+    return o;
+  }
+};
 
 // Columns of the tile's MMA: its columns rounded up to the granule (16, in a pair 32); whole 64-column
 // boxes where the columns are the contiguous index.
@@ -608,15 +631,18 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const int part = CG == 1 && a.split > 1 ? (int)cluster_ctarank() : 0;
   if (CG == 1 && a.split > 1) tiles = min(tiles, first + 1);  // one tile a cluster, whatever the offsets say
 
-  if (warp == 0 && !GEN) {
-    // ------------------------------------------------------------------ TMA producer
-    const bool a_red = p.a.red_major, b_red = p.b.red_major;
+  if ((warp == 0 || warp == 3) && !GEN) {
+    // ------------------------------------------------------------------ TMA producers: warp 0 of A, warp 3 of B
+    // One warp for both issues a stage's copies no faster than the MMAs use it up (y of 256 experts, 128 rows each: 726
+    // us, 714 with two; gradients of 4096 x 2048 x 4096: 108, 105).
+    const bool a_red = p.a.red_major, b_red = p.b.red_major, of_a = warp == 0;
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
     const int a_boxes = a_red ? 1 : 2 / a.a_blocks;
+    Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
       const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
@@ -625,33 +651,29 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
       const int ga = p.rag == MM_RAG_COLS ? o.g : 0;
       for (int k = 0; k < o.red; k += BK) {
-        if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
-          ok = false;
-          break;
-        }
-        uint8_t* st = smem + s * stage_bytes;
-        if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);
-        __syncwarp();
-        const uint32_t bar = CG == 2 ? mapa(su32(full + s), 0) : su32(full + s);
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1));
+        if (!ok) break;
+        const uint32_t st = su32(smem + s * stage_bytes), bar = CG == 2 ? mapa(su32(full + s), 0) : su32(full + s);
         const int r = o.r0 + k;
-        if (lane < a_boxes) {
-          if (a_red)
-            tma_load<CG>(su32(st), &ta, r, la, 0, ga, bar);
-          else if (a.a_blocks > 1)
-            tma_load<CG>(su32(st), &ta, 0, r, la / 64, ga, bar);
-          else
-            tma_load<CG>(su32(st + lane * 8192), &ta, la + 64 * lane, r, 0, ga, bar);
-        } else if (lane >= 4 && lane < 4 + b_boxes) {
-          const int i = lane - 4;
-          const uint32_t to = su32(st + A_BYTES + i * b_box_bytes);
+        if (of_a) {
+          if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);  // (copies may report before it)
+          if (lane < a_boxes) {
+            if (a_red)
+              tma_load<CG>(st, &ta, r, la, 0, ga, bar);
+            else if (a.a_blocks > 1)
+              tma_load<CG>(st, &ta, 0, r, la / 64, ga, bar);
+            else
+              tma_load<CG>(st + lane * 8192, &ta, la + 64 * lane, r, 0, ga, bar);
+          }
+        } else if (lane < b_boxes) {
+          const uint32_t to = st + A_BYTES + lane * b_box_bytes;
           if (b_red)
-            tma_load<CG>(to, &tb, r, cb + i * a.b_box, 0, 0, bar);
+            tma_load<CG>(to, &tb, r, cb + lane * a.b_box, 0, 0, bar);
           else if (a.b_blocks > 1)
-            tma_load<CG>(to, &tb, 0, r, cb / 64 + i * a.b_blocks, 0, bar);
+            tma_load<CG>(to, &tb, 0, r, cb / 64 + lane * a.b_blocks, 0, bar);
           else
-            tma_load<CG>(to, &tb, cb + 64 * i, r, 0, 0, bar);
+            tma_load<CG>(to, &tb, cb + 64 * lane, r, 0, 0, bar);
         }
-        __syncwarp();
         if (++s == a.stages) s = 0, ph ^= 1;
       }
     }
@@ -661,8 +683,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     const int tid = threadIdx.x - kThreads;
+    Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const int nb = mma_n<CG>(p, o.n);
@@ -674,10 +697,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       if (o.red > 0) la.load(0, BM / 32, wa);
       for (int k = 0; k < o.red; k += BK) {
         lb.load(0, b_units, wb);
-        if (!mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1));
+        if (!ok) break;
         uint8_t* st = smem + s * stage_bytes;
         la.put(st, 0, BM / 32, wa);
         la.next_stage(p.a.red_major ? BK : BK * p.a.ld);
@@ -766,20 +787,22 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
+    Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       for (int k = 0; k < o.red; k += BK) {
-        if (!mbar_wait(full + s, ph, abort_flag, p.err, 2)) {
-          ok = false;
-          break;
-        }
+        ok = __all_sync(0xffffffffu, mbar_wait(full + s, ph, abort_flag, p.err, 2));
+        if (!ok) break;
         const int left = min(BK, o.red - k);
         if (left & 15) {
-          uint8_t* st = smem + s * stage_bytes;
-          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, end = (left + 15) & ~15;
-          for (int box = 0; box < boxes; ++box)
-            for (int row = left + (lane >> 3); row < end; row += 4)
-              *reinterpret_cast<uint4*>(st + box * 8192 + row * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, from = left + (lane >> 3), end = (left + 15) & ~15;
+          uint8_t* st = smem + s * stage_bytes + from * 128 + (lane & 7) * 16;
+#pragma unroll
+          for (int box = 0; box < 6; ++box) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (box < boxes && from + 4 * r < end) *reinterpret_cast<uint4*>(st + box * 8192 + r * 512) = make_uint4(0, 0, 0, 0);
+          }
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         }
         __syncwarp();
@@ -796,8 +819,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     const uint32_t stage = su32(out_stage) + half * kOutBytes, from = stage + (uint32_t)(row * kRowBytes + piece * 16);
     const int64_t ld = p.e.ld;
     int local = 0;
+    Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const bool sum = o.red > 0;
       const int buf = local & 1, l = o.l0 + BM * rank + 8 * piece;
@@ -862,8 +886,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
     const int c_first = 32 * half, c_step = 64;
     int local = 0;
+    Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;

@@ -1,8 +1,8 @@
 """CPU: a model of the 16-bit products' barrier protocol under random interleavings.
 
 The persistent kernel (csrc/mm16_tc.cu) runs, over a ring of stages whose waits test only a phase's
-parity: a TMA producer in each CTA of the tile (one, or the two of a pair, whose copies all report to
-the leader's full barrier), the thread that issues the MMAs (the leader's; its commits complete in issue
+parity: two TMA producers in each CTA of the tile, one of each operand (one CTA, or the two of a pair, whose copies all
+report to the leader's full barrier, perhaps before its A producer has announced their bytes), the thread that issues the MMAs (the leader's; its commits complete in issue
 order and release the stage in every CTA), for ragged reductions a cleaner that passes every stage,
 clears a tile's last one where the group ends inside a step of 16, and has to arrive on the stage's empty
 barrier too, and the epilogue warps of every CTA, which hand accumulators back to the leader. Two accumulators
@@ -37,14 +37,14 @@ def simulate(seed, ctas, stages, tiles, ragged=False, seg=None, side_by_side=Fal
             yield
         bar.check_wait(k)
 
-    def producer(c):
+    def producer(c, of_a):
         g = 0
         for n, _ in tiles:
             for _ in range(n):
                 s, use = g % stages, g // stages
                 yield from wait(empty[c][s], use - 1)
-                if c == 0:
-                    full[s].arrive(use, tx=ctas)
+                if c == 0 and of_a:
+                    full[s].arrive(use, tx=2 * ctas)
                 yield
                 landing.append((full[s], use))
                 g += 1
@@ -109,7 +109,7 @@ def simulate(seed, ctas, stages, tiles, ragged=False, seg=None, side_by_side=Fal
                     acc_empty[acc % 2].arrive(acc // 2)
                 acc += 1
 
-    actors = [producer(c) for c in range(ctas)] + [mma()] + [epilogue(c) for c in range(ctas) for _ in range(WARPS)]
+    actors = [producer(c, of_a) for c in range(ctas) for of_a in (True, False)] + [mma()] + [epilogue(c) for c in range(ctas) for _ in range(WARPS)]
     if ragged:
         actors.append(cleaner())
     weight = [rng.choice((1, 1, 5)) for _ in actors]  # some actors run far more often than others
