@@ -21,7 +21,7 @@
 //
 // What bounds it (GB300, measured): the experts' products stream their weights (256 experts, 32768
 // rows, n 2048, k 4096: 0.70-0.72 ms = 6.5-6.8 TB/s, 96-99 % of the copy bandwidth, for y and dx; the
-// weight gradients, 4.3 GB of results, 0.86 ms = 5.5 TB/s, bound by the roles' work per tile of two stages);
+// weight gradients, 4.3 GB of results, 0.85 ms = 5.5 TB/s: their way through shared memory beside the MMAs' operands);
 // large dense products the tensor pipe and the SMs' L2 reads (2048 x 129280 x 4096: 1.12 ms = 1.94
 // PFLOP/s, the rate of a large library product; 4096^3 with its epilogue 94 us = 1.46 PFLOP/s, of
 // which a seventh is the last, partial round and the launch); single tokens the launch and one pass of
