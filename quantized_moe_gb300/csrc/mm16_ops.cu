@@ -245,7 +245,7 @@ extern "C" int ds4moe_linear(const void* x, const void* w, const void* bias, con
 }
 
 extern "C" int64_t ds4moe_linear_grad_workspace(int32_t rows, int32_t n, int32_t act) {
-  if (rows <= 0 || n <= 0) return 16;
+  if (rows <= 0 || n <= 0) return 16;  // (without rows nothing is kept: ds4moe_linear_grad writes the zeros directly)
   return 16 + (act == DS4MOE_ACT_NONE ? 0 : up(2 * (int64_t)rows * up(n, 8), 16)) + 4 * (int64_t)ds4::mm_colsum_chunks(rows) * n;
 }
 
@@ -272,11 +272,16 @@ extern "C" int ds4moe_linear_grad(const void* dy, const void* x, const void* w, 
     int* err = c.err_word();
     if (!c.ok()) return c.code;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (none) {  // empty sums, which need no scratch: dw is the product's own zeros, db (0 is +0 in either type) a fill
+      cudaError_t e = db ? cudaMemsetAsync(db, 0, 2 * (size_t)n, s) : cudaSuccess;
+      if (e == cudaSuccess && dw) e = ds4::mm_launch(product(x, ldx, false, dy, lddy, false, k, n, 0, dtype, dw, lddw, err), s);
+      return c.cuda(e);
+    }
     char* ws = static_cast<char*>(workspace);
     const void* dz = dy;
     int64_t lddz = lddy;
     cudaError_t e = cudaSuccess;
-    if (act != DS4MOE_ACT_NONE && !none && (dx || dw)) dz = ws, lddz = up(n, 8);
+    if (act != DS4MOE_ACT_NONE && (dx || dw)) dz = ws, lddz = up(n, 8);
     float* part = db ? reinterpret_cast<float*>(ws + (act == DS4MOE_ACT_NONE ? 0 : up(2 * (int64_t)rows * up(n, 8), 16))) : nullptr;
     if (db || dz != dy) e = ds4::mm_act_grad(dy, lddy, z, ldz, dz == dy ? nullptr : ws, lddz, part, db, rows, n, act, dtype == DS4MOE_FP16, s);
     if (e == cudaSuccess && dx) e = ds4::mm_launch(product(w, ldw, false, dz, lddz, true, k, rows, n, dtype, dx, lddx, err), s);
