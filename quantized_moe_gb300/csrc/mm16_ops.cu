@@ -336,11 +336,7 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     c.rows(rows), c.width("vocab", vocab), c.width("d", d), c.dtype(dtype);
     ldx = c.ld("ldx", ldx, d), ldw = c.ld("ldw", ldw, d), lddx = c.ld("lddx", lddx, d), lddw = c.ld("lddw", lddw, d);
     if (!c.ok() || (!dx && !dw)) return c.code;
-    // the largest piece of the vocabulary that the workspace holds
-    const int64_t full = std::min<int64_t>(kPieceMax, up(vocab, kPieceMin));
-    int64_t piece = rows ? (workspace_bytes - ce_grad_bytes(rows, d, 0)) / (2 * up(rows, 8)) / kPieceMin * kPieceMin : full;
-    piece = std::min(piece, full);
-    if (piece < kPieceMin) {
+    if (rows && workspace_bytes < ce_grad_bytes(rows, d, kPieceMin)) {  // (compared before it is reduced: it may be any number)
       c.fail(DS4MOE_ERR_CAPACITY, "workspace_bytes is less than the " + std::to_string(ce_grad_bytes(rows, d, kPieceMin)) + " of the smallest piece of the vocabulary");
       return c.code;
     }
@@ -361,7 +357,9 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     char* dz = ws + 16 + up(4 * (int64_t)rows * d, 16);
     const char* wb = static_cast<const char*>(w);
     const int64_t lddz = up(rows, 8);
-    piece = best_piece(piece, rows, vocab, d, dx, dw);
+    // the largest piece of the vocabulary that the workspace holds
+    const int64_t fits = (workspace_bytes - ce_grad_bytes(rows, d, 0)) / (2 * lddz) / kPieceMin * kPieceMin;
+    const int64_t piece = best_piece(std::min<int64_t>({fits, kPieceMax, up(vocab, kPieceMin)}), rows, vocab, d, dx, dw);
     cudaError_t e = ds4::mm_grad_scale(dloss, labels, ignore_index, vocab, rows, gs, s);
     for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += piece) {
       const int pv = (int)std::min<int64_t>(piece, vocab - v0);
