@@ -26,6 +26,14 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s,
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+// Eight 16-bit elements that are also moved as one 16-byte piece (a plain array is aligned to 2 bytes only, and the piece's
+// loads and stores could fault wherever the compiler keeps it in memory).
+struct Eight {
+  alignas(16) uint16_t h[8];
+  __device__ __forceinline__ uint4& piece() { return *reinterpret_cast<uint4*>(h); }
+};
+static_assert(alignof(Eight) >= alignof(uint4) && sizeof(Eight) == sizeof(uint4), "a piece of eight elements");
+
 // dz = dy * act'(z), and the column sums of dz (unrounded, fp32). A block takes 256 columns of one chunk of rows: each of
 // its eight warps walks every eighth row with one 16-byte load per operand (eight columns a thread), then the warps'
 // sums are added in order through shared memory, one partial per column and chunk. The second kernel adds the chunks
@@ -44,20 +52,20 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t l
   float sum[8] = {};
   if (c < n) {
     for (int r = r0 + warp; r < r1; r += 16) {  // two rows in flight
-      uint16_t hy[2][8], hz[2][8];
+      Eight hy[2], hz[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int rk = r + 8 * k;
         const uint16_t* py = static_cast<const uint16_t*>(dy) + (int64_t)rk * lddy + c;
         const uint16_t* pz = static_cast<const uint16_t*>(z) + (int64_t)rk * ldz + c;
         if (VEC) {
-          *reinterpret_cast<uint4*>(hy[k]) = rk < r1 ? *reinterpret_cast<const uint4*>(py) : make_uint4(0, 0, 0, 0);
-          if (ACT != MM_ACT_NONE) *reinterpret_cast<uint4*>(hz[k]) = rk < r1 ? *reinterpret_cast<const uint4*>(pz) : make_uint4(0, 0, 0, 0);
+          hy[k].piece() = rk < r1 ? *reinterpret_cast<const uint4*>(py) : make_uint4(0, 0, 0, 0);
+          if (ACT != MM_ACT_NONE) hz[k].piece() = rk < r1 ? *reinterpret_cast<const uint4*>(pz) : make_uint4(0, 0, 0, 0);
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            hy[k][i] = rk < r1 && c + i < n ? py[i] : (uint16_t)0;
-            if (ACT != MM_ACT_NONE) hz[k][i] = rk < r1 && c + i < n ? pz[i] : (uint16_t)0;
+            hy[k].h[i] = rk < r1 && c + i < n ? py[i] : (uint16_t)0;
+            if (ACT != MM_ACT_NONE) hz[k].h[i] = rk < r1 && c + i < n ? pz[i] : (uint16_t)0;
           }
         }
       }
@@ -65,22 +73,22 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t l
       for (int k = 0; k < 2; ++k) {
         const int rk = r + 8 * k;
         if (rk >= r1) break;
-        uint16_t h[8];
+        Eight out;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float g = ld16(hy[k], i, f16);
-          if (ACT != MM_ACT_NONE) g *= mm_act_slope(ld16(hz[k], i, f16), ACT);
+          float g = ld16(hy[k].h, i, f16);
+          if (ACT != MM_ACT_NONE) g *= mm_act_slope(ld16(hz[k].h, i, f16), ACT);
           sum[i] += g;
-          st16(h, i, g, f16);
+          st16(out.h, i, g, f16);
         }
         if (dz) {
           uint16_t* pd = static_cast<uint16_t*>(dz) + (int64_t)rk * lddz + c;
           if (VEC) {
-            *reinterpret_cast<uint4*>(pd) = *reinterpret_cast<const uint4*>(h);
+            *reinterpret_cast<uint4*>(pd) = out.piece();
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (c + i < n) pd[i] = h[i];
+              if (c + i < n) pd[i] = out.h[i];
           }
         }
       }
