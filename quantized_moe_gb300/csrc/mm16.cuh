@@ -129,7 +129,7 @@ cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz
 // Joins the softmax partials of each token: lse, loss, and bit 0 of *err for labels outside the vocabulary.
 cudaError_t mm_softmax_join(const float2* part, int tiles, const float* zlab, const int* labels, int ignore, int vocab,
                             int rows, float* loss, float* lse, int* err, cudaStream_t s);
-// gs[0] = max |g| over the rows with a label (1 where that is 0 or not finite), gs[1] = gs[0] / kMmGradOne.
+// gs[0] = max |g| over the rows with a label and a finite g (1 where that is 0), gs[1] = gs[0] / kMmGradOne.
 cudaError_t mm_grad_scale(const float* g, const int* labels, int ignore, int vocab, int rows, float* gs, cudaStream_t s);
 
 }  // namespace ds4

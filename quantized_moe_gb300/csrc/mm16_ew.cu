@@ -157,6 +157,8 @@ __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* part, i
   }
 }
 
+// The scale of dz: the largest |g| of the rows with a label. A row whose g is not finite keeps that to itself: its dz is
+// not finite under any scale, and the scale of the others may not depend on it (an fp16 dz would overflow).
 __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* g, const int* labels,
                                                           int ignore, int vocab, int rows, float* gs) {
   __shared__ float s[32];
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* g, const 
   float m = 0.f;
   for (int i = threadIdx.x; i < rows; i += 1024) {
     const int lab = labels[i];
-    if (lab != ignore && lab >= 0 && lab < vocab) m = fmaxf(m, fabsf(g[i]));
+    if (lab != ignore && lab >= 0 && lab < vocab) m = fmaxf(m, isfinite(g[i]) ? fabsf(g[i]) : 0.f);
   }
   m = warp_max(m);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* g, const 
   if (threadIdx.x < 32) {
     m = warp_max(s[threadIdx.x]);
     if (threadIdx.x == 0) {
-      if (!(m > 0.f) || !isfinite(m)) m = 1.f;
+      if (m == 0.f) m = 1.f;
       gs[0] = m;
       gs[1] = m * (1.f / kMmGradOne);
     }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_mm16 import ULP, gen, normal, stream
+from test_gpu_mm16 import _ce, _ce_check, gen, normal, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +22,27 @@ def test_gradients_of_no_rows_stay_inside_the_workspace(n, act):
     assert not bool(dw[:n * k].any()) and bool((dw[n * k:] == 1).all())
     assert not bool(db[:n].any()) and bool((db[n:] == 1).all())
     assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_a_weight_that_is_not_finite_stays_in_its_row(dtype, bad, pad):
+    """dx[t] depends on row t alone: the other rows' are what they are without the bad one, bit for bit."""
+    rows, vocab, d = 37, 600, 72
+    x, w = normal((rows, d), dtype, 1, 0.2), normal((vocab, d), dtype, 2, d ** -0.5)
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    dloss = 1.0 + 60000.0 * torch.rand(rows, generator=gen(4), device="cuda")  # (times 2^13, far past fp16)
+    dloss[0], dloss[5], dloss[11] = 61001.0, 1e-3, 0.0
+    want = _ce(x, w, labels, dloss, dtype, pad=pad)
+    _ce_check(x, w, labels, dloss, dtype, want)
+    dloss[8] = 0.0
+    want = _ce(x, w, labels, dloss, dtype, pad=pad)[2]
+    dloss[8] = bad
+    loss, lse, dx, dw = _ce(x, w, labels, dloss, dtype, pad=pad)
+    others = torch.arange(rows, device="cuda") != 8
+    assert torch.equal(dx[others], want[others])
+    assert not bool(dx[8].isfinite().any()) and not bool(dw.isfinite().any())
+    labels[8] = -100  # without a label it is read by nothing
+    loss, lse, dx, dw = _ce(x, w, labels, dloss, dtype, pad=pad)
+    assert torch.equal(dx[others], want[others]) and not bool(dx[8].any()) and bool(dw.isfinite().all())
