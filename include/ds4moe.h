@@ -307,7 +307,8 @@ int ds4moe_linear_grad(const void* dy, const void* x, const void* w, const void*
 /* Softmax cross entropy of the logits z[t] = W x[t], without storing them: lse[t] = log sum_v exp z[t][v],
  * loss[t] = lse[t] - z[t][labels[t]] (fp32 [rows] each). x [rows x d], w [vocab x d], labels device int32
  * [rows]. A row whose label is ignore_index has loss 0 and no gradient; so has one whose label lies outside
- * [0, vocab), which also sets bit 0 of ds4moe_ops_status. lse is written for every row.
+ * [0, vocab), which also sets bit 0 of ds4moe_ops_status. lse is written for every row; it
+ * is -inf for a row whose every logit is -inf.
  *   ds4moe_cross_entropy_grad: for dloss (fp32 [rows]) and the lse of the forward,
  *     dz[t][v] = (exp(z[t][v] - lse[t]) - [v == labels[t]]) * dloss[t],
  *     dx[t] = sum_v dz[t][v] W[v], dw[v] = sum_t dz[t][v] x[t], rounded to dtype. Either may be NULL.

@@ -129,7 +129,8 @@ __global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int
 }
 
 // One warp per token: the tiles' (max, sum) are joined as (M, S) with M = max m_i and
-// S = sum s_i exp(m_i - M); lse = M + log S.
+// S = sum s_i exp(m_i - M); lse = M + log S. A tile at the maximum adds its sum as it is, so that a row whose every logit is
+// -inf has S = 0 and lse = -inf (exp(-inf + inf) would be NaN); a tile with NaN logits has a sum of NaN.
 __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* part, int tiles,
                                                            const float* zlab,
                                                            const int* labels, int ignore, int vocab,
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(256) softmax_join_kernel(const float2* part, i
   float sum = 0.f;
   for (int i = lane; i < tiles; i += 32) {
     const float2 q = part[(int64_t)i * rows + t];
-    sum += q.y * expf(q.x - m);
+    sum += q.x == m ? q.y : q.y * expf(q.x - m);
   }
   sum = warp_sum(sum);
   if (lane == 0) {

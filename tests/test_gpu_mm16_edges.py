@@ -46,3 +46,25 @@ def test_a_weight_that_is_not_finite_stays_in_its_row(dtype, bad, pad):
     labels[8] = -100  # without a label it is read by nothing
     loss, lse, dx, dw = _ce(x, w, labels, dloss, dtype, pad=pad)
     assert torch.equal(dx[others], want[others]) and not bool(dx[8].any()) and bool(dw.isfinite().all())
+
+
+@pytest.mark.parametrize("rows,pad", [(5, 0), (5, 3), (300, 0)])
+def test_a_row_of_closed_words_only(rows, pad):
+    """A row whose every logit is -inf has lse -inf (the logarithm of an empty sum); NaN logits stay NaN, whatever else
+    the row holds; the rows beside them are what they are without them."""
+    vocab, d = 700, 72
+    x, w = normal((rows, d), "bf16", 1), normal((vocab, d), "bf16", 2, d ** -0.5)
+    x[:, 0], w[:, 0] = 0.0, 1.0
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    labels[3] = -100
+    one = torch.ones(rows, device="cuda")
+    clean = _ce(x, w, labels, one, "bf16", pad=pad)
+    x[1, 0], x[3, 0] = -float("inf"), -float("inf")  # every word's logit of the row
+    x[2, 0] = float("nan")
+    loss, lse, dx, dw = _ce(x, w, labels, one, "bf16", pad=pad)
+    fine = torch.ones(rows, dtype=torch.bool, device="cuda")
+    fine[1:4] = False
+    assert torch.equal(lse[fine], clean[1][fine]) and torch.equal(loss[fine], clean[0][fine]) and torch.equal(dx[fine], clean[2][fine])
+    assert lse[1] == -float("inf") and lse[3] == -float("inf") and bool(lse[2].isnan())
+    assert loss[3] == 0 and not bool(dx[3].any()) and bool(loss[2].isnan())
+    assert bool(loss[1].isnan())  # -inf less the label's -inf: no word has a probability
