@@ -295,7 +295,8 @@ int ds4moe_linear(const void* x, const void* w, const void* bias, const void* re
 /* Its gradients, for dy [rows x n]: dz = dy * act'(z), dx = W^T dz [rows x k], dw = sum_t dz[t] x[t]^T
  * [n x k], db = sum_t dz[t] [n] (the residual's gradient is dy itself). z is what zout received (not
  * read, may be NULL, for DS4MOE_ACT_NONE). Each of dx, dw, db may be NULL: it is then not computed (w is
- * read only for dx, x only for dw). rows == 0 writes zeros into dw and db. dz is rounded to dtype
+ * read only for dx, x only for dw). Where z is infinite act' is its limit (0 or 1), where it is NaN dz is NaN;
+ * where relu is 0 (z <= 0) dz is 0 whatever dy holds. rows == 0 writes zeros into dw and db. dz is rounded to dtype
  * between its computation and the products; db sums the unrounded dz in fp32. workspace: 16-byte
  * aligned device memory of ds4moe_linear_grad_workspace bytes (DS4MOE_ERR_CAPACITY if less). */
 int64_t ds4moe_linear_grad_workspace(int32_t rows, int32_t n, int32_t act);

@@ -89,15 +89,18 @@ __device__ __forceinline__ float mm_act(float z, int act) {
   if (act == MM_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   return z;
 }
-__device__ __forceinline__ float mm_act_slope(float z, int act) {
-  if (act == MM_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+// dy * act'(z). z is what its type kept of an fp32 value, so that it may be infinite where the forward was finite: the
+// slope's limits are 0 and 1 there. z times a slope's factor that has run to 0 is taken at +-256, where that factor is
+// already 0 in fp32 (infinity times 0 would be NaN). NaN stays NaN; a place that relu closes passes nothing, whatever lies
+// in dy.
+__device__ __forceinline__ float mm_act_back(float dy, float z, int act) {
+  if (act == MM_ACT_RELU) return z > 0.f ? dy : z == z ? 0.f : z;
+  const float near = z > 256.f ? 256.f : z < -256.f ? -256.f : z;  // (NaN stays)
   if (act == MM_ACT_SILU) {
     const float s = __fdividef(1.f, 1.f + __expf(-z));
-    return s * (1.f + z * (1.f - s));
+    return dy * (s * (1.f + near * (1.f - s)));
   }
-  if (act == MM_ACT_GELU)
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * expf(-0.5f * z * z) * 0.39894228040143268f;
-  return 1.f;
+  return dy * (0.5f * (1.f + erff(z * 0.70710678118654752f)) + near * expf(-0.5f * near * near) * 0.39894228040143268f);
 }
 
 // dz of the cross entropy is kept in 16 bits as (exp(z - lse) - [label]) * (g / max |g|) * 2^13. The

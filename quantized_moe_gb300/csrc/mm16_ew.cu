@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t l
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float g = ld16(hy[k].h, i, f16);
-          if (ACT != MM_ACT_NONE) g *= mm_act_slope(ld16(hz[k].h, i, f16), ACT);
+          if (ACT != MM_ACT_NONE) g = mm_act_back(g, ld16(hz[k].h, i, f16), ACT);
           sum[i] += g;
           st16(out.h, i, g, f16);
         }

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_mm16 import _ce, _ce_check, gen, normal, stream
+from test_gpu_mm16 import DT, _ce, _ce_check, gen, normal, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,40 @@ def test_a_row_of_closed_words_only(rows, pad):
     assert lse[1] == -float("inf") and lse[3] == -float("inf") and bool(lse[2].isnan())
     assert loss[3] == 0 and not bool(dx[3].any()) and bool(loss[2].isnan())
     assert bool(loss[1].isnan())  # -inf less the label's -inf: no word has a probability
+
+
+def _dz(z, dy, act, dtype):
+    """dy * act'(z), through the gradient's column sums: one row, so that db is dz."""
+    n = z.numel()
+    size = api.ds4moe_linear_grad_workspace(1, n, act)
+    ws, db, dx = torch.empty(size, dtype=torch.uint8, device="cuda"), torch.empty_like(z), torch.empty((1, 8), dtype=z.dtype, device="cuda")
+    w = torch.zeros((n, 8), dtype=z.dtype, device="cuda")
+    api.ds4moe_linear_grad(dy, None, w, z, dx, None, db, 1, n, 8, act, dtype, ws, size, stream=stream())
+    kept = ws[:2 * n].view(z.dtype)  # dz as the products read it
+    assert torch.equal(kept.isnan(), db.isnan()) and torch.equal(kept.nan_to_num(), db.nan_to_num())
+    return db
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [8, 13])  # by 16-byte loads, and one by one
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu"])
+def test_slopes_where_the_kept_sums_are_not_finite(dtype, act, n):
+    """z overflows its type long before the forward's fp32 does: at -inf the slope is 0, at +inf 1, as it is for every
+    large z; at NaN it is NaN, as the forward's value is."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.zeros(n, dtype=torch.float32, device="cuda")
+    z[:6] = torch.tensor([inf, -inf, nan, 6e4, -6e4, 1.0])
+    dy = torch.full((n,), 0.75, device="cuda").to(z.dtype)
+    got = _dz(z.to(DT[dtype]), dy.to(DT[dtype]), act, dtype).float()
+    assert got[0] == 0.75 and got[1] == 0 and bool(got[2].isnan()) and got[3] == 0.75 and got[4] == 0
+    assert bool(got[5:].isfinite().all())
+
+
+@pytest.mark.parametrize("n", [8, 13])
+def test_relu_passes_nothing_through_a_closed_place(n):
+    """Where z <= 0 the gradient is 0 whatever dy holds; where z > 0 it is dy."""
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([-1.0, 0.0, -0.0, -inf, 2.0, 2.0, 2.0, -3.0] + [1.0] * (n - 8), device="cuda").to(torch.bfloat16)
+    dy = torch.tensor([inf, -inf, nan, nan, inf, nan, 3.0, 3.0] + [1.0] * (n - 8), device="cuda").to(torch.bfloat16)
+    got = _dz(z, dy, "relu", "bf16").float().tolist()
+    assert got[:5] == [0.0, 0.0, 0.0, 0.0, inf] and got[5] != got[5] and got[6:] == [3.0, 0.0] + [1.0] * (n - 8)
