@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_mm16 import DT, _ce, _ce_check, gen, normal, stream
+from test_gpu_mm16 import DT, ULP, _ce, _ce_check, gen, normal, stream
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,44 @@ def test_relu_passes_nothing_through_a_closed_place(n):
     dy = torch.tensor([inf, -inf, nan, nan, inf, nan, 3.0, 3.0] + [1.0] * (n - 8), device="cuda").to(torch.bfloat16)
     got = _dz(z, dy, "relu", "bf16").float().tolist()
     assert got[:5] == [0.0, 0.0, 0.0, 0.0, inf] and got[5] != got[5] and got[6:] == [3.0, 0.0] + [1.0] * (n - 8)
+
+
+# exp(-z^2 / 2) by an fp32 exponent: z^2, its way to base 2 and that base's constant are each rounded, 2.5 * 2^-24 of 84.5
+# at z = -13, 2^-16.2 of the result; the rest of the arithmetic, 5e-7 and a few units, is less
+TAIL = 2.0 ** -15
+
+
+def _tail(dtype):
+    """-13 to 3 in bf16's steps, less what the type cannot hold as a normal result."""
+    z = torch.linspace(-13.0, 3.0, 4001, device="cuda").to(torch.bfloat16).unique().to(DT[dtype])
+    z = z[z.abs() > 2.0 ** -9]
+    return z if dtype == "bf16" else z[z > -3.8]  # gelu(-3.8) = 2^-11.8, and fp16 is normal from 2^-14
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_the_tail_of_gelu(dtype):
+    """gelu is relatively exact far into its negative tail, where 1 + erf cancels."""
+    z = _tail(dtype)
+    n = z.numel()
+    one, y, y32 = torch.ones((1, 1), dtype=z.dtype, device="cuda"), torch.empty_like(z), torch.empty_like(z)
+    api.ds4moe_linear(z, one, None, None, y, n, 1, 1, "gelu", dtype, stream=stream())
+    want = 0.5 * z.double() * torch.special.erfc(-z.double() * 0.5 ** 0.5)
+    assert bool(((y.double() - want).abs() <= (ULP[dtype] + TAIL) * want.abs()).all())
+    wide, ones = z.repeat(16, 1), torch.eye(16, dtype=z.dtype, device="cuda")  # results by rows: 16 lanes
+    out = torch.empty((n, 16), dtype=z.dtype, device="cuda")
+    api.ds4moe_linear(wide.T.contiguous(), ones, None, None, out, n, 16, 16, "gelu", dtype, stream=stream())
+    assert torch.equal(out, y[:, None].expand(n, 16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_the_tail_of_gelus_slope(dtype):
+    """0.5 erfc(-z / sqrt 2) + z phi(z): the two terms are z^2 times the result's size apart and cancel by it where z is
+    far below zero; each is relatively exact."""
+    z = _tail(dtype)
+    got = _dz(z, torch.ones_like(z), "gelu", dtype).double()
+    phi = torch.exp(-0.5 * z.double() ** 2) / (2 * 3.141592653589793) ** 0.5
+    cdf = 0.5 * torch.special.erfc(-z.double() * 0.5 ** 0.5)
+    want = cdf + z.double() * phi
+    off = TAIL * (cdf + (z.double() * phi).abs()) + 2.0 ** -23 * want.abs()
+    sub = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -133
+    assert bool(((got - want).abs() <= ULP[dtype] * want.abs() + off + sub).all())
