@@ -45,6 +45,7 @@ constexpr int BM = 128, BK = 64;          // lanes per CTA; reduction of one sta
 constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulator where the result is fp32
+constexpr int kSegFold = 16384;           // and where it has 16 bits
 constexpr int kEpiPlain = 3;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
@@ -75,6 +76,7 @@ struct TcArgs {
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
   int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
   int accs;                   // accumulators of one tile that lie side by side in tensor memory (1: two take turns; 2: none is left to)
+  int fold;                   // a tile with more reduction than seg is summed up in tensor memory (fold_acc), seg by seg
   int split;                  // CTAs (a cluster) that share a tile's reduction; 1: none
   int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
   Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
@@ -181,6 +183,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_get16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
 }
 
 // One output tile.
@@ -334,6 +353,25 @@ struct Loader {
 };
 
 // ------------------------------------------------------------------------------------ epilogues
+
+// The running sum of a long reduction: adds (first: copies) an accumulator of n columns to the other one's place, from column
+// c0 on every second 32 columns, the warp's own lanes. Only this warp reads what it wrote there.
+__device__ __forceinline__ void fold_acc(uint32_t acc, uint32_t sum, bool first, int c0, int n) {
+  for (int c = c0; c < n; c += 64) {
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t v[16], w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = 0u;
+      tmem_get16(acc + c + h, v);
+      if (!first) tmem_get16(sum + c + h, w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+      tmem_put16(sum + c + h, v);
+    }
+  }
+  tmem_st_wait();
+}
 
 // 32 elements of one lane, nv of them there, `ld` apart: the type is chosen once for all of them.
 __device__ __forceinline__ void to16(const float (&v)[32], uint16_t (&h)[32], int f16) {
@@ -718,8 +756,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ------------------------------------------------------------------ MMA (one thread)
     if (elect_one()) {
-      int s = 0, local = 0;
-      uint32_t ph = 0, cleaned = 0;
+      int s = 0, buf = 0;
+      uint32_t ph = 0, cleaned = 0, used = 0;  // (used: the parity of each accumulator's uses)
       bool ok = true;
       const uint64_t a_step = (p.a.red_major ? 32 : 2048) >> 4, b_step = (p.b.red_major ? 32 : 2048) >> 4;
       const uint64_t a_desc = op_desc(su32(smem), p.a.red_major), b_desc = op_desc(su32(smem + A_BYTES), p.b.red_major);
@@ -730,26 +768,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         const int n = mma_n<CG>(p, o.n);
         const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
                                (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
+        // Accumulators take turns from tile to tile (or, of a result added up in memory, from seg to seg). A tile that is
+        // summed up in tensor memory stays with its own one, seg after seg, and so does the tile after it: the other
+        // one holds the sum, which the epilogue is done with when it hands the last seg's accumulator back.
+        const bool folds = a.fold && o.red > a.seg;
         uint32_t d = 0;
         int in_seg = 0;  // reduction already in this accumulator
         for (int k = 0; k < o.red; k += BK) {
-          const int buf = a.accs == 1 ? local & 1 : 0;
           if (in_seg == 0) {
-            if (a.accs == 1 || k == 0) {
-              if (!mbar_wait(acc_empty + buf, ((a.accs == 1 ? local >> 1 : local) & 1) ^ 1, abort_flag, p.err, 6)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              d = tmem + (uint32_t)(buf * acc_stride);
-            } else {  // the second accumulator of the same tile
-              if (!mbar_wait(acc_empty + 1, (local & 1) ^ 1, abort_flag, p.err, 6)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              d = tmem + acc_stride;
+            const int b = a.accs == 1 || k == 0 ? buf : 1;  // (1: the second accumulator of the same tile)
+            if (!mbar_wait(acc_empty + b, (used >> b & 1) ^ 1, abort_flag, p.err, 6)) {
+              ok = false;
+              break;
             }
+            tc_fence_after();
+            d = tmem + (uint32_t)(b * acc_stride);
           }
           const int left = min(BK, o.red - k);
           if (!mbar_wait(full + s, ph, abort_flag, p.err, 7) ||
@@ -770,9 +803,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (++s == a.stages) s = 0, ph ^= 1;
           in_seg += BK;
           if (in_seg == a.seg || k + BK >= o.red) {
-            if (a.accs == 1 || k + BK >= o.red) {
+            if (a.accs == 1) {
               commit<CG>(acc_full + buf);
-              ++local;
+              used ^= 1u << buf;
+              if (!folds) buf ^= 1;
+            } else if (k + BK >= o.red) {
+              commit<CG>(acc_full);
+              used ^= 3u;
             }
             in_seg = 0;
           }
@@ -818,24 +855,39 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     const int quad = warp & 3, half = (warp - 4) >> 2, piece = threadIdx.x & 15, row = (threadIdx.x & 127) >> 4;
     const uint32_t stage = su32(out_stage) + half * kOutBytes, from = stage + (uint32_t)(row * kRowBytes + piece * 16);
     const int64_t ld = p.e.ld;
-    int local = 0;
+    int buf = 0;
+    uint32_t used = 0;  // as the MMA counts them
     Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const bool sum = o.red > 0;
-      const int buf = local & 1, l = o.l0 + BM * rank + 8 * piece;
-      const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      const int l = o.l0 + BM * rank + 8 * piece;
+      uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
       int left = l < p.lanes ? o.n - 32 * half - row : 0;  // rows from the thread's first to the tile's end
       uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.out) + (p.rag == MM_RAG_RED ? o.g * p.e.group_stride : 0) +
                                           (o.c0 + 32 * half + row) * ld + l);
+      const bool folds = a.fold && o.red > a.seg;
+      const uint32_t held = tmem + (uint32_t)((buf ^ 1) * acc_stride) + ((uint32_t)(32 * quad) << 16);
       bool ok = true;
-      if (sum) {
-        ok = mbar_wait(acc_full + buf, (local >> 1) & 1, abort_flag, p.err, 5);
+      for (int k = 0; ok && k < o.red; k += a.seg) {  // (one round unless the tile folds)
+        ok = mbar_wait(acc_full + buf, used >> buf & 1, abort_flag, p.err, 5);
         __syncwarp();
         tc_fence_after();
-        ++local;
+        used ^= 1u << buf;
+        if (!folds || !ok) break;
+        fold_acc(taddr, held, k == 0, 32 * half, o.n);
+        if (k + a.seg >= o.red) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (CG == 2)
+            mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
+          else
+            mbar_arrive(acc_empty + buf);
+        }
       }
+      if (folds) taddr = held;
       if (!named_bar_all(2 + half, 128, ok)) break;  // (the warps that share barriers leave together)
       for (int c = 32 * half; c < o.n; c += 64) {
         Frag f;
@@ -868,6 +920,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           else
             mbar_arrive(acc_empty + buf);
         }
+        if (!folds) buf ^= 1;
       }
     }
   } else if (EPI != kEpiPlain && warp >= 4 && warp < kFirstLoader) {
@@ -885,7 +938,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.live = false;
     }
     const int c_first = 32 * half, c_step = 64;
-    int local = 0;
+    int buf = 0;
+    uint32_t used = 0;  // as the MMA counts them
     Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -926,15 +980,31 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       float m = -INFINITY, total = 0.f;
       constexpr bool kHold = EPI == MM_EPI_STATS && CG == 2;  // sums over accumulators are held in registers
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
+      const bool folds = a.fold && o.red > a.seg;
       bool ok = true;
       for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
-        const int buf = a.accs == 1 ? local & 1 : 0;
-        const uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+        uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
         if (sum) {
-          ok = mbar_wait(acc_full + buf, (a.accs == 1 ? local >> 1 : local) & 1, abort_flag, p.err, 5);
+          ok = mbar_wait(acc_full + buf, used >> buf & 1, abort_flag, p.err, 5);
           __syncwarp();
           tc_fence_after();
-          ++local;
+          used ^= 1u << buf;
+        }
+        if (folds && ok) {
+          const uint32_t held = tmem + (uint32_t)((buf ^ 1) * acc_stride) + ((uint32_t)(32 * quad) << 16);
+          fold_acc(taddr, held, k == 0, c_first, o.n);
+          taddr = held;
+          if (k + a.seg < o.red) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (CG == 2)
+                mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
+              else
+                mbar_arrive(acc_empty + buf);
+            }
+            continue;
+          }
         }
         // (the warps that share barriers in what follows leave together)
         ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
@@ -1105,7 +1175,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             }
             const int nv = min(32, o.n - c);
             if (EPI == MM_EPI_STORE) {
-              epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || k, v);
+              epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
               put(p, o.g, l, o.c0 + c, nv, v);
             } else {
               const int at = lab[0] - (o.c0 + c);
@@ -1124,6 +1194,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             else
               mbar_arrive(acc_empty + (two ? 1 : buf));
           }
+          if (a.accs == 1 && !folds) buf ^= 1;
         }
       }
       if (!ok) break;
@@ -1350,18 +1421,26 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK, a.b_blocks);
     if (!ok) return cudaErrorInvalidValue;
   }
-  // The tensor cores' fp32 accumulation cuts instead of rounding: over 256 steps of 16 the sums lose about 1e-5 of their
-  // size towards zero, which a 16-bit result does not show. Results in fp32 take several accumulators, added up with
-  // ordinary additions: weight gradients one for every 512 rows (added to what the tile has stored), losses one for
-  // every 2048 of d (their relative error at d 4096: 9.3e-7 with one accumulator, 4.6e-7 with two; four, 1.6e-7, cost
-  // the 2048-row forward 7 % for their hand-overs, two 1 %). Pairs hold the sums in registers; single CTAs, where
-  // that many registers keep the next launch from starting early (16 rows: 195 us, 174 without), use all of
-  // tensor memory for the two of a tile, and the epilogue folds the first into the second at once and hands it back.
-  a.seg = INT32_MAX / BK * BK;
+  // The tensor cores' fp32 accumulation cuts instead of rounding: a sum of positive terms loses 2^-24 of its size for every
+  // step of 16 (measured: 9.7e-4 over 2^18 terms), so that no accumulator may take all of a long reduction.
+  //  * Results in 16 bits: one accumulator for every 16384 terms, 6e-5 at most, an eighth of fp16's rounding; the epilogue
+  //    adds them up in the other accumulator's place, which costs a long tile the overlap of the two.
+  //  * Weight gradients in fp32: one for every 512 rows, added to what the tile has stored.
+  //  * Losses: one for every 2048 of d (their relative error at d 4096: 9.3e-7 with one accumulator, 4.6e-7 with two; four,
+  //    1.6e-7, cost the 2048-row forward 7 % for their hand-overs, two 1 %). Pairs hold the sums in registers; single
+  //    CTAs, where that many registers keep the next launch from starting early (16 rows: 195 us, 174 without), use all
+  //    of tensor memory for the two of a tile, and the epilogue folds the first into the second at once and hands it
+  //    back. A longer d is added up as for 16 bits.
+  a.seg = kSegFold;
   a.accs = 1;
-  if (p.epi == MM_EPI_STATS && cg == 2) a.seg = kSegStats;
-  if (p.epi == MM_EPI_STATS && cg == 1 && p.red > kSegStats) a.seg = (p.red + 2 * BK - 1) / (2 * BK) * BK, a.accs = 2;
-  if (ep.out_f32 && !ep.acc_in && p.rag == MM_RAG_RED) a.seg = kSegStore;
+  if (p.epi == MM_EPI_STATS && (cg == 2 || p.red > 2 * kSegStats))
+    a.seg = kSegStats, a.fold = cg == 1;
+  else if (p.epi == MM_EPI_STATS && p.red > kSegStats)
+    a.seg = (p.red + 2 * BK - 1) / (2 * BK) * BK, a.accs = 2;
+  else if (ep.out_f32 && !ep.acc_in && p.rag == MM_RAG_RED)
+    a.seg = kSegStore;
+  else
+    a.fold = 1;
   if (a.split > 1) {
     const int64_t most = a.lane_tiles * (p.rag == MM_RAG_COLS ? (int64_t)std::min(p.groups, p.cols) : a.col_tiles);
     return gen ? launch_epi<1, true>(ta, tb, a, (int)most * a.split, s) : launch_epi<1, false>(ta, tb, a, (int)most * a.split, s);

@@ -146,3 +146,115 @@ def test_the_tail_of_gelus_slope(dtype):
     off = TAIL * (cdf + (z.double() * phi).abs()) + 2.0 ** -23 * want.abs()
     sub = 2.0 ** -25 if dtype == "fp16" else 2.0 ** -133
     assert bool(((got - want).abs() <= ULP[dtype] * want.abs() + off + sub).all())
+
+
+# The tensor cores' fp32 sums cut what they cannot hold instead of rounding: a step of 16 terms loses up to a unit, 2^-23
+# of the sum so far. A result may have collected that over 2^14 terms, 2^10 steps of half the sum on average, 2^-14 in
+# all; what is added up beyond them is rounded, 2^-24 for each of at most 2^10 additions. On top comes the one rounding
+# of the result, and the inputs of these sums are positive, so that the loss cannot average out.
+CUT = 2.0 ** -14 + 2.0 ** -14
+
+
+def _positive(shape, dtype, seed, scale=1.0):
+    return ((torch.rand(shape, generator=gen(seed), device="cuda") + 0.5) * scale).to(DT[dtype])
+
+
+def _check_long(got, a, b, dtype, extra=0.0):
+    want = torch.zeros(got.shape, dtype=torch.float64, device="cuda") + extra
+    for i in range(0, a.shape[1], 1 << 16):
+        want += a[:, i:i + (1 << 16)].double() @ b[:, i:i + (1 << 16)].double().T
+    # rounding is monotone: the result lies between the rounded ends of what the fp32 sum may be (the few rounded additions
+    # may also lie above, 2^-25 for each of at most 2^8)
+    low, high = (want * (1 - CUT)).to(DT[dtype]), (want * (1 + 2.0 ** -17)).to(DT[dtype])
+    assert bool(((got >= low) & (got <= high)).all()), float(((got.double() - want) / want).abs().max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,n,k,skew", [((1 << 20) + 21, 72, 136, 0),    # a cluster shares the sum
+                                           ((1 << 18) + 5, 72, 136, 1),     # unaligned operands
+                                           ((1 << 17) + 100, 1024, 1032, 0)])  # pairs of CTAs
+def test_weight_gradients_of_many_rows(dtype, rows, n, k, skew):
+    dy, x = _positive((rows * n + skew,), dtype, 1, 2.0 ** -10), _positive((rows * k + skew,), dtype, 2, 2.0 ** -4)
+    dyv, xv = dy[skew:].view(rows, n), x[skew:].view(rows, k)
+    dw, db = torch.empty((n, k), dtype=x.dtype, device="cuda"), torch.empty(n, dtype=x.dtype, device="cuda")
+    size = api.ds4moe_linear_grad_workspace(rows, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    api.ds4moe_linear_grad(dy.data_ptr() + 2 * skew, x.data_ptr() + 2 * skew, None, None, None, dw, db, rows, n, k, "none", dtype, ws, size, stream=stream())
+    _check_long(dw, dyv.T, xv.T, dtype)
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("skew", [0, 1])
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("n,k", [(136, 72), (520, 264)])
+def test_experts_with_many_rows_beside_experts_with_few(dtype, skew, accumulate, n, k):
+    counts = [5, (1 << 18) + 37, 0, 130, 16384, 16385, 1, 40000, 64, 300, 0, 33000, 2]
+    rows, g = sum(counts), len(counts)
+    dy, x = _positive((rows * n + skew,), dtype, 1, 2.0 ** -5), _positive((rows * k + skew,), dtype, 2, 2.0 ** -4)
+    dyv, xv = dy[skew:].view(rows, n), x[skew:].view(rows, k)
+    dw = torch.full((g, n, k), 1.0, dtype=x.dtype, device="cuda")
+    again = dw.clone()
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32).cuda()
+    for out in (dw, again):
+        api.ds4moe_grouped_mm_dw(dy.data_ptr() + 2 * skew, x.data_ptr() + 2 * skew, off, out, rows, n, k, g, dtype, accumulate=accumulate, stream=stream())
+    assert torch.equal(dw, again)
+    lo = 0
+    for e, c in enumerate(counts):
+        if c or accumulate:
+            _check_long(dw[e], dyv[lo:lo + c].T, xv[lo:lo + c].T, dtype, 1.0 if accumulate else 0.0)
+        else:
+            assert not bool(dw[e].any())
+        lo += c
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,n,skew", [(1, 72, 0), (64, 200, 0), (300, 2056, 0), (33, 72, 1), (600, 1032, 1)])
+def test_products_of_long_rows(rows, n, skew):
+    """y over k, and dx over n."""
+    k, dtype = (1 << 18) + 24, "fp16"
+    x, w = _positive((rows * k + skew,), dtype, 1, 2.0 ** -8), _positive((n * k + skew,), dtype, 2, 2.0 ** -6)
+    xv, wv = x[skew:].view(rows, k), w[skew:].view(n, k)
+    y, z, bias, r = (torch.empty((rows, n), dtype=x.dtype, device="cuda") for _ in range(4))
+    bias, r = torch.full((n,), 0.5, dtype=x.dtype, device="cuda"), torch.full((rows, n), 0.25, dtype=x.dtype, device="cuda")
+    api.ds4moe_linear(x.data_ptr() + 2 * skew, w.data_ptr() + 2 * skew, bias, r, y, rows, n, k, "relu", dtype, z, stream=stream())
+    _check_long(z, xv, wv, dtype, 0.5)
+    _check_long(y, xv, wv, dtype, 0.75)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    api.ds4moe_grouped_mm(x.data_ptr() + 2 * skew, w.data_ptr() + 2 * skew, off, y, rows, n, k, 1, dtype, stream=stream())
+    _check_long(y, xv, wv, dtype)
+    # the same matrices the other way round: w as the gradient [n, k] of n rows, x as weights [k, rows] read across
+    wt = torch.empty(k * rows + skew, dtype=x.dtype, device="cuda")
+    wt[skew:].view(k, rows).copy_(xv.T)
+    dx = torch.empty((n, rows), dtype=x.dtype, device="cuda")
+    off = torch.tensor([0, n // 3, n], dtype=torch.int32, device="cuda")
+    both = torch.cat([wt[skew:], wt[skew:]])
+    src = both if skew == 0 else torch.cat([both[:1], both])
+    api.ds4moe_grouped_mm_dx(w.data_ptr() + 2 * skew, src.data_ptr() + 2 * skew, off, dx, n, k, rows, 2, dtype, stream=stream())
+    _check_long(dx, wv, xv, dtype)
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,pad", [(3, 0), (130, 0), (20, 1)])
+def test_losses_over_long_rows(rows, pad):
+    """The logits of a long d, of one sign: a logit may have lost what 2^14 terms cut, and half as much in the loss's own
+    shorter sums. The labels' probability and the gradients follow within that error of the exponent."""
+    vocab, d = 300, (1 << 17) + 8
+    x, w = _positive((rows, d), "bf16", 1, 2.0 ** -8), _positive((vocab, d), "bf16", 2, 2.0 ** -6)
+    w *= torch.linspace(0.98, 1.0, vocab, device="cuda")[:, None].to(w.dtype)
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    dloss = torch.ones(rows, device="cuda")
+    loss, lse, dx, dw = _ce(x, w, labels, dloss, "bf16", pad=pad)
+    z = x.double() @ w.double().T
+    want = torch.logsumexp(z, 1)
+    # accumulators of 2^11 to 2^12 terms: 2^-17 to 2^-16 of a logit (about 8), rounded additions 2^-24 * 64 more
+    tol = (2.0 ** -16 + 2.0 ** -18) * z.max() + 2.0 ** -21 * (1 + want.abs().max())
+    assert float((lse - want).abs().max()) <= float(tol)
+    own = z.gather(1, labels.long()[:, None])[:, 0]
+    assert float((loss - (want - own)).abs().max()) <= 2 * float(tol)
+    p = torch.softmax(z, 1)
+    dz = p.scatter_add(1, labels.long()[:, None], -torch.ones((rows, 1), dtype=torch.float64, device="cuda"))
+    for got, ref, terms in ((dx, dz @ w.double(), dz.abs() @ w.double()), (dw, dz.T @ x.double(), dz.abs().T @ x.double())):
+        # the exponents are off by the logit's and the lse's error, dz is rounded (2^-9), the result too
+        assert bool(((got.double() - ref).abs() <= ULP["bf16"] * ref.abs() + (2.0 ** -9 + CUT * z.max() + tol + 2.0 ** -14) * terms + 1e-30).all())
+    assert api.ds4moe_ops_status() == 0
