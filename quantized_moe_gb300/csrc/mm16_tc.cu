@@ -1297,21 +1297,23 @@ cudaError_t prepare_epi() {
 
 // The column tile with the shortest schedule: rounds over the SMs times a tile's columns (and what a tile costs
 // whatever its width, about 24 columns' time). Widths that are no multiple of 64 run at the next larger one's rate
-// (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us).
+// (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us). Groups of a ragged reduction (0: a dense product, the only
+// one whose last round is split) run on single CTAs, where a tile costs 200 columns more, the loads of its 128 lanes
+// (one group, 8192 rows, 4096 x 4096: 256 columns 189 us in 4 rounds, 192 194 us in 5, 128 238 us in 7).
 struct Schedule {
   int64_t cost;  // columns' time
   int bn, tail_lg, tail_from;
 };
 Schedule schedule(int64_t lane_tiles, int cols, bool b_red, int groups, int cg, int units) {
   Schedule best = {INT64_MAX, 256, 0, 0};
-  const int grain = b_red ? 64 : 64 * cg;
+  const int grain = b_red ? 64 : 64 * cg, fixed = groups ? 200 : 24;
   for (int bn = 256; bn >= grain; bn -= grain) {
-    const int64_t tiles = lane_tiles * ((cols + bn - 1) / bn) * groups;
+    const int64_t tiles = lane_tiles * ((cols + bn - 1) / bn) * std::max(1, groups);
     const int64_t tail = tiles % units;
     // the last, partial round of a dense product: its tiles are split while all parts still fit one round
     int lg = 0;
-    while (groups == 1 && tail && lg < 2 && (tail << (lg + 1)) <= units && (bn >> (lg + 1)) % grain == 0) ++lg;
-    const int64_t cost = tiles / units * (bn + 24) + (tail ? (bn >> lg) + 24 : 0);
+    while (groups == 0 && tail && lg < 2 && (tail << (lg + 1)) <= units && (bn >> (lg + 1)) % grain == 0) ++lg;
+    const int64_t cost = tiles / units * (bn + fixed) + (tail ? (bn >> lg) + fixed : 0);
     if (cost < best.cost) best = {cost, bn, lg, (int)std::min<int64_t>(tiles - tail, INT32_MAX)};
   }
   return best;
@@ -1323,7 +1325,7 @@ int64_t mm_cost(int lanes, int cols, int red, bool b_red) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   const int cg = lanes > BM && g_pairs[dev & 63] > 0 ? 2 : 1, units = std::max(1, cg == 2 ? g_pairs[dev & 63] : g_sms[dev & 63]);
-  return schedule((lanes + BM * cg - 1) / (BM * cg), cols, b_red, 1, cg, units).cost * ((red + BK - 1) / BK + 4);
+  return schedule((lanes + BM * cg - 1) / (BM * cg), cols, b_red, 0, cg, units).cost * ((red + BK - 1) / BK + 4);
 }
 
 cudaError_t mm_prepare() {
@@ -1393,7 +1395,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
   } else if (p.epi != MM_EPI_STATS) {
-    const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 1, cg, units);
+    const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 0, cg, units);
     a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;
   }
   a.stages = 1;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_mm16 import DT, ULP, _ce, _ce_check, gen, normal, stream
+from test_gpu_mm16 import DT, ULP, _ce, _ce_check, gen, normal, stream, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -258,3 +258,17 @@ def test_losses_over_long_rows(rows, pad):
         # the exponents are off by the logit's and the lse's error, dz is rounded (2^-9), the result too
         assert bool(((got.double() - ref).abs() <= ULP["bf16"] * ref.abs() + (2.0 ** -9 + CUT * z.max() + tol + 2.0 ** -14) * terms + 1e-30).all())
     assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("n,k", [(1024, 1024), (2304, 512), (1000, 520), (4096, 256), (2056, 1544)])
+@pytest.mark.parametrize("out_dtype", ["bf16", "fp32"])
+def test_weight_gradients_of_one_group(n, k, out_dtype):
+    """One group's last round of tiles is not split as a dense product's is, whatever width its tiles have."""
+    rows, used = 300, 287
+    x, dy = whole((rows, k), "bf16", 1), whole((rows, n), "bf16", 2)
+    x[used:], dy[used:] = float("nan"), float("nan")
+    dw = torch.full((n * k + 64,), 7.0, dtype=DT[out_dtype], device="cuda")
+    off = torch.tensor([0, used], dtype=torch.int32, device="cuda")
+    api.ds4moe_grouped_mm_dw(dy, x, off, dw, rows, n, k, 1, "bf16", out_dtype, stream=stream())
+    assert torch.equal(dw[:n * k].view(n, k), (dy[:used].double().T @ x[:used].double()).to(DT[out_dtype]))
+    assert bool((dw[n * k:] == 7.0).all()) and api.ds4moe_ops_status() == 0
