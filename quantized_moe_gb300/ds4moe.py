@@ -260,21 +260,44 @@ def _enum(table: dict, v) -> int:
 
 # Operators on 16-bit matrices (see the header for the mathematics, layouts and limits). dtype and act
 # are names ("bf16", "fp16"; "none", "relu", "silu", "gelu") or the ABI's numbers; a row distance of 0
-# means that the rows lie back to back.
+# means that the rows lie back to back. Tensors may be views: one whose strides are not those that the call
+# gives (elements of a row apart from each other, rows at another distance) is refused.
+
+
+def _operand(a, ld: int = 0, step: int = 0) -> Optional[int]:
+    """The address of a vector, of a matrix with rows `ld` apart or of a stack of matrices `step` apart."""
+    if a is None or type(a) is int:
+        return a
+    try:
+        if a.is_contiguous():  # (a buffer: the call alone says how it is read)
+            return a.data_ptr()
+    except AttributeError:
+        return _ptr(a)
+    strides = a.stride()
+    if strides == (ld, 1):
+        return a.data_ptr()
+    shape = tuple(a.shape)
+    want = (ld or shape[-1], 1)[-len(shape):]
+    while len(want) < len(shape):
+        want = (len(want) == 2 and step or shape[-len(want)] * want[0],) + want
+    if any(n > 1 and have != w for n, have, w in zip(shape, strides, want)):
+        raise ValueError(f"a tensor of shape {shape} has strides {strides}, the call reads it with {want}")
+    return a.data_ptr()
 
 
 def ds4moe_grouped_mm(x, w, offsets, y, rows: int, n: int, k: int, n_groups: int, dtype="bf16", ldx: int = 0,
                       ldw: int = 0, w_stride: int = 0, ldy: int = 0, stream: int = 0) -> None:
     """y[t] = W_g x[t] for the rows t of each group g."""
-    _check(lib().ds4moe_grouped_mm(_ptr(x), _ptr(w), _ptr(offsets), _ptr(y), rows, n, k, n_groups,
-                                   _enum(DTYPES, dtype), ldx, ldw, w_stride, ldy, stream))
+    _check(lib().ds4moe_grouped_mm(_operand(x, ldx), _operand(w, ldw, w_stride), _operand(offsets), _operand(y, ldy),
+                                   rows, n, k, n_groups, _enum(DTYPES, dtype), ldx, ldw, w_stride, ldy, stream))
 
 
 def ds4moe_grouped_mm_dx(dy, w, offsets, dx, rows: int, n: int, k: int, n_groups: int, dtype="bf16", lddy: int = 0,
                          ldw: int = 0, w_stride: int = 0, lddx: int = 0, stream: int = 0) -> None:
     """dx[t] = W_g^T dy[t] for the rows t of each group g."""
-    _check(lib().ds4moe_grouped_mm_dx(_ptr(dy), _ptr(w), _ptr(offsets), _ptr(dx), rows, n, k, n_groups,
-                                      _enum(DTYPES, dtype), lddy, ldw, w_stride, lddx, stream))
+    _check(lib().ds4moe_grouped_mm_dx(_operand(dy, lddy), _operand(w, ldw, w_stride), _operand(offsets),
+                                      _operand(dx, lddx), rows, n, k, n_groups, _enum(DTYPES, dtype), lddy, ldw,
+                                      w_stride, lddx, stream))
 
 
 def ds4moe_grouped_mm_dw(dy, x, offsets, dw, rows: int, n: int, k: int, n_groups: int, dtype="bf16", dw_dtype=None,
@@ -282,7 +305,8 @@ def ds4moe_grouped_mm_dw(dy, x, offsets, dw, rows: int, n: int, k: int, n_groups
                          stream: int = 0) -> None:
     """dW_g = sum over the rows t of group g of dy[t] x[t]^T (added to dw with accumulate)."""
     dt = _enum(DTYPES, dtype)
-    _check(lib().ds4moe_grouped_mm_dw(_ptr(dy), _ptr(x), _ptr(offsets), _ptr(dw), rows, n, k, n_groups, dt,
+    _check(lib().ds4moe_grouped_mm_dw(_operand(dy, lddy), _operand(x, ldx), _operand(offsets),
+                                      _operand(dw, lddw, dw_stride), rows, n, k, n_groups, dt,
                                       dt if dw_dtype is None else _enum(DTYPES, dw_dtype), int(bool(accumulate)),
                                       lddy, ldx, lddw, dw_stride, stream))
 
@@ -290,8 +314,9 @@ def ds4moe_grouped_mm_dw(dy, x, offsets, dw, rows: int, n: int, k: int, n_groups
 def ds4moe_linear(x, w, bias, residual, y, rows: int, n: int, k: int, act="none", dtype="bf16", zout=None,
                   ldx: int = 0, ldw: int = 0, ldr: int = 0, ldy: int = 0, ldz: int = 0, stream: int = 0) -> None:
     """y = act(W x + bias) + residual; zout receives W x + bias."""
-    _check(lib().ds4moe_linear(_ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(zout), rows, n, k,
-                               _enum(ACTS, act), _enum(DTYPES, dtype), ldx, ldw, ldr, ldy, ldz, stream))
+    _check(lib().ds4moe_linear(_operand(x, ldx), _operand(w, ldw), _operand(bias), _operand(residual, ldr),
+                               _operand(y, ldy), _operand(zout, ldz), rows, n, k, _enum(ACTS, act),
+                               _enum(DTYPES, dtype), ldx, ldw, ldr, ldy, ldz, stream))
 
 
 def ds4moe_linear_grad_workspace(rows: int, n: int, act="none") -> int:
@@ -302,9 +327,10 @@ def ds4moe_linear_grad(dy, x, w, z, dx, dw, db, rows: int, n: int, k: int, act="
                        workspace=None, workspace_bytes: int = 0, lddy: int = 0, ldx: int = 0, ldw: int = 0,
                        ldz: int = 0, lddx: int = 0, lddw: int = 0, stream: int = 0) -> None:
     """Gradients of ds4moe_linear: dx, dw and db (each may be None)."""
-    _check(lib().ds4moe_linear_grad(_ptr(dy), _ptr(x), _ptr(w), _ptr(z), _ptr(dx), _ptr(dw), _ptr(db), rows, n, k,
+    _check(lib().ds4moe_linear_grad(_operand(dy, lddy), _operand(x, ldx), _operand(w, ldw), _operand(z, ldz),
+                                    _operand(dx, lddx), _operand(dw, lddw), _operand(db), rows, n, k,
                                     _enum(ACTS, act), _enum(DTYPES, dtype), lddy, ldx, ldw, ldz, lddx, lddw,
-                                    _ptr(workspace), workspace_bytes, stream))
+                                    _operand(workspace), workspace_bytes, stream))
 
 
 def ds4moe_cross_entropy_workspace(rows: int, vocab: int, d: int) -> int:
@@ -315,18 +341,19 @@ def ds4moe_cross_entropy(x, w, labels, loss, lse, rows: int, vocab: int, d: int,
                          ignore_index: int = -100, workspace=None, workspace_bytes: int = 0, ldx: int = 0,
                          ldw: int = 0, stream: int = 0) -> None:
     """loss[t] = lse[t] - z[t][labels[t]] of the logits z = W x, which are not stored."""
-    _check(lib().ds4moe_cross_entropy(_ptr(x), _ptr(w), _ptr(labels), _ptr(loss), _ptr(lse), rows, vocab, d,
-                                      _enum(DTYPES, dtype), ignore_index, ldx, ldw, _ptr(workspace),
-                                      workspace_bytes, stream))
+    _check(lib().ds4moe_cross_entropy(_operand(x, ldx), _operand(w, ldw), _operand(labels), _operand(loss),
+                                      _operand(lse), rows, vocab, d, _enum(DTYPES, dtype), ignore_index, ldx,
+                                      ldw, _operand(workspace), workspace_bytes, stream))
 
 
 def ds4moe_cross_entropy_grad(x, w, labels, lse, dloss, dx, dw, rows: int, vocab: int, d: int, dtype="bf16",
                               ignore_index: int = -100, workspace=None, workspace_bytes: int = 0, ldx: int = 0,
                               ldw: int = 0, lddx: int = 0, lddw: int = 0, stream: int = 0) -> None:
     """Gradients of sum_t dloss[t] loss[t] with respect to x and w (each may be None)."""
-    _check(lib().ds4moe_cross_entropy_grad(_ptr(x), _ptr(w), _ptr(labels), _ptr(lse), _ptr(dloss), _ptr(dx),
-                                           _ptr(dw), rows, vocab, d, _enum(DTYPES, dtype), ignore_index, ldx, ldw,
-                                           lddx, lddw, _ptr(workspace), workspace_bytes, stream))
+    _check(lib().ds4moe_cross_entropy_grad(_operand(x, ldx), _operand(w, ldw), _operand(labels), _operand(lse),
+                                           _operand(dloss), _operand(dx, lddx), _operand(dw, lddw), rows, vocab, d,
+                                           _enum(DTYPES, dtype), ignore_index, ldx, ldw, lddx, lddw,
+                                           _operand(workspace), workspace_bytes, stream))
 
 
 def ds4moe_ops_status() -> int:
