@@ -106,12 +106,9 @@ __device__ __forceinline__ float mm_gelu(float z) {
   return z > 0.f ? z - away : z == z ? -away : z;
 }
 
-__device__ __forceinline__ float mm_act(float z, int act) {
-  if (act == MM_ACT_RELU) return z > 0.f ? z : z == z ? 0.f : z;  // NaN stays NaN
-  if (act == MM_ACT_SILU) return z / (1.f + __expf(-z));
-  if (act == MM_ACT_GELU) return mm_gelu(z);
-  return z;
-}
+__device__ __forceinline__ float mm_relu(float z) { return z > 0.f ? z : z == z ? 0.f : z; }  // (NaN stays NaN)
+// silu with the hardware exponential and division: a few units of 2^-22, and 0 instead of a value below 2^-118.
+__device__ __forceinline__ float mm_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 // dy * act'(z). z is what its type kept of an fp32 value, so that it may be infinite where the forward was finite: the
 // slope's limits are 0 and 1 there. z times a slope's factor that has run to 0 is taken at +-256, where that factor is
 // already 0 in fp32 (infinity times 0 would be NaN). NaN stays NaN; a place that relu closes passes nothing, whatever lies

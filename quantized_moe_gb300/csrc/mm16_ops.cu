@@ -1,5 +1,5 @@
 // C entry points of the operators on 16-bit matrices: argument checks, workspace layout and the
-// sequence of launches. Host code only.
+// sequence of launches. Host code, and the device word that the kernels raise flags in.
 #include <algorithm>
 #include <mutex>
 #include <string>

@@ -57,7 +57,8 @@ constexpr int kPartLd = BM + 4;           // floats from one column of a partial
 constexpr int kOutBytes = 32 * kRowBytes;  // 32 columns of 128 lanes on their way out, one per half of the epilogue
 constexpr int kSmemMax = 232448;
 
-// n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d).
+// n / d for 0 <= n < 2^31 by a multiplication: m = floor(2^32 (2^l - d) / d) + 1, l = ceil(log2 d) (T. Granlund and
+// P. L. Montgomery, Division by Invariant Integers using Multiplication, 1994).
 struct Divider {
   uint32_t m, l;
   Divider() = default;
@@ -427,9 +428,6 @@ __device__ __forceinline__ void add32(float (&v)[32], const float* q, int64_t ld
   for (int j = 0; j < 32; ++j) v[j] += h[j];
 }
 
-// silu with the hardware exponential and division: a few units of 2^-22, and 0 instead of a value below 2^-118.
-__device__ __forceinline__ float silu_fast(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-
 // Writes 32 columns (nv exist for this lane) of lane l.
 __device__ __forceinline__ void put(const MmProblem& p, int g, int l, int c, int nv, const float (&v)[32]) {
   const MmEpiArgs& e = p.e;
@@ -466,13 +464,13 @@ __device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int 
   }
   if (e.act == MM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = silu_fast(v[j]);
+    for (int j = 0; j < 32; ++j) v[j] = mm_silu(v[j]);
   } else if (e.act == MM_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], MM_ACT_GELU);
+    for (int j = 0; j < 32; ++j) v[j] = mm_gelu(v[j]);
   } else if (e.act == MM_ACT_RELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], MM_ACT_RELU);
+    for (int j = 0; j < 32; ++j) v[j] = mm_relu(v[j]);
   }
   if (e.residual) add16(v, e.residual, (int64_t)c * e.ldr + l, e.ldr, nv, p.f16);
   if (accumulate) {
@@ -1130,17 +1128,17 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = silu_fast(f.v[j][r][0]), f.v[j][r][1] = silu_fast(f.v[j][r][1]);
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_silu(f.v[j][r][0]), f.v[j][r][1] = mm_silu(f.v[j][r][1]);
               } else if (e.act == MM_ACT_GELU) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_GELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_GELU);
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_gelu(f.v[j][r][0]), f.v[j][r][1] = mm_gelu(f.v[j][r][1]);
               } else if (e.act == MM_ACT_RELU) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_act(f.v[j][r][0], MM_ACT_RELU), f.v[j][r][1] = mm_act(f.v[j][r][1], MM_ACT_RELU);
+                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_relu(f.v[j][r][0]), f.v[j][r][1] = mm_relu(f.v[j][r][1]);
               }
               if (add) {
                 rows.stage(next);
@@ -1371,7 +1369,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   TcArgs a = {};
   a.p = p;
   const bool gen = p.red <= 0 || !mm_aligned(p.a) || !mm_aligned(p.b);
-  // Few tiles: the reduction of a tile is split over a cluster of CTAs, as many as keep every SM busy once, with four
+  // Few tiles: the reduction of a tile is split over a cluster of CTAs, as many as keep every SM busy once, with six
   // stages each at least.
   a.split = 1;
   const int64_t lanes128 = (p.lanes + BM - 1) / BM;

@@ -1,5 +1,5 @@
 // Inline-PTX wrappers for the sm_103a tensor-core path: mbarriers (with bounded waits), TMA and
-// bulk copies, tcgen05 MMA / TMEM loads and stores. Only the prefill GEMM includes this header.
+// bulk copies, tcgen05 MMA / TMEM loads and stores, shared by the prefill GEMM and the 16-bit products.
 #pragma once
 
 #include <cuda.h>
