@@ -272,3 +272,37 @@ def test_weight_gradients_of_one_group(n, k, out_dtype):
     api.ds4moe_grouped_mm_dw(dy, x, off, dw, rows, n, k, 1, "bf16", out_dtype, stream=stream())
     assert torch.equal(dw[:n * k].view(n, k), (dy[:used].double().T @ x[:used].double()).to(DT[out_dtype]))
     assert bool((dw[n * k:] == 7.0).all()) and api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,vocab,d,pad,dtype", [
+    (16, 80001, 2056, 0, "bf16"), (1, 45000, 4096, 0, "fp16"), (128, 45000, 4096, 0, "bf16"), (16, 80001, 4104, 0, "bf16"),
+    (100, 41000, 6200, 0, "fp16"), (20, 45000, 2100, 3, "bf16"), (200, 41000, 4200, 3, "fp16")])
+def test_losses_of_few_rows_over_a_wide_model(rows, vocab, d, pad, dtype):
+    """A token's logits take two accumulators side by side (d above 2048) or one after the other (above 4096), on
+    single CTAs, and there are more tiles of the vocabulary than SMs: both accumulators are used again."""
+    x, w = normal((rows, d), dtype, 1), normal((vocab, d), dtype, 2, 2.0 * d ** -0.5)
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    if rows > 1:
+        labels[::7] = -100
+        labels[1], labels[rows - 1] = vocab - 1, 0
+    dloss = torch.rand(rows, generator=gen(4), device="cuda") / rows
+    got = _ce(x, w, labels, dloss, dtype, pad=pad)
+    _ce_check(x, w, labels, dloss, dtype, got)
+    again = _ce(x, w, labels, dloss, dtype, pad=pad)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,d,pad", [(16, 512, 0), (40, 520, 0), (9, 136, 3), (33, 1000, 0)])
+@pytest.mark.parametrize("piece", [768, 1024, 2560])
+def test_pieces_that_split_their_sums_over_a_cluster(rows, d, pad, piece):
+    """dx of few rows, piece after piece of the vocabulary: each piece's sum is shared out over the CTAs of a cluster and
+    added to the one before it in fp32."""
+    vocab = 10007
+    x, w = normal((rows, d), "bf16", 1), normal((vocab, d), "bf16", 2, d ** -0.5)
+    labels = torch.randint(0, vocab, (rows,), generator=gen(3), device="cuda", dtype=torch.int32)
+    labels[::5] = -100
+    dloss = torch.rand(rows, generator=gen(4), device="cuda")
+    size = 16 + (4 * rows * d + 15) // 16 * 16 + 2 * ((rows + 7) // 8 * 8) * piece
+    _ce_check(x, w, labels, dloss, "bf16", _ce(x, w, labels, dloss, "bf16", ws_bytes=size, pad=pad))
+    assert api.ds4moe_ops_status() == 0
