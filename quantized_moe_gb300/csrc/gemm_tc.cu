@@ -15,8 +15,9 @@
 // tensor pipe, bounds the stage rate. The A stages have their own full barrier (the two dequant
 // groups that wrote the sub-tiles) and empty barrier (MMA commit), and so have the activation
 // stages (TMA bytes; MMA commit), so that the activation ring can run a stage further ahead.
-// With an even number of weight slices the CTAs run in clusters of two on adjacent slices of the
-// same token tile and each loads half of every activation stage, multicast to both.
+// Every CTA loads its own activation stages: CTAs on adjacent weight slices of the same token tile run side by side and
+// find the tile in L2. (Clusters that shared the loads by multicast gained 0.7 % of a 4096-token forward, 1.774 -> 1.762 ms,
+// and nothing of a 512-token one; the same library serves the ranks of a job on several GPUs, which have no such loads.)
 // Warp roles (23 warps):
 //   warp 0     weight producer: bulk-copies the packed weight units of each K unit (256 k for
 //              Q2_K, 128 k for Q8_0) of the tile's rows;
@@ -110,7 +111,7 @@ struct Bars {
   uint64_t* a_full;     // [A_STAGES] the dequant groups' warps -> MMA
   uint64_t* a_empty;    // [A_STAGES] MMA commit -> dequant groups
   uint64_t* b_full;     // [B_STAGES] activation TMA (with its bytes) -> MMA
-  uint64_t* b_empty;    // [B_STAGES] MMA commits of every CTA of the cluster -> activation producer
+  uint64_t* b_empty;    // [B_STAGES] MMA commits -> activation producer
   uint64_t* raw_full;   // [RAWS] weight bulk copy -> dequant
   uint64_t* raw_empty;  // [RAWS] dequant -> producer
   uint64_t* acc_full;   // [2] MMA -> epilogue
@@ -246,12 +247,7 @@ __device__ __forceinline__ int item_count(const GemmArgs& p) {
   return tiles * p.m_tiles;
 }
 
-// CS = 1, or the size (2 or 4) of a cluster of CTAs that take adjacent weight slices of the same
-// token tile (items CS c + r + k G, r < CS, the weight slices fastest and their count a multiple
-// of CS): each loads its share of the rows of every activation stage and multicasts it to all,
-// and each MMA commit releases the stage in all of them, so the activation tile crosses L2 once
-// per cluster.
-template <int FMT, bool GATEUP, int CS, int GEOM>
+template <int FMT, bool GATEUP, int GEOM>
 __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap16,
                                                                       const __grid_constant__ CUtensorMap tmap32,
                                                                       const __grid_constant__ CUtensorMap tmap64,
@@ -293,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
     }
     for (int i = 0; i < BS; ++i) {
       mbar_init(&b.b_full[i], 1);
-      mbar_init(&b.b_empty[i], CS);  // the MMA commit of every CTA of the cluster
+      mbar_init(&b.b_empty[i], 1);
     }
     for (int r = 0; r < RAWS; ++r) {
       mbar_init(&b.raw_full[r], 1);
@@ -311,20 +307,15 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
     tmem_relinquish();
   }
   tc_fence_before();
-  if (CS > 1)
-    cluster_sync();  // the peer's barriers are initialized before any multicast reaches them
-  else
-    __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int rank = CS > 1 ? (int)cluster_ctarank() : 0;
   if (warp == 2 && lane == 0) {  // the activation producer's descriptors, ahead of its first loads
     tmap_prefetch(&tmap16);
     tmap_prefetch(&tmap32);
     tmap_prefetch(&tmap64);
     tmap_prefetch(&tmap128);
   }
-  constexpr uint16_t kMask = (uint16_t)((1u << CS) - 1u);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ weight producer
@@ -352,26 +343,24 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
   } else if (warp == 2) {
     // ------------------------------------------------------------------ activation producer
     // The warp waits for a free stage together; lane 0 announces the stage's bytes and lane 8j + q
-    // issues box q of sub-tile j: the CTA's rows [lo, hi) of the MMA's N rows as boxes of 128,
+    // issues box q of sub-tile j: the MMA's N rows as boxes of 128,
     // 128, 64, 32 and 16 rows (those the length needs), so that all of a stage's loads go out in
     // one instruction instead of one after another from a single thread.
     uint32_t gs = 0;  // stages issued over all items
     const int j = lane >> 3, q = lane & 7;
     for (int it = blockIdx.x; it < n_items && !*abort_flag; it += gridDim.x) {
       const Item t = item_of<C::BN>(p, it);
-      const int rows = t.n;  // all of them land in this CTA
-      const int lo = 16 * ((rows / 16) * rank / CS), hi = 16 * ((rows / 16) * (rank + 1) / CS);
-      const int len = hi - lo, n128 = len / 128, rem = len - 128 * n128;
+      const int rows = t.n, n128 = rows / 128, rem = rows - 128 * n128;
       int r = -1;
       const CUtensorMap* map = &tmap16;
       if (q < 2) {
-        if (q < n128) r = lo + 128 * q, map = &tmap128;
+        if (q < n128) r = 128 * q, map = &tmap128;
       } else if (q == 2) {
-        if (rem & 64) r = lo + 128 * n128, map = &tmap64;
+        if (rem & 64) r = 128 * n128, map = &tmap64;
       } else if (q == 3) {
-        if (rem & 32) r = lo + 128 * n128 + (rem & 64), map = &tmap32;
+        if (rem & 32) r = 128 * n128 + (rem & 64), map = &tmap32;
       } else if (q == 4) {
-        if (rem & 16) r = lo + 128 * n128 + (rem & 96), map = &tmap16;
+        if (rem & 16) r = 128 * n128 + (rem & 96), map = &tmap16;
       }
       const bool issue = j < SUB && r >= 0;
       for (int sB = 0; sB < n_stages; ++sB, ++gs) {
@@ -381,10 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
         if (issue) {
           unsigned char* dst = smem + C::OFF_B + sb * C::B_BYTES + j * C::SUB_BYTES + r * BK * 2;
           const int x = (sB * SUB + j) * BK;
-          if (CS > 1)
-            tma_load_2d_mc(dst, map, x, t.row0 + r, &b.b_full[sb], kMask);
-          else
-            tma_load_2d(dst, map, x, t.row0 + r, &b.b_full[sb]);
+          tma_load_2d(dst, map, x, t.row0 + r, &b.b_full[sb]);
         }
       }
     }
@@ -423,15 +409,14 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
         for (int h = 0; h < SUB / 2; ++h)
           tc_mma8_ts_elect(acc, ta + 64 * h, sw128_desc(bsm + 2 * h * C::SUB_BYTES),
                            sw128_desc(bsm + (2 * h + 1) * C::SUB_BYTES), idesc, (s | h) != 0);
-        tc_commit2_elect(&b.b_empty[sb], CS > 1 ? kMask : 0, &b.a_empty[st]);
+        tc_commit2_elect(&b.b_empty[sb], &b.a_empty[st]);
       }
       if (!ok) break;
       tc_commit_elect(&b.acc_full[buf]);
     }
-    // The MMAs already issued must finish before TMEM is freed (after an abort), and in a cluster
-    // every commit of both CTAs must have reached its barriers before either CTA exits: the
-    // last stage's empty phase completes only then.
-    if ((*abort_flag || CS > 1) && gs > 0 && lane == 0)
+    // The MMAs already issued must finish before TMEM is freed (after an abort): the last stage's empty phase completes
+    // only then.
+    if (*abort_flag && gs > 0 && lane == 0)
       bounded_try(&b.b_empty[(gs - 1) % BS], ((gs - 1) / BS) & 1, limit);
     __syncwarp();
   } else if (warp < kFirstDeq + kDeqWarps) {
@@ -549,101 +534,40 @@ __global__ void __launch_bounds__(kThreads, 1) expert_gemm_tc_kernel(const __gri
     }
   }
   tc_fence_before();
-  if (CS > 1)
-    cluster_sync();  // no copy or commit of either CTA still targets the other's shared memory
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, TMEM_COLS);
 }
 
-template <int FMT, bool GATEUP, int CS, int GEOM>
+template <int FMT, bool GATEUP, int GEOM>
 cudaError_t launch_one(const ActMaps& tm, const GemmArgs& p, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Cfg<FMT, GEOM>::SMEM_BYTES;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CS > 1 ? 1 : 0;  // a plain launch without clusters
-  return cudaLaunchKernelEx(&cfg, expert_gemm_tc_kernel<FMT, GATEUP, CS, GEOM>, tm.r16, tm.r32, tm.r64, tm.r128, p);
+  return cudaLaunchKernelEx(&cfg, expert_gemm_tc_kernel<FMT, GATEUP, GEOM>, tm.r16, tm.r32, tm.r64, tm.r128, p);
 }
 
-// Clusters of CS CTAs that can be resident at once (0 if none).
-template <int FMT, bool GATEUP, int CS, int GEOM>
-int max_clusters() {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * CS);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Cfg<FMT, GEOM>::SMEM_BYTES;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CS;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, expert_gemm_tc_kernel<FMT, GATEUP, CS, GEOM>, &cfg) != cudaSuccess) {
-    cudaGetLastError();
-    return 0;
-  }
-  return n;
-}
-
-template <int FMT, bool GATEUP, int CS, int GEOM>
+template <int FMT, bool GATEUP, int GEOM>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(expert_gemm_tc_kernel<FMT, GATEUP, CS, GEOM>,
+  return cudaFuncSetAttribute(expert_gemm_tc_kernel<FMT, GATEUP, GEOM>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FMT, GEOM>::SMEM_BYTES);
 }
 
-// Per device, geometry and (format, gate/up or down) kernel: resident clusters of two and four.
-int g_pairs[64][2][4], g_quads[64][2][4];
-
-template <int FMT, bool GATEUP, int GEOM>
-cudaError_t prepare_fmt(int dev, int k) {
-  cudaError_t e = prepare_one<FMT, GATEUP, 1, GEOM>();
-  if (e == cudaSuccess) e = prepare_one<FMT, GATEUP, 2, GEOM>();
-  if (e == cudaSuccess) e = prepare_one<FMT, GATEUP, 4, GEOM>();
-  if (e == cudaSuccess && dev >= 0 && dev < 64) {
-    g_pairs[dev][GEOM][k] = max_clusters<FMT, GATEUP, 2, GEOM>();
-    g_quads[dev][GEOM][k] = max_clusters<FMT, GATEUP, 4, GEOM>();
-  }
+template <int GEOM>
+cudaError_t prepare_geom() {
+  cudaError_t e = prepare_one<FMT_Q2_K, true, GEOM>();
+  if (e == cudaSuccess) e = prepare_one<FMT_Q2_K, false, GEOM>();
+  if (e == cudaSuccess) e = prepare_one<FMT_Q8_0, true, GEOM>();
+  if (e == cudaSuccess) e = prepare_one<FMT_Q8_0, false, GEOM>();
   return e;
 }
 
 template <int GEOM>
-cudaError_t prepare_geom(int dev) {
-  cudaError_t e = prepare_fmt<FMT_Q2_K, true, GEOM>(dev, 0);
-  if (e == cudaSuccess) e = prepare_fmt<FMT_Q2_K, false, GEOM>(dev, 1);
-  if (e == cudaSuccess) e = prepare_fmt<FMT_Q8_0, true, GEOM>(dev, 2);
-  if (e == cudaSuccess) e = prepare_fmt<FMT_Q8_0, false, GEOM>(dev, 3);
-  return e;
-}
-
-template <int CS, int GEOM>
-cudaError_t launch_cs(int fmt, bool gateup, const ActMaps& tm, const GemmArgs& p, int grid, cudaStream_t s) {
+cudaError_t launch_geom(int fmt, bool gateup, const ActMaps& tm, const GemmArgs& p, int grid, cudaStream_t s) {
   if (fmt == FMT_Q2_K)
-    return gateup ? launch_one<FMT_Q2_K, true, CS, GEOM>(tm, p, grid, s)
-                  : launch_one<FMT_Q2_K, false, CS, GEOM>(tm, p, grid, s);
-  return gateup ? launch_one<FMT_Q8_0, true, CS, GEOM>(tm, p, grid, s) : launch_one<FMT_Q8_0, false, CS, GEOM>(tm, p, grid, s);
-}
-
-template <int GEOM>
-cudaError_t launch_geom(int fmt, bool gateup, const ActMaps& tm, const GemmArgs& p, int items, int m_tiles, int sms,
-                        int dev, cudaStream_t s) {
-  const bool known = dev >= 0 && dev < 64;
-  const int k = (fmt == FMT_Q2_K ? 0 : 2) + (gateup ? 0 : 1);
-  const int quads = known ? g_quads[dev][GEOM][k] : 0, pairs = known ? g_pairs[dev][GEOM][k] : 0;
-  if (!p.tiles && m_tiles % 4 == 0 && quads > 0)
-    return launch_cs<4, GEOM>(fmt, gateup, tm, p, 4 * std::max(1, std::min(quads, items / 4)), s);
-  if (m_tiles % 2 == 0 && pairs > 0)
-    return launch_cs<2, GEOM>(fmt, gateup, tm, p, 2 * std::max(1, std::min(pairs, items / 2)), s);
-  return launch_cs<1, GEOM>(fmt, gateup, tm, p, std::max(1, std::min(sms, items)), s);
+    return gateup ? launch_one<FMT_Q2_K, true, GEOM>(tm, p, grid, s) : launch_one<FMT_Q2_K, false, GEOM>(tm, p, grid, s);
+  return gateup ? launch_one<FMT_Q8_0, true, GEOM>(tm, p, grid, s) : launch_one<FMT_Q8_0, false, GEOM>(tm, p, grid, s);
 }
 
 }  // namespace
@@ -656,18 +580,13 @@ int gemm_geometry(int n_tokens, int top_k, int n_experts, int k_gcd) {
 }
 
 cudaError_t gemm_prepare() {
-  int dev = 0;
-  cudaGetDevice(&dev);
-  cudaError_t e = prepare_geom<0>(dev);
-  if (e == cudaSuccess) e = prepare_geom<1>(dev);
+  cudaError_t e = prepare_geom<0>();
+  if (e == cudaSuccess) e = prepare_geom<1>();
   return e;
 }
 
 // Persistent launch: one CTA per SM (at most), each looping over the (token tile, weight slice)
-// items; n_tiles bounds the token tiles (the routed count itself is read on the device). When the
-// weight slices divide evenly, the CTAs run in clusters that share the activation loads: of four
-// for the dense (shared expert) GEMMs, of two for the routed ones (measured: clusters of four leave
-// more SMs idle than the routed GEMMs gain from the smaller activation traffic).
+// items; n_tiles bounds the token tiles (the routed count itself is read on the device).
 cudaError_t launch_gemm(int fmt, bool gateup, const ActMaps& tm, const GemmArgs& args, int m_tiles, int n_tiles,
                         int geom, cudaStream_t s) {
   static int n_sm[64] = {};
@@ -678,9 +597,8 @@ cudaError_t launch_gemm(int fmt, bool gateup, const ActMaps& tm, const GemmArgs&
   const int sms = (known && n_sm[dev] > 0) ? n_sm[dev] : 152;
   GemmArgs p = args;
   p.m_tiles = m_tiles;
-  const int items = m_tiles * n_tiles;
-  return geom ? launch_geom<1>(fmt, gateup, tm, p, items, m_tiles, sms, dev, s)
-              : launch_geom<0>(fmt, gateup, tm, p, items, m_tiles, sms, dev, s);
+  const int grid = std::max(1, std::min(sms, m_tiles * n_tiles));
+  return geom ? launch_geom<1>(fmt, gateup, tm, p, grid, s) : launch_geom<0>(fmt, gateup, tm, p, grid, s);
 }
 
 // fp16 2D tensor map over a row-major [rows x cols] buffer, boxes of 64 columns x box_rows rows

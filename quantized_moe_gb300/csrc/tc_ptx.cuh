@@ -73,16 +73,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar))
       : "memory");
 }
-// The same load multicast to every CTA of the cluster named in mask: the box lands at the same
-// shared-memory offset in each, and each CTA's mbarrier at bar's offset receives the bytes.
-__device__ __forceinline__ void tma_load_2d_mc(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
-                                               uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      " [%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(su32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(su32(bar)), "h"(mask)
-      : "memory");
-}
 
 // Brings a tensor map's descriptor into the TMA unit's cache before its first use.
 __device__ __forceinline__ void tmap_prefetch(const CUtensorMap* map) {
@@ -167,24 +157,14 @@ __device__ __forceinline__ void tc_mma8_ts_elect(uint32_t d_tmem, uint32_t a_tme
       : "memory");
 }
 
-// The commits that release a stage: a multicast commit to the activation stage's barrier in every
-// CTA of the cluster in mask (or a plain one if mask is 0) and a commit to the local A stage's
-// barrier, issued by one elected lane.
-__device__ __forceinline__ void tc_commit2_elect(uint64_t* b_bar, uint16_t mask, uint64_t* a_bar) {
-  if (mask)
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%2];\n}\n" ::"r"(su32(b_bar)),
-        "h"(mask), "r"(su32(a_bar))
-        : "memory");
-  else
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
-        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(su32(b_bar)),
-        "r"(su32(a_bar))
-        : "memory");
+// The commits that release a stage, of the activation stage's barrier and of the A stage's, issued by one elected lane.
+__device__ __forceinline__ void tc_commit2_elect(uint64_t* b_bar, uint64_t* a_bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n}\n" ::"r"(su32(b_bar)),
+      "r"(su32(a_bar))
+      : "memory");
 }
 
 // 32 lanes x 16 consecutive 32-bit columns of the warp's TMEM lane quadrant.
