@@ -315,7 +315,8 @@ int ds4moe_linear_grad(const void* dy, const void* x, const void* w, const void*
  *     dx[t] = sum_v dz[t][v] W[v], dw[v] = sum_t dz[t][v] x[t], rounded to dtype. Either may be NULL.
  *     The logits are computed again one piece of the vocabulary at a time and dz is rounded to dtype
  *     (relative to the largest finite |dloss|, so that fp16 does not underflow) in the workspace. A dloss
- *     that is not finite makes its own row's dx not finite, and every dw.
+ *     that is not finite makes its own row's dx not finite, and every dw. Rows without a gradient enter dw as zeros
+ *     times x: their x has to be finite (padding cleared, not left as it was allocated).
  * workspace: 16-byte aligned device memory. The gradient takes pieces that fit it, of up to 16384
  * words; ds4moe_cross_entropy_workspace returns the bytes that let either call run at full speed. The
  * forward needs 8 bytes per row and 256 words (and 4 per row), the gradient 16 + 4 rows d (rounded up to

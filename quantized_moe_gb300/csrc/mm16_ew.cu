@@ -37,7 +37,8 @@ static_assert(alignof(Eight) >= alignof(uint4) && sizeof(Eight) == sizeof(uint4)
 // dz = dy * act'(z), and the column sums of dz (unrounded, fp32). A block takes 256 columns of one chunk of rows: each of
 // its eight warps walks every eighth row with one 16-byte load per operand (eight columns a thread), then the warps'
 // sums are added in order through shared memory, one partial per column and chunk. The second kernel adds the chunks
-// in order, 8 rows of threads per column. The order of every sum is fixed. HBM bound: dy, z and dz cross it once
+// in order, 8 rows of threads per column. The order of every sum is fixed. dz itself is rounded to 16 bits, because the
+// tensor cores multiply such operands: the gradients' error is 1.4 times that of a result rounded once. HBM bound: dy, z and dz cross it once
 // (elements that cannot be moved 8 at a time go one by one).
 template <bool VEC, int ACT>
 __global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t lddy,
