@@ -306,3 +306,41 @@ def test_pieces_that_split_their_sums_over_a_cluster(rows, d, pad, piece):
     size = 16 + (4 * rows * d + 15) // 16 * 16 + 2 * ((rows + 7) // 8 * 8) * piece
     _ce_check(x, w, labels, dloss, "bf16", _ce(x, w, labels, dloss, "bf16", ws_bytes=size, pad=pad))
     assert api.ds4moe_ops_status() == 0
+
+
+def test_graphs_whose_calls_follow_fills_and_copies():
+    """Captured behind a fill and a copy, which are no kernels: each call still sees what they wrote."""
+    rows, n, k = 40, 136, 72
+    x, w, dy = whole((rows, k), "bf16", 1), whole((n, k), "bf16", 2), whole((rows, n), "bf16", 3)
+    src, y, dw, db, dw0, db0 = torch.zeros_like(x), torch.empty_like(dy), torch.empty_like(w), torch.empty_like(w[:, 0].contiguous()), torch.ones_like(w), torch.ones_like(w[:, 0].contiguous())
+    size = api.ds4moe_linear_grad_workspace(rows, n)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    acc = torch.empty((1, n, k), device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+
+    def calls():
+        s = stream()
+        src.copy_(x)
+        api.ds4moe_linear(src, w, None, None, y, rows, n, k, stream=s)
+        src.zero_()
+        src[1:].copy_(x[1:])
+        api.ds4moe_linear_grad(dy, src, w, None, None, dw, db, rows, n, k, workspace=ws, workspace_bytes=size, stream=s)
+        acc.zero_()
+        api.ds4moe_grouped_mm_dw(dy, x, off, acc, rows, n, k, 1, dw_dtype="fp32", accumulate=True, stream=s)
+        api.ds4moe_linear_grad(None, None, None, None, None, dw0, db0, 0, n, k, workspace=ws, workspace_bytes=16, stream=s)
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    for _ in range(3):
+        for t in (src, y, dw, db, dw0, db0, acc):
+            t.fill_(1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, (x.double() @ w.double().T).to(y.dtype))
+        assert torch.equal(dw, (dy[1:].double().T @ x[1:].double()).to(dw.dtype)) and torch.equal(db, dy.double().sum(0).to(db.dtype))
+        assert torch.equal(acc[0].double(), dy.double().T @ x.double())
+        assert not bool(dw0.any()) and not bool(db0.any())
+    assert api.ds4moe_ops_status() == 0
