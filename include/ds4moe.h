@@ -330,8 +330,72 @@ int ds4moe_cross_entropy_grad(const void* x, const void* w, const int32_t* label
                               int32_t dtype, int32_t ignore_index, int64_t ldx, int64_t ldw, int64_t lddx,
                               int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* A gated feed-forward block's first half in one kernel, grouped by expert as above: group g's weights W_g are
+ * [2n x k], n rows of the gate G_g and then n rows of U_g (w_stride 0 means 2 n ldw), and
+ *   h[t] = act(G_g x[t]) * (U_g x[t])        x [rows x k], h [rows x n]; products and act in fp32, rounded once.
+ * offsets NULL (n_groups 1): one dense block of all rows. zout [rows x 2n] or NULL receives G_g x[t] and then U_g x[t],
+ * rounded to dtype, which the gradient needs. n is 1..2^23. The second half is ds4moe_grouped_mm (ds4moe_linear).
+ *   ds4moe_grouped_glu_grad: for dh [rows x n] and z what zout received, a = z's first n columns and b its others,
+ *     dz = [dh * b * act'(a), dh * act(a)]  [rows x 2n], required: rounded to dtype, what the products read
+ *     dx[t] = W_g^T dz[t]                   [rows x k]
+ *     dW_g  = sum_t dz[t] x[t]^T            [2n x k] at dw + g * dw_stride; zero for an empty group
+ *   dx and dw may each be NULL (w is read only for dx, x only for dw): ds4moe_grouped_mm_dw takes dz where a gradient in
+ *   fp32, or added to an older one, is wanted. dz may be z itself. Where act'(a) is 0 the first part of dz is 0 whatever dh and b hold;
+ *   act(a) is taken at its limit where a is infinite. rows == 0 writes zeros into dw. */
+int ds4moe_grouped_glu(const void* x, const void* w, const int32_t* offsets, void* h, void* zout, int32_t rows, int32_t n,
+                       int32_t k, int32_t n_groups, int32_t act, int32_t dtype, int64_t ldx, int64_t ldw,
+                       int64_t w_stride, int64_t ldh, int64_t ldz, void* stream);
+int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const int32_t* offsets, const void* z, void* dz,
+                            void* dx, void* dw, int32_t rows, int32_t n, int32_t k, int32_t n_groups, int32_t act,
+                            int32_t dtype, int64_t lddh, int64_t ldx, int64_t ldw, int64_t w_stride, int64_t ldz,
+                            int64_t lddz, int64_t lddx, int64_t lddw, int64_t dw_stride, void* stream);
+
+/* Scores of the logits z[t] = W x[t] at a temperature T (0.001..1000), x [rows x d], w [vocab x d]:
+ *   lse[t]        = log sum_v exp(z[t][v] / T)
+ *   logprob[t][j] = z[t][tokens[t][j]] / T - lse[t]          tokens device int32 [rows x n_tokens], n_tokens 0..256
+ *   entropy[t]    = -sum_v p log p, p = exp(z[t][v] / T - lse[t])   (absolute error about 1e-6)
+ *   top_index[t], top_logprob[t]: the top_k words with the largest logits, in order, ties to the lower index
+ *                                  (int32 and fp32 [rows x top_k], top_k 0..64 and at most vocab)
+ * all fp32 but the indices, lists without gaps between rows. A place without a token holds -1 and has logprob 0; so has one
+ * that lies outside the vocabulary otherwise, which also sets bit 0 of ds4moe_ops_status. lse and entropy may be NULL, the
+ * lists where they have no places. A logit of -inf has probability 0; the entropy of a row with no other is NaN. A logit
+ * that is NaN makes lse, logprob and entropy of its row NaN and is listed nowhere; places of top_index that this leaves
+ * hold -1 and NaN.
+ * workspace: 16-byte aligned device memory. ds4moe_logprobs_workspace returns the bytes for all rows at once (with top_k the
+ * logits in fp32 are in it); a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
+ * which reads W, and less than a block of 128 (or all) rows needs returns DS4MOE_ERR_CAPACITY. */
+int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k);
+int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* logprob, float* lse, float* entropy,
+                    int32_t* top_index, float* top_logprob, int32_t rows, int32_t vocab, int32_t d, int32_t n_tokens,
+                    int32_t top_k, int32_t dtype, float temperature, int64_t ldx, int64_t ldw, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/* Distillation from a teacher's top logits, the student's logits z[t] = W x[t] not stored. Row t has top_k entries (1..256):
+ * words ids[t][j] (device int32 [rows x top_k]; -1: no entry) with the teacher's logits teacher[t][j] (fp32, before the
+ * temperature; log probabilities do as well). With p = softmax over the row's entries of teacher / T and
+ * q = softmax over the vocabulary of z / T:
+ *   loss[t] = sum_j p_j (log p_j - logq[t][j]), logq[t][j] = z[t][ids[t][j]] / T - lse[t], lse as above (fp32, all written;
+ *   logq is 0 without an entry). A word named twice counts with both its entries. A row without entries, or with none above
+ *   -inf, has loss 0 and no gradient; an id other than -1 outside the vocabulary is no entry and sets bit 0 of
+ *   ds4moe_ops_status. A teacher logit of +inf or NaN makes its row's loss NaN.
+ *   ds4moe_distill_grad: for dloss (fp32 [rows]) and the lse and logq of the forward,
+ *     dz[t][v] = (q_v - sum over the entries that name v of p_j) * dloss[t] / T, dx[t] = sum_v dz[t][v] W[v],
+ *     dw[v] = sum_t dz[t][v] x[t], rounded to dtype. Either may be NULL. dz, the pieces of the vocabulary and what is not
+ *     finite are as for ds4moe_cross_entropy_grad.
+ * T is not applied to the loss once more (a caller who wants T^2 has it in dloss). workspace: as for the cross entropy;
+ * ds4moe_distill_workspace returns the bytes that let either call run at full speed. The forward takes the rows in blocks as
+ * ds4moe_logprobs does; the gradient needs 16 + 4 rows (d + 1 + top_k) + 512 (rows rounded up to 8) and 48 for rounding. */
+int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k);
+int ds4moe_distill(const void* x, const void* w, const int32_t* ids, const float* teacher, float* loss, float* lse,
+                   float* logq, int32_t rows, int32_t vocab, int32_t d, int32_t top_k, int32_t dtype, float temperature,
+                   int64_t ldx, int64_t ldw, void* workspace, int64_t workspace_bytes, void* stream);
+int ds4moe_distill_grad(const void* x, const void* w, const int32_t* ids, const float* teacher, const float* lse,
+                        const float* logq, const float* dloss, void* dx, void* dw, int32_t rows, int32_t vocab, int32_t d,
+                        int32_t top_k, int32_t dtype, float temperature, int64_t ldx, int64_t ldw, int64_t lddx,
+                        int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Device-side conditions of the 16-bit operators on the current device since the last call of this
- * function: synchronises the device, copies the flags to the host word and clears them. bit 0: a label
+ * function: synchronises the device, copies the flags to the host word and clears them. bit 0: a label, token or id
  * outside the vocabulary; bit 2: a pipeline wait gave up after its time limit (about one second) and the
  * results of that call are incomplete. One of bits 17..23 names the wait: 17 loads (stage free), 18 the
  * clearing of a ragged end (stage loaded), 21 epilogue (accumulator full), 22 MMA (accumulator free), 23 MMA

@@ -12,6 +12,10 @@
 //              token, so that its softmax needs no exchange between threads
 //   dx = dz W  lanes = features (A = W, l contiguous), cols = tokens (B = dz, c contiguous)
 //   dW = dz x  lanes = features (A = x, l contiguous), cols = words (B = dz, r contiguous)
+// and, of the gated block with weights W = [gate; up] ([2 n][k]):
+//   h          lanes = 16 gate features, the same 16 up features, the next 16 gate features, ... (A = W, r
+//              contiguous), cols = rows of x: the 32 lanes of one warp of the epilogue hold both factors of its
+//              16 results
 #pragma once
 
 #include "common.cuh"
@@ -26,7 +30,9 @@ enum MmRag : int {
 enum MmEpi : int {
   MM_EPI_STORE = 0,     // out = act(v + bias) + residual, or v * scale + what is there
   MM_EPI_STATS = 1,     // per lane: max and sum of exponentials over the tile's columns; the label's value
-  MM_EPI_SOFTGRAD = 2   // out = (exp(v - lse) - [column is the label]) * g
+  MM_EPI_SOFTGRAD = 2,  // out = (exp(v / T - lse) - [column is the label]) * g
+  MM_EPI_GLU = 3,       // out = act(gate) * up; lanes are the features of out, A has twice as many rows
+  MM_EPI_SCORE = 4      // per lane: as STATS of v / T, and the entropy's sum; the logits of listed words; the logits
 };
 enum MmAct : int { MM_ACT_NONE = 0, MM_ACT_RELU = 1, MM_ACT_SILU = 2, MM_ACT_GELU = 3 };
 
@@ -59,6 +65,13 @@ struct MmEpiArgs {
   const float* gscale;   // device scalar: max |g|
   float2* part;          // [column tiles][lanes] (max, sum)
   float* zlab;           // [lanes] the label's logit
+  float inv_t;           // 1 / T
+  // scores: lanes are tokens, columns the vocabulary
+  float* ent;            // [column tiles][lanes] sum of (v - max) exp((v - max) / T)
+  const int2* want;      // [lanes][n_want] (word, place), ascending; words that there are not come last
+  int n_want;
+  float* zwant;          // [lanes][n_want] the listed words' logits, by place
+  float* logits;         // [cols][lanes], or null
 };
 
 struct MmProblem {
@@ -124,6 +137,18 @@ __device__ __forceinline__ float mm_act_back(float dy, float z, int act) {
   return z > 0.f ? dy * (1.f - f) : z == z ? dy * f : z;
 }
 
+// The gated block: h = act(g) u, and from z as its type kept it act(g) (silu at -inf is its limit 0) and
+// dh u act'(g). Where the slope is 0 nothing passes, whatever dh and u hold.
+__device__ __forceinline__ float mm_act(float z, int act) {
+  return act == MM_ACT_SILU ? mm_silu(z) : act == MM_ACT_GELU ? mm_gelu(z) : act == MM_ACT_RELU ? mm_relu(z) : z;
+}
+__device__ __forceinline__ float mm_act_kept(float z, int act) { return mm_act(act == MM_ACT_SILU && z < -256.f ? -256.f : z, act); }
+__device__ __forceinline__ float mm_glu_dgate(float dh, float g, float u, int act) {
+  if (act == MM_ACT_NONE) return dh * u;
+  const float slope = mm_act_back(1.f, g, act);
+  return slope == 0.f ? 0.f : dh * u * slope;
+}
+
 // dz of the cross entropy is kept in 16 bits as (exp(z - lse) - [label]) * (g / max |g|) * 2^13. The
 // division makes the label's term of a mean's gradient, -1 + p, a value just below a power of two,
 // which 8 bits hold to about p (kept with g folded in, every label's term carried the same rounding
@@ -153,7 +178,45 @@ cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz
 // Joins the softmax partials of each token: lse, loss, and bit 0 of *err for labels outside the vocabulary.
 cudaError_t mm_softmax_join(const float2* part, int tiles, const float* zlab, const int* labels, int ignore, int vocab,
                             int rows, float* loss, float* lse, int* err, cudaStream_t s);
-// gs[0] = max |g| over the rows with a label and a finite g (1 where that is 0), gs[1] = gs[0] / kMmGradOne.
+// gs[0] = max |g| over the rows with a label (labels null: all) and a finite g (1 where that is 0), gs[1] = gs[0] / kMmGradOne.
 cudaError_t mm_grad_scale(const float* g, const int* labels, int ignore, int vocab, int rows, float* gs, cudaStream_t s);
+
+// The gated block's dz = [dh * up * act'(gate), dh * act(gate)] rounded to 16 bits, from z = [gate, up] ([rows][2 n]), of
+// the rows that have a group (offsets null: all).
+cudaError_t mm_glu_grad(const void* dh, int64_t lddh, const void* z, int64_t ldz, void* dz, int64_t lddz, const int* offsets,
+                        int groups, int rows, int n, int act, int f16, cudaStream_t s);
+
+// Sorts each row's n words for the scores' epilogue (MmEpiArgs::want): a word outside the vocabulary comes last.
+cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int2* want, cudaStream_t s);
+// What the scores' partials say of each row (temperature T = 1 / inv_t).
+struct MmScores {
+  const float2* part;
+  const float* ent;
+  int tiles, rows, vocab;
+  float inv_t;
+  const float* zwant;   // [rows][n] logits of the listed words
+  const int* words;     // [rows][n]
+  int n;
+  float* lse;           // [rows], or null
+  int* err;             // bit 0: a word other than -1 outside the vocabulary
+  // log probabilities
+  float* logprob;       // [rows][n]
+  float* entropy;       // [rows], or null
+  const float* logits;  // [vocab][rows]
+  int top_k;
+  int* top_index;       // [rows][top_k]
+  float* top_logprob;
+  // distillation: logprob is log q of the listed words
+  const float* teacher;  // [rows][n] logits
+  float* loss;           // [rows]
+};
+cudaError_t mm_score_join(const MmScores& a, cudaStream_t s);
+// The distillation's gradient at the listed words: g[t] = dloss[t] / T of the rows with a teacher, else 0, and
+// at[t][j] = exp(log q_j) - the teacher's probability of that word (all its entries together).
+cudaError_t mm_distill_prepare(const int* ids, const float* teacher, const float* logq, const float* dloss, int n, int vocab,
+                               int rows, float inv_t, float* g, float* at, cudaStream_t s);
+// ... and its way into a piece of dz ([words][lddz], from word0): the listed words' places are overwritten.
+cudaError_t mm_distill_scatter(const int* ids, const float* at, const float* g, const float* gs, int n, int rows, int word0,
+                               int words, void* dz, int64_t lddz, int f16, cudaStream_t s);
 
 }  // namespace ds4

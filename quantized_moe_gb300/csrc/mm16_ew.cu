@@ -1,38 +1,11 @@
 // The small kernels beside the 16-bit products: dz = dy * act'(z) with the column sums of db, the
-// join of the softmax partials, and the scale that dz of the cross entropy carries.
-#include "mm16.cuh"
+// gated block's dz, the join of the softmax partials, and the scale that dz of the cross entropy carries.
+#include "mm16_small.cuh"
 
 namespace ds4 {
 namespace {
 
 constexpr int kMaxChunks = 128;
-
-// Programmatic dependent launch, as in the products: a kernel sets itself up while its predecessor runs, and touches
-// global memory only after that is complete.
-__device__ __forceinline__ void begin() {
-  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;\n" ::: "memory");
-}
-template <class... P, class... A>
-cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
-// Eight 16-bit elements that are also moved as one 16-byte piece (a plain array is aligned to 2 bytes only, and the piece's
-// loads and stores could fault wherever the compiler keeps it in memory).
-struct Eight {
-  alignas(16) uint16_t h[8];
-  __device__ __forceinline__ uint4& piece() { return *reinterpret_cast<uint4*>(h); }
-};
-static_assert(alignof(Eight) >= alignof(uint4) && sizeof(Eight) == sizeof(uint4), "a piece of eight elements");
 
 // dz = dy * act'(z), and the column sums of dz (unrounded, fp32). A block takes 256 columns of one chunk of rows: each of
 // its eight warps walks every eighth row with one 16-byte load per operand (eight columns a thread), then the warps'
@@ -108,6 +81,50 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const void* dy, int64_t l
   }
 }
 
+// The gated block's dz: for h = act(g) u, dg = dh u act'(g) and du = dh act(g), each rounded to 16 bits because the
+// tensor cores multiply such operands. A thread takes eight neighbouring features of a row; dh, z and dz cross HBM once.
+template <bool VEC, int ACT>
+__global__ void __launch_bounds__(256) glu_grad_kernel(const void* dh, int64_t lddh, const void* z, int64_t ldz, void* dz,
+                                                       int64_t lddz, const int* offsets, int groups, int rows, int n, int f16) {
+  begin();
+  const int units = (n + 7) / 8;
+  int lo = 0, hi = rows;
+  if (offsets) lo = min(max(*offsets, 0), rows), hi = min(max(*(offsets + groups), 0), rows);
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < (int64_t)rows * units; i += gridDim.x * (int64_t)256) {
+    const int r = (int)(i / units), c = (int)(i - (int64_t)r * units) * 8;
+    if (r < lo || r >= hi) continue;
+    const uint16_t* ph = static_cast<const uint16_t*>(dh) + r * lddh + c;
+    const uint16_t* pz = static_cast<const uint16_t*>(z) + r * ldz + c;
+    uint16_t* pd = static_cast<uint16_t*>(dz) + r * lddz + c;
+    Eight h, g, u, dg, du;
+    if (VEC) {
+      h.piece() = *reinterpret_cast<const uint4*>(ph);
+      g.piece() = *reinterpret_cast<const uint4*>(pz);
+      u.piece() = *reinterpret_cast<const uint4*>(pz + n);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool there = c + k < n;
+        h.h[k] = there ? ph[k] : (uint16_t)0, g.h[k] = there ? pz[k] : (uint16_t)0, u.h[k] = there ? pz[n + k] : (uint16_t)0;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float dhv = ld16(h.h, k, f16), gv = ld16(g.h, k, f16), uv = ld16(u.h, k, f16);
+      st16(dg.h, k, mm_glu_dgate(dhv, gv, uv, ACT), f16);
+      st16(du.h, k, dhv * mm_act_kept(gv, ACT), f16);
+    }
+    if (VEC) {
+      *reinterpret_cast<uint4*>(pd) = dg.piece();
+      *reinterpret_cast<uint4*>(pd + n) = du.piece();
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < n) pd[k] = dg.h[k], pd[n + k] = du.h[k];
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) colsum_join_kernel(const float* part, int chunks, int n,
                                                           void* db, int f16) {
   __shared__ float s[8][32];
@@ -167,8 +184,8 @@ __global__ void __launch_bounds__(1024) grad_scale_kernel(const float* g, const 
   begin();
   float m = 0.f;
   for (int i = threadIdx.x; i < rows; i += 1024) {
-    const int lab = labels[i];
-    if (lab != ignore && lab >= 0 && lab < vocab) m = fmaxf(m, isfinite(g[i]) ? fabsf(g[i]) : 0.f);
+    const int lab = labels ? labels[i] : 0;
+    if (!labels || (lab != ignore && lab >= 0 && lab < vocab)) m = fmaxf(m, isfinite(g[i]) ? fabsf(g[i]) : 0.f);
   }
   m = warp_max(m);
   if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
@@ -206,6 +223,22 @@ cudaError_t mm_act_grad(const void* dy, int64_t lddy, const void* z, int64_t ldz
   }
   if (e == cudaSuccess && part) e = launch(colsum_join_kernel, dim3((n + 31) / 32), 256, s, part, chunks, n, db, f16);
   return e;
+}
+
+cudaError_t mm_glu_grad(const void* dh, int64_t lddh, const void* z, int64_t ldz, void* dz, int64_t lddz, const int* offsets,
+                        int groups, int rows, int n, int act, int f16, cudaStream_t s) {
+  const auto vec = [](const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; };
+  const bool wide = n % 8 == 0 && vec(dh, lddh) && vec(z, ldz) && vec(dz, lddz);
+  const int units = (n + 7) / 8;
+  const int64_t blocks = ((int64_t)rows * units + 255) / 256;
+  const dim3 grid((unsigned)(blocks < 1 << 20 ? blocks : 1 << 20));
+  const auto run = [&](auto kernel) { return launch(kernel, grid, 256, s, dh, lddh, z, ldz, dz, lddz, offsets, groups, rows, n, f16); };
+  switch (act) {
+    case MM_ACT_RELU: return run(wide ? glu_grad_kernel<true, MM_ACT_RELU> : glu_grad_kernel<false, MM_ACT_RELU>);
+    case MM_ACT_SILU: return run(wide ? glu_grad_kernel<true, MM_ACT_SILU> : glu_grad_kernel<false, MM_ACT_SILU>);
+    case MM_ACT_GELU: return run(wide ? glu_grad_kernel<true, MM_ACT_GELU> : glu_grad_kernel<false, MM_ACT_GELU>);
+    default: return run(wide ? glu_grad_kernel<true, MM_ACT_NONE> : glu_grad_kernel<false, MM_ACT_NONE>);
+  }
 }
 
 cudaError_t mm_softmax_join(const float2* part, int tiles, const float* zlab, const int* labels, int ignore, int vocab,

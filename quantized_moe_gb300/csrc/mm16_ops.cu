@@ -17,6 +17,8 @@ constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxWidth = 1 << 24;
 constexpr int kMaxGroups = 1024;
 constexpr int kPieceMax = 16384, kPieceMin = 256;  // words of one piece of the vocabulary
+constexpr int kMaxListed = 256, kMaxTop = 64;      // given words, and best words, of one row of scores
+constexpr int kScoreRows = 128;                    // scores take blocks of so many rows at least, whatever the workspace
 
 static __device__ int g_mm_err;  // flags of ds4moe_ops_status
 std::mutex g_mu;
@@ -43,6 +45,12 @@ struct Check {
   }
   void act(int v) {
     if (v < DS4MOE_ACT_NONE || v > DS4MOE_ACT_GELU) invalid("act=" + std::to_string(v) + " is not a ds4moe_act");
+  }
+  void listed(const char* name, int v, int least, int most) {
+    if (v < least || v > most) invalid(std::string(name) + "=" + std::to_string(v) + " must be in " + std::to_string(least) + ".." + std::to_string(most));
+  }
+  void temperature(float v) {
+    if (!(v >= 1e-3f && v <= 1e3f)) invalid("temperature=" + std::to_string(v) + " must be in 0.001..1000");
   }
   // A row distance: 0 stands for the width.
   int64_t ld(const char* name, int64_t v, int64_t width) {
@@ -119,6 +127,7 @@ ds4::MmProblem product(const void* a, int64_t lda, bool a_red, const void* b, in
   p.f16 = dtype == DS4MOE_FP16;
   p.e.out = out;
   p.e.ld = ld;
+  p.e.inv_t = 1.f;
   p.err = err;
   return p;
 }
@@ -156,6 +165,59 @@ int64_t best_piece(int64_t most, int rows, int vocab, int d, bool dx, bool dw) {
     if (cost < best_cost) best_cost = cost, best = piece;
   }
   return best;
+}
+
+// The gradient of a softmax loss in pieces of the vocabulary: the logits again, dz of one piece in the workspace, its
+// parts of dx and dw. labels: the cross entropy's; ids, places: the distillation's listed words.
+struct SoftGrad {
+  const void *x, *w;
+  int64_t ldx, ldw;
+  void *dx, *dw;
+  int64_t lddx, lddw;
+  int rows, vocab, d, dtype;
+  int* err;
+  float *gs, *sum;
+  char* dz;
+  int64_t dz_bytes;
+  const float *lse, *g;
+  float inv_t;
+  const int* labels;
+  int ignore;
+  const int* ids;
+  const float* places;
+  int listed;
+};
+cudaError_t soft_grad(const SoftGrad& q, cudaStream_t s) {
+  const char* wb = static_cast<const char*>(q.w);
+  const int rows = q.rows, vocab = q.vocab, d = q.d, dtype = q.dtype;
+  const int64_t lddz = up(rows, 8), ldx = q.ldx, ldw = q.ldw;
+  // the largest piece of the vocabulary that the workspace holds
+  const int64_t fits = q.dz_bytes / (2 * lddz) / kPieceMin * kPieceMin;
+  const int64_t piece = best_piece(std::min<int64_t>({fits, kPieceMax, up(vocab, kPieceMin)}), rows, vocab, d, q.dx, q.dw);
+  cudaError_t e = cudaSuccess;
+  for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += piece) {
+    const int pv = (int)std::min<int64_t>(piece, vocab - v0);
+    const bool last = v0 + pv == vocab;
+    ds4::MmProblem p = product(q.x, ldx, true, wb + 2 * v0 * ldw, ldw, true, rows, pv, d, dtype, q.dz, lddz, q.err);
+    p.epi = ds4::MM_EPI_SOFTGRAD;
+    p.e.word0 = (int)v0, p.e.vocab = vocab, p.e.ignore = q.ignore;
+    p.e.labels = q.labels, p.e.lse = q.lse, p.e.g = q.g, p.e.gscale = q.gs, p.e.inv_t = q.inv_t;
+    e = ds4::mm_launch(p, s);
+    if (e == cudaSuccess && q.ids) e = ds4::mm_distill_scatter(q.ids, q.places, q.g, q.gs, q.listed, rows, (int)v0, pv, q.dz, lddz, p.f16, s);
+    if (e == cudaSuccess && q.dx) {  // the pieces add up in fp32; the last one rounds
+      p = product(wb + 2 * v0 * ldw, ldw, false, q.dz, lddz, false, d, rows, pv, dtype, last ? q.dx : q.sum, last ? q.lddx : d, q.err);
+      p.e.out_f32 = !last;
+      p.e.acc_in = v0 ? q.sum : nullptr, p.e.acc_ld = d;
+      p.e.scale = last ? q.gs + 1 : nullptr;
+      e = ds4::mm_launch(p, s);
+    }
+    if (e == cudaSuccess && q.dw) {
+      p = product(q.x, ldx, false, q.dz, lddz, true, d, pv, rows, dtype, static_cast<char*>(q.dw) + 2 * v0 * q.lddw, q.lddw, q.err);
+      p.e.scale = q.gs + 1;
+      e = ds4::mm_launch(p, s);
+    }
+  }
+  return e;
 }
 
 }  // namespace
@@ -354,35 +416,272 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     char* ws = static_cast<char*>(workspace);
     float* gs = reinterpret_cast<float*>(ws);
     float* sum = reinterpret_cast<float*>(ws + 16);
-    char* dz = ws + 16 + up(4 * (int64_t)rows * d, 16);
-    const char* wb = static_cast<const char*>(w);
-    const int64_t lddz = up(rows, 8);
-    // the largest piece of the vocabulary that the workspace holds
-    const int64_t fits = (workspace_bytes - ce_grad_bytes(rows, d, 0)) / (2 * lddz) / kPieceMin * kPieceMin;
-    const int64_t piece = best_piece(std::min<int64_t>({fits, kPieceMax, up(vocab, kPieceMin)}), rows, vocab, d, dx, dw);
+    const int64_t held = ce_grad_bytes(rows, d, 0);
     cudaError_t e = ds4::mm_grad_scale(dloss, labels, ignore_index, vocab, rows, gs, s);
-    for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += piece) {
-      const int pv = (int)std::min<int64_t>(piece, vocab - v0);
-      const bool last = v0 + pv == vocab;
-      ds4::MmProblem p = product(x, ldx, true, wb + 2 * v0 * ldw, ldw, true, rows, pv, d, dtype, dz, lddz, err);
-      p.epi = ds4::MM_EPI_SOFTGRAD;
-      p.e.word0 = (int)v0, p.e.vocab = vocab, p.e.ignore = ignore_index;
-      p.e.labels = labels, p.e.lse = lse, p.e.g = dloss, p.e.gscale = gs;
-      e = ds4::mm_launch(p, s);
-      if (e == cudaSuccess && dx) {  // the pieces add up in fp32; the last one rounds
-        p = product(wb + 2 * v0 * ldw, ldw, false, dz, lddz, false, d, rows, pv, dtype, last ? dx : sum, last ? lddx : d, err);
-        p.e.out_f32 = !last;
-        p.e.acc_in = v0 ? sum : nullptr, p.e.acc_ld = d;
-        p.e.scale = last ? gs + 1 : nullptr;
-        e = ds4::mm_launch(p, s);
-      }
-      if (e == cudaSuccess && dw) {
-        p = product(x, ldx, false, dz, lddz, true, d, pv, rows, dtype, static_cast<char*>(dw) + 2 * v0 * lddw, lddw, err);
-        p.e.scale = gs + 1;
-        e = ds4::mm_launch(p, s);
-      }
-    }
+    if (e != cudaSuccess) return c.cuda(e);
+    SoftGrad q = {x, w, ldx, ldw, dx, dw, lddx, lddw, rows, vocab, d, dtype, err};
+    q.gs = gs, q.sum = sum, q.dz = ws + held, q.dz_bytes = workspace_bytes - held;
+    q.lse = lse, q.g = dloss, q.inv_t = 1.f, q.labels = labels, q.ignore = ignore_index;
+    return c.cuda(soft_grad(q, s));
+  });
+}
+
+namespace {
+
+// The gradient of rows whose dz is given: dx and dW of W [n x k], grouped or (offsets null) dense.
+cudaError_t block_grad(const void* dz, int64_t lddz, const void* x, int64_t ldx, const void* w, int64_t ldw, int64_t w_stride,
+                       const int32_t* offsets, int n_groups, void* dx, int64_t lddx, void* dw, int64_t lddw, int64_t dw_stride,
+                       int rows, int n, int k, int dtype, int* err, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (dx && rows) {
+    ds4::MmProblem p = product(w, ldw, false, dz, lddz, true, k, rows, n, dtype, dx, lddx, err);
+    p.a.group_stride = w_stride;
+    if (offsets) p.groups = n_groups, p.offsets = offsets, p.rag = ds4::MM_RAG_COLS;
+    e = ds4::mm_launch(p, s);
+  }
+  if (e == cudaSuccess && dw) {
+    ds4::MmProblem p = product(x, ldx, false, dz, lddz, false, k, n, rows, dtype, dw, lddw, err);
+    if (offsets) p.groups = n_groups, p.offsets = offsets, p.rag = ds4::MM_RAG_RED;
+    p.e.group_stride = dw_stride;
+    e = ds4::mm_launch(p, s);
+  }
+  return e;
+}
+
+// A block without offsets is one dense one.
+void block_groups(Check& c, const void* offsets, int n_groups) {
+  groups(c, n_groups);
+  if (!offsets && n_groups > 1) c.invalid("offsets is NULL with n_groups=" + std::to_string(n_groups) + " (a dense block has one)");
+}
+
+// Workspace of the scores of `rows` rows: softmax partials, sorted lists with their logits, all logits where the best
+// words are asked for.
+struct ScoreSpace {
+  int64_t part, ent, want, zwant, logits, total;
+  ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
+    const int64_t tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile;
+    part = 0;
+    ent = up(8 * rows * tiles, 16);
+    want = ent + up(4 * rows * tiles, 16);
+    zwant = want + up(8 * rows * n, 16);
+    logits = zwant + up(4 * rows * n, 16);
+    total = logits + (top_k ? up(4 * rows * vocab, 16) : 0);
+  }
+};
+
+// The scores of all rows, in blocks that the workspace holds: what `a` asks for, from its row 0 on.
+struct ScoreCall {
+  const void *x, *w;
+  int64_t ldx, ldw;
+  int vocab, d, dtype;
+  int* err;
+};
+int score_rows(Check& c, int rows, int vocab, int n, int top_k, int64_t bytes) {
+  const int64_t least = ScoreSpace(std::min(rows, kScoreRows), vocab, n, top_k).total;
+  if (bytes < least) {
+    c.fail(DS4MOE_ERR_CAPACITY, "workspace_bytes is less than the " + std::to_string(least) + " of a block of rows");
+    return 0;
+  }
+  if (bytes >= ScoreSpace(rows, vocab, n, top_k).total) return rows;
+  int64_t lo = 1, hi = (rows + kScoreRows - 1) / kScoreRows;  // blocks of kScoreRows that fit, and that do not
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) / 2;
+    (bytes >= ScoreSpace(mid * kScoreRows, vocab, n, top_k).total ? lo : hi) = mid;
+  }
+  return (int)lo * kScoreRows;
+}
+cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, char* ws, cudaStream_t s) {
+  const int vocab = call.vocab;
+  a.vocab = vocab, a.tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile, a.err = call.err;
+  const ScoreSpace at(block, vocab, a.n, a.top_k);
+  cudaError_t e = cudaSuccess;
+  for (int64_t t0 = 0; t0 < rows && e == cudaSuccess; t0 += block) {
+    const int nr = (int)std::min<int64_t>(block, rows - t0);
+    ds4::MmScores b = a;
+    b.rows = nr;
+    const auto move = [&](auto*& p, int64_t per_row) { if (p) p += t0 * per_row; };
+    move(b.words, a.n), move(b.lse, 1), move(b.logprob, a.n), move(b.entropy, 1), move(b.top_index, a.top_k);
+    move(b.top_logprob, a.top_k), move(b.teacher, a.n), move(b.loss, 1);
+    ds4::MmProblem p = product(static_cast<const char*>(call.x) + 2 * t0 * call.ldx, call.ldx, true, call.w, call.ldw, true, nr, vocab,
+                               call.d, call.dtype, nullptr, 0, call.err);
+    p.epi = ds4::MM_EPI_SCORE;
+    p.e.inv_t = a.inv_t;
+    p.e.part = reinterpret_cast<float2*>(ws + at.part), p.e.ent = reinterpret_cast<float*>(ws + at.ent);
+    p.e.want = reinterpret_cast<int2*>(ws + at.want), p.e.n_want = a.n, p.e.zwant = reinterpret_cast<float*>(ws + at.zwant);
+    p.e.logits = a.top_k ? reinterpret_cast<float*>(ws + at.logits) : nullptr;
+    b.part = p.e.part, b.ent = p.e.ent, b.zwant = p.e.zwant, b.logits = p.e.logits;
+    if (a.n) e = ds4::mm_sort_words(b.words, a.n, vocab, nr, reinterpret_cast<int2*>(ws + at.want), s);
+    if (e == cudaSuccess) e = ds4::mm_launch(p, s);
+    if (e == cudaSuccess) e = ds4::mm_score_join(b, s);
+  }
+  return e;
+}
+
+// Workspace of the distillation's gradient: the scale words, fp32 sum of dx, each row's weight, the listed words' places,
+// one piece of dz.
+struct DistillSpace {
+  int64_t sum, g, at, dz;
+  DistillSpace(int64_t rows, int64_t d, int64_t n) {
+    sum = 16;
+    g = sum + up(4 * rows * d, 16);
+    at = g + up(4 * rows, 16);
+    dz = at + up(4 * rows * n, 16);
+  }
+  int64_t total(int64_t rows, int64_t piece) const { return dz + 2 * up(rows, 8) * piece; }
+};
+
+}  // namespace
+
+extern "C" int ds4moe_grouped_glu(const void* x, const void* w, const int32_t* offsets, void* h, void* zout, int32_t rows,
+                                  int32_t n, int32_t k, int32_t n_groups, int32_t act, int32_t dtype, int64_t ldx,
+                                  int64_t ldw, int64_t w_stride, int64_t ldh, int64_t ldz, void* stream) {
+  return guarded("ds4moe_grouped_glu", [&]() -> int {
+    Check c("ds4moe_grouped_glu");
+    c.rows(rows), c.listed("n", n, 1, kMaxWidth / 2), c.width("k", k), c.act(act), c.dtype(dtype), groups(c, n_groups);
+    ldx = c.ld("ldx", ldx, k), ldw = c.ld("ldw", ldw, k), ldh = c.ld("ldh", ldh, n), ldz = c.ld("ldz", ldz, 2 * (int64_t)n);
+    w_stride = stride(c, "w_stride", w_stride, 2 * (int64_t)n, ldw);
+    if (!c.ok() || rows == 0) return c.code;
+    block_groups(c, offsets, n_groups);
+    c.device();
+    c.ptr("x", x, 2), c.ptr("w", w, 2), c.ptr("offsets", offsets, 4, true), c.ptr("h", h, 2), c.ptr("zout", zout, 2, true);
+    int* err = c.err_word();
+    if (!c.ok()) return c.code;
+    ds4::MmProblem p = product(w, ldw, true, x, ldx, true, n, rows, k, dtype, h, ldh, err);
+    p.epi = ds4::MM_EPI_GLU;
+    p.a.group_stride = w_stride;
+    if (offsets) p.groups = n_groups, p.offsets = offsets, p.rag = ds4::MM_RAG_COLS;
+    p.e.z = zout, p.e.ldz = ldz, p.e.act = act;
+    return c.cuda(ds4::mm_launch(p, static_cast<cudaStream_t>(stream)));
+  });
+}
+
+extern "C" int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const int32_t* offsets, const void* z,
+                                       void* dz, void* dx, void* dw, int32_t rows, int32_t n, int32_t k, int32_t n_groups,
+                                       int32_t act, int32_t dtype, int64_t lddh, int64_t ldx, int64_t ldw, int64_t w_stride,
+                                       int64_t ldz, int64_t lddz, int64_t lddx, int64_t lddw, int64_t dw_stride, void* stream) {
+  return guarded("ds4moe_grouped_glu_grad", [&]() -> int {
+    Check c("ds4moe_grouped_glu_grad");
+    const int64_t n2 = 2 * (int64_t)n;
+    c.rows(rows), c.listed("n", n, 1, kMaxWidth / 2), c.width("k", k), c.act(act), c.dtype(dtype), groups(c, n_groups);
+    lddh = c.ld("lddh", lddh, n), ldx = c.ld("ldx", ldx, k), ldw = c.ld("ldw", ldw, k), ldz = c.ld("ldz", ldz, n2);
+    lddz = c.ld("lddz", lddz, n2), lddx = c.ld("lddx", lddx, k), lddw = c.ld("lddw", lddw, k);
+    w_stride = stride(c, "w_stride", w_stride, n2, ldw), dw_stride = stride(c, "dw_stride", dw_stride, n2, lddw);
+    if (!c.ok()) return c.code;
+    block_groups(c, offsets, n_groups);
+    c.device();
+    const bool none = rows == 0;  // (nothing of the operands is read, dw is zeros)
+    c.ptr("dh", dh, 2, none), c.ptr("x", x, 2, none || !dw), c.ptr("w", w, 2, none || !dx), c.ptr("offsets", offsets, 4, true);
+    c.ptr("z", z, 2, none), c.ptr("dz", dz, 2, none), c.ptr("dx", dx, 2, true), c.ptr("dw", dw, 2, true);
+    int* err = c.err_word();
+    if (!c.ok()) return c.code;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (!none) e = ds4::mm_glu_grad(dh, lddh, z, ldz, dz, lddz, offsets, n_groups, rows, n, act, dtype == DS4MOE_FP16, s);
+    if (e == cudaSuccess)
+      e = block_grad(dz, lddz, x, ldx, w, ldw, w_stride, offsets, n_groups, dx, lddx, dw, lddw, dw_stride, rows, (int)n2, k, dtype, err, s);
     return c.cuda(e);
+  });
+}
+
+extern "C" int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k) {
+  if (rows <= 0 || vocab <= 0 || n_tokens < 0) return 16;
+  return std::max<int64_t>(16, ScoreSpace(rows, vocab, n_tokens, top_k).total);
+}
+
+extern "C" int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* logprob, float* lse,
+                               float* entropy, int32_t* top_index, float* top_logprob, int32_t rows, int32_t vocab,
+                               int32_t d, int32_t n_tokens, int32_t top_k, int32_t dtype, float temperature, int64_t ldx,
+                               int64_t ldw, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded("ds4moe_logprobs", [&]() -> int {
+    Check c("ds4moe_logprobs");
+    c.rows(rows), c.width("vocab", vocab), c.width("d", d), c.dtype(dtype), c.temperature(temperature);
+    c.listed("n_tokens", n_tokens, 0, kMaxListed), c.listed("top_k", top_k, 0, std::min(kMaxTop, vocab));
+    ldx = c.ld("ldx", ldx, d), ldw = c.ld("ldw", ldw, d);
+    if (!c.ok() || rows == 0) return c.code;
+    const int block = score_rows(c, rows, vocab, n_tokens, top_k, workspace_bytes);
+    if (!c.ok()) return c.code;
+    c.device();
+    c.ptr("x", x, 2), c.ptr("w", w, 2), c.ptr("tokens", tokens, 4, n_tokens == 0), c.ptr("logprob", logprob, 4, n_tokens == 0);
+    c.ptr("lse", lse, 4, true), c.ptr("entropy", entropy, 4, true);
+    c.ptr("top_index", top_index, 4, top_k == 0), c.ptr("top_logprob", top_logprob, 4, top_k == 0);
+    c.ptr("workspace", workspace, 16);
+    int* err = c.err_word();
+    if (!c.ok()) return c.code;
+    ds4::MmScores a = {};
+    a.inv_t = 1.f / temperature;
+    a.words = tokens, a.n = n_tokens, a.logprob = logprob, a.lse = lse, a.entropy = entropy;
+    a.top_k = top_k, a.top_index = top_index, a.top_logprob = top_logprob;
+    return c.cuda(scores({x, w, ldx, ldw, vocab, d, dtype, err}, a, rows, block, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
+  });
+}
+
+extern "C" int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k) {
+  if (rows <= 0 || vocab <= 0 || d <= 0 || top_k <= 0) return 16;
+  return std::max<int64_t>(ScoreSpace(rows, vocab, top_k, 0).total,
+                           DistillSpace(rows, d, top_k).total(rows, std::min<int64_t>(kPieceMax, up(vocab, kPieceMin))));
+}
+
+extern "C" int ds4moe_distill(const void* x, const void* w, const int32_t* ids, const float* teacher, float* loss,
+                              float* lse, float* logq, int32_t rows, int32_t vocab, int32_t d, int32_t top_k, int32_t dtype,
+                              float temperature, int64_t ldx, int64_t ldw, void* workspace, int64_t workspace_bytes,
+                              void* stream) {
+  return guarded("ds4moe_distill", [&]() -> int {
+    Check c("ds4moe_distill");
+    c.rows(rows), c.width("vocab", vocab), c.width("d", d), c.dtype(dtype), c.temperature(temperature);
+    c.listed("top_k", top_k, 1, kMaxListed);
+    ldx = c.ld("ldx", ldx, d), ldw = c.ld("ldw", ldw, d);
+    if (!c.ok() || rows == 0) return c.code;
+    const int block = score_rows(c, rows, vocab, top_k, 0, workspace_bytes);
+    if (!c.ok()) return c.code;
+    c.device();
+    c.ptr("x", x, 2), c.ptr("w", w, 2), c.ptr("ids", ids, 4), c.ptr("teacher", teacher, 4), c.ptr("loss", loss, 4);
+    c.ptr("lse", lse, 4), c.ptr("logq", logq, 4), c.ptr("workspace", workspace, 16);
+    int* err = c.err_word();
+    if (!c.ok()) return c.code;
+    ds4::MmScores a = {};
+    a.inv_t = 1.f / temperature;
+    a.words = ids, a.n = top_k, a.teacher = teacher, a.loss = loss, a.lse = lse, a.logprob = logq;
+    return c.cuda(scores({x, w, ldx, ldw, vocab, d, dtype, err}, a, rows, block, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream)));
+  });
+}
+
+extern "C" int ds4moe_distill_grad(const void* x, const void* w, const int32_t* ids, const float* teacher, const float* lse,
+                                   const float* logq, const float* dloss, void* dx, void* dw, int32_t rows, int32_t vocab,
+                                   int32_t d, int32_t top_k, int32_t dtype, float temperature, int64_t ldx, int64_t ldw,
+                                   int64_t lddx, int64_t lddw, void* workspace, int64_t workspace_bytes, void* stream) {
+  return guarded("ds4moe_distill_grad", [&]() -> int {
+    Check c("ds4moe_distill_grad");
+    c.rows(rows), c.width("vocab", vocab), c.width("d", d), c.dtype(dtype), c.temperature(temperature);
+    c.listed("top_k", top_k, 1, kMaxListed);
+    ldx = c.ld("ldx", ldx, d), ldw = c.ld("ldw", ldw, d), lddx = c.ld("lddx", lddx, d), lddw = c.ld("lddw", lddw, d);
+    if (!c.ok() || (!dx && !dw)) return c.code;
+    const DistillSpace at(rows, d, top_k);
+    if (rows && workspace_bytes < at.total(rows, kPieceMin)) {
+      c.fail(DS4MOE_ERR_CAPACITY, "workspace_bytes is less than the " + std::to_string(at.total(rows, kPieceMin)) + " of the smallest piece of the vocabulary");
+      return c.code;
+    }
+    c.device();
+    const bool none = rows == 0;
+    c.ptr("x", x, 2, none), c.ptr("w", w, 2, none), c.ptr("ids", ids, 4, none), c.ptr("teacher", teacher, 4, none);
+    c.ptr("lse", lse, 4, none), c.ptr("logq", logq, 4, none), c.ptr("dloss", dloss, 4, none);
+    c.ptr("dx", dx, 2, true), c.ptr("dw", dw, 2, true), c.ptr("workspace", workspace, 16, none);
+    int* err = c.err_word();
+    if (!c.ok()) return c.code;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (none) {  // an empty sum
+      if (dw) return c.cuda(ds4::mm_launch(product(x, ldx, false, x, ldx, false, d, vocab, 0, dtype, dw, lddw, err), s));
+      return c.code;
+    }
+    char* ws = static_cast<char*>(workspace);
+    float *gs = reinterpret_cast<float*>(ws), *g = reinterpret_cast<float*>(ws + at.g), *places = reinterpret_cast<float*>(ws + at.at);
+    const float inv_t = 1.f / temperature;
+    cudaError_t e = ds4::mm_distill_prepare(ids, teacher, logq, dloss, top_k, vocab, rows, inv_t, g, places, s);
+    if (e == cudaSuccess) e = ds4::mm_grad_scale(g, nullptr, 0, vocab, rows, gs, s);
+    if (e != cudaSuccess) return c.cuda(e);
+    SoftGrad q = {x, w, ldx, ldw, dx, dw, lddx, lddw, rows, vocab, d, dtype, err};
+    q.gs = gs, q.sum = reinterpret_cast<float*>(ws + at.sum), q.dz = ws + at.dz, q.dz_bytes = workspace_bytes - at.dz;
+    q.lse = lse, q.g = g, q.inv_t = inv_t, q.ids = ids, q.places = places, q.listed = top_k;
+    return c.cuda(soft_grad(q, s));
   });
 }
 

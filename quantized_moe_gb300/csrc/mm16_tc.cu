@@ -46,7 +46,7 @@ constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulator where the result is fp32
 constexpr int kSegFold = 16384;           // and where it has 16 bits
-constexpr int kEpiPlain = 3;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
+constexpr int kEpiPlain = 5;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -298,17 +298,26 @@ struct Loader {
   int64_t step;         // elements to the chunk 32 rows on
   int odd, red_major, row, ch;
   int mn_left, r_left;  // lanes or columns, and reduction, from the thread's first element to their ends
+  int pitch;            // lanes or columns from one of the thread's rows to the next (K-major)
   __device__ __forceinline__ void start(const uint16_t* base, int64_t ld, int red, int mn0, int mn_end, int r0, int r_end, int tid) {
     red_major = red;
-    row = tid >> 3, ch = tid & 7;
+    row = tid >> 3, ch = tid & 7, pitch = 32;
     const int mn = red ? mn0 + row : mn0 + ch * 8, r = red ? r0 + ch * 8 : r0 + row;
     src = base + (red ? (int64_t)mn * ld + r : (int64_t)r * ld + mn);
     step = 32 * ld;
     odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
     mn_left = mn_end - mn, r_left = r_end - r;
   }
+  // The gated block's weights, `up` elements from a gate row to its up row: 16 gate rows, then the same 16 up rows.
+  __device__ __forceinline__ void start_glu(const uint16_t* base, int64_t ld, int64_t up, int f0, int f_end, int r0, int r_end, int tid) {
+    start(base, ld, 1, f0 + ((tid >> 3) & 15), f_end, r0, r_end, tid & 7);
+    row = tid >> 3, pitch = 16;
+    if (row & 16) src += up;
+    step = 16 * ld;
+    odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
+  }
   __device__ __forceinline__ int valid(int u) const {
-    if (red_major) return mn_left > 32 * u ? min(8, r_left) : 0;
+    if (red_major) return mn_left > pitch * u ? min(8, r_left) : 0;
     return r_left > 32 * (u & 1) ? min(8, mn_left - 64 * (u >> 1)) : 0;
   }
   // The words of the chunks in rows 32 u0 .. 32 u0 + 96 of the current stage, and their way into the stage: other work
@@ -482,6 +491,22 @@ __device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int 
   }
 }
 
+// The gated block: lanes l of a group of 32 hold 16 features' gates, then their ups; 32 columns, nv exist.
+__device__ __forceinline__ void glu_out(const MmProblem& p, int l, int c, int nv, float (&v)[32]) {
+  const MmEpiArgs& e = p.e;
+  const int f = (l >> 5) * 16 + (l & 15), is_up = (l >> 4) & 1;
+  if (f >= p.lanes) nv = 0;
+  uint16_t h[32];
+  if (e.z) {
+    to16(v, h, p.f16);
+    store_col(static_cast<uint16_t*>(e.z) + (int64_t)c * e.ldz + (is_up ? p.lanes : 0) + f, e.ldz, nv, h);
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = mm_act(v[j], e.act) * __shfl_xor_sync(0xffffffffu, v[j], 16);
+  to16(v, h, p.f16);
+  store_col(static_cast<uint16_t*>(e.out) + (int64_t)c * e.ld + f, e.ld, is_up ? 0 : nv, h);
+}
+
 // ---- 16-bit results by rows: the warps hold 32 lanes x 32 columns as fragments (a thread: lanes i/4 + 8 r, columns
 // 8 j + 2 (i % 4) and the next), which stmatrix writes transposed into shared memory, from where whole rows of 128
 // lanes leave as 16-byte stores.
@@ -588,6 +613,44 @@ __device__ __forceinline__ void epi_stats(float (&v)[32], int nv, float& m, floa
   m = top;
 }
 
+// The same for scores: c = log2(e) / T, u the running sum of (z - m) exp((z - m) / T), from which the entropy comes
+// without the cancellation that a sum of p z would have.
+__device__ __forceinline__ float exp2_fast(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void epi_score(const float (&v)[32], int nv, float c, float& m, float& s, float& u) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j < nv) top = fmaxf(top, v[j]);
+  if (top == -INFINITY) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) bad |= j < nv && v[j] != v[j];
+    if (bad) s = NAN;
+    return;
+  }
+  if (m != top) {
+    const float d = fmaxf(m - top, -1e30f), r = exp2_fast(d * c);  // (m = -inf: s and u are 0, or NaN)
+    u = (u + d * s) * r;
+    s *= r;
+    m = top;
+  }
+  float t = 0.f, w = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (j < nv) {
+      const float d = v[j] - top, e = exp2_fast(d * c);
+      t += e;
+      w += fmaxf(d, -1e30f) * e;  // (words of probability zero add nothing)
+    }
+  }
+  s += t;
+  u += w;
+}
+
 template <int CG, int EPI, bool GEN>
 __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     mm_tc_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
@@ -675,7 +738,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int a_boxes = a_red ? 1 : 2 / a.a_blocks;
+    const int a_boxes = EPI == MM_EPI_GLU ? BM / 16 : a_red ? 1 : 2 / a.a_blocks;
     Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -694,7 +757,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (of_a) {
           if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);  // (copies may report before it)
           if (lane < a_boxes) {
-            if (a_red)
+            if (EPI == MM_EPI_GLU)  // 16 rows of the gate, the same 16 of up, and so on
+              tma_load<CG>(st + lane * 2048, &ta, r, la / 2 + 16 * (lane >> 1) + (lane & 1 ? p.lanes : 0), 0, ga, bar);
+            else if (a_red)
               tma_load<CG>(st, &ta, r, la, 0, ga, bar);
             else if (a.a_blocks > 1)
               tma_load<CG>(st, &ta, 0, r, la / 64, ga, bar);
@@ -726,7 +791,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const int nb = mma_n<CG>(p, o.n);
       Loader la, lb;
-      la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
+      if (EPI == MM_EPI_GLU)
+        la.start_glu(pa, p.a.ld, p.lanes * p.a.ld, o.l0 / 2, p.lanes, o.r0, o.r0 + o.red, tid);
+      else
+        la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
       lb.start(static_cast<const uint16_t*>(p.b.p), p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0, o.r0 + o.red, tid);
       const int b_units = (nb + 31) / 32;
       uint32_t wa[4][5], wb[4][5];
@@ -936,6 +1004,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.live = false;
     }
     const int c_first = 32 * half, c_step = 64;
+    constexpr bool kStats = EPI == MM_EPI_STATS || EPI == MM_EPI_SCORE;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
     Walk<CG> walk;
@@ -945,7 +1014,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
       // what the tile needs besides its sums is fetched before they are waited for
-      const bool by_rows = EPI != MM_EPI_STATS && a.rows_out;
+      const bool by_rows = !kStats && a.rows_out;
       const int64_t group_out = p.rag == MM_RAG_RED ? o.g * e.group_stride : 0;
       const void* add = e.accumulate ? e.out : e.residual;
       const int64_t add_ld = e.accumulate ? e.ld : e.ldr;
@@ -965,18 +1034,34 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (l >= p.lanes || (!by_rows && r)) continue;
         if (EPI == MM_EPI_STORE) {
           if (e.bias) bias[r] = ld16(e.bias, l, p.f16);
-        } else {
-          lab[r] = max(*(e.labels + l), -1);
+        } else if (EPI == MM_EPI_STATS || EPI == MM_EPI_SOFTGRAD) {
+          if (EPI == MM_EPI_STATS || e.labels) lab[r] = max(*(e.labels + l), -1);
           if (EPI == MM_EPI_SOFTGRAD) {
-            const bool skip = lab[r] == e.ignore || lab[r] < 0 || lab[r] >= e.vocab;
+            const bool skip = e.labels && (lab[r] == e.ignore || lab[r] < 0 || lab[r] >= e.vocab);
             lse[r] = *(e.lse + l);
             gw[r] = skip ? 0.f : *(e.g + l) / *e.gscale * kMmGradOne;
             lab[r] = skip ? -1 : lab[r] - e.word0;
           }
         }
       }
-      float m = -INFINITY, total = 0.f;
-      constexpr bool kHold = EPI == MM_EPI_STATS && CG == 2;  // sums over accumulators are held in registers
+      float m = -INFINITY, total = 0.f, spread = 0.f;
+      // the listed words of the thread's token: the first one from the tile's start on
+      const int2* want = nullptr;
+      int want_left = 0, want_next = INT32_MAX;
+      if (EPI == MM_EPI_SCORE && e.n_want > 0 && l0 + 32 * quad + lane < p.lanes) {
+        want = e.want + (int64_t)(l0 + 32 * quad + lane) * e.n_want;
+        want_left = e.n_want;
+        while (want_left > 0) {  // (halves: the first that is not below)
+          const int mid = want_left >> 1;
+          if (want[mid].x < o.c0)
+            want += mid + 1, want_left -= mid + 1;
+          else
+            want_left = mid;
+        }
+        want_left = (int)(e.want + (int64_t)(l0 + 32 * quad + lane + 1) * e.n_want - want);
+        if (want_left > 0) want_next = want->x;
+      }
+      constexpr bool kHold = kStats && CG == 2;  // sums over accumulators are held in registers
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       const bool folds = a.fold && o.red > a.seg;
       bool ok = true;
@@ -1005,7 +1090,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         }
         // (the warps that share barriers in what follows leave together)
-        ok = EPI == MM_EPI_STATS ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
+        ok = kStats ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
         if (CG == 1 && a.split > 1) {
           // the CTAs of a cluster have each summed a share of the reduction: the others hand theirs to the first one's
           // shared memory, which adds them in order
@@ -1028,7 +1113,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (part > 0) ok = false;
         }
         if (!ok) break;
-        const bool two = EPI == MM_EPI_STATS && !kHold && a.accs > 1;
+        const bool two = kStats && !kHold && a.accs > 1;
         if (two) {  // fold the first accumulator into the second and hand it back: the next tile's first half needs it soon
           for (int c = c_first; o.red > a.seg && c < o.n && l0 + 32 * quad < p.lanes; c += c_step) {
             float v[32], more[32];
@@ -1044,7 +1129,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(acc_empty);
         }
-        if (EPI == MM_EPI_STATS) {
+        if (kStats) {
           const uint32_t sums = two && o.red > a.seg ? taddr + acc_stride : taddr;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -1059,6 +1144,24 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
               if (k + a.seg < o.red) continue;
             }
             const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
+            if (EPI == MM_EPI_SCORE) {
+              epi_score(y, nv, e.inv_t * 1.4426950408889634f, m, total, spread);
+              if (e.logits && l0 + 32 * quad + lane < p.lanes)
+                store_col(e.logits + (int64_t)(o.c0 + c) * p.lanes + l0 + 32 * quad + lane, p.lanes, nv, y);
+              while (want_next < o.c0 + c + nv) {
+                const int j_at = want_next - (o.c0 + c);
+                if (j_at >= 0) {  // (the other half's words are passed over)
+                  float own = 0.f;
+#pragma unroll
+                  for (int j = 0; j < 32; ++j)
+                    if (j == j_at) own = y[j];
+                  e.zwant[(int64_t)(l0 + 32 * quad + lane) * e.n_want + want->y] = own;
+                }
+                ++want;
+                want_next = --want_left > 0 ? want->x : INT32_MAX;
+              }
+              continue;
+            }
             epi_stats(y, nv, m, total);
             if (at >= 0 && at < nv) {  // (the label of a lane that exists)
               float own = 0.f;
@@ -1101,7 +1204,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 #pragma unroll
                   for (int q = 0; q < 2; ++q) {
                     // (a row without gradient stays zero even where its logits are not finite)
-                    const float d = (__expf(f.v[j][r][q] - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
+                    const float d = (__expf(f.v[j][r][q] * e.inv_t - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
                     f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
                   }
             } else {
@@ -1172,13 +1275,15 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
               }
             }
             const int nv = min(32, o.n - c);
-            if (EPI == MM_EPI_STORE) {
+            if (EPI == MM_EPI_GLU) {
+              glu_out(p, l, o.c0 + c, nv, v);
+            } else if (EPI == MM_EPI_STORE) {
               epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
               put(p, o.g, l, o.c0 + c, nv, v);
             } else {
               const int at = lab[0] - (o.c0 + c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
+              for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] * e.inv_t - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
               put(p, 0, l, o.c0 + c, nv, v);
             }
           }
@@ -1196,6 +1301,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
       }
       if (!ok) break;
+      if (EPI == MM_EPI_SCORE) {
+        float4* x = reinterpret_cast<float4*>(out_stage) + 32 * quad + lane;
+        const int l = l0 + 32 * quad + lane;
+        if (half) *x = make_float4(m, total, spread, 0.f);
+        named_bar(2, 32 * kEpiWarps);
+        if (!half && l < p.lanes) {
+          const float4 q = *x;
+          const float top = fmaxf(m, q.x), c = e.inv_t * 1.4426950408889634f;
+          const float d0 = m == top ? 0.f : fmaxf(m - top, -1e30f), d1 = q.x == top ? 0.f : fmaxf(q.x - top, -1e30f);
+          const float r0 = exp2_fast(d0 * c), r1 = exp2_fast(d1 * c);
+          const int64_t at = (int64_t)(o.c0 / a.bn) * p.lanes + l;
+          e.part[at] = make_float2(top, total * r0 + q.y * r1);
+          e.ent[at] = (spread + d0 * total) * r0 + (q.z + d1 * q.y) * r1;
+        }
+      }
       if (EPI == MM_EPI_STATS) {  // the two halves' partials are joined
         float2* x = reinterpret_cast<float2*>(out_stage) + 32 * quad + lane;
         const int l = l0 + 32 * quad + lane;
@@ -1273,6 +1393,8 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   switch (a.p.epi) {
     case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SOFTGRAD: return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_GLU: return launch<CG, MM_EPI_GLU, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_SCORE: return launch<CG, MM_EPI_SCORE, GEN>(ta, tb, a, grid, s);
     default: break;
   }
   const MmEpiArgs& e = a.p.e;
@@ -1290,6 +1412,8 @@ cudaError_t prepare_epi() {
   cudaError_t e = prepare_one<CG, MM_EPI_STORE, GEN>();
   if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_STATS, GEN>();
   if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_SOFTGRAD, GEN>();
+  if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_GLU, GEN>();
+  if (e == cudaSuccess) e = prepare_one<CG, MM_EPI_SCORE, GEN>();
   return e;
 }
 
@@ -1374,18 +1498,20 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   // 16 x 2048 x 1024, 16 stages: 7.4 alone, 6.6 in two; but 64 x 1024 x 512, 8 stages: 5.6 alone, 6.4 in two, and
   // 300 x 1000 x 576, 9 stages: 6.0 alone, 7.0 in two).
   a.split = 1;
-  const int64_t lanes128 = (p.lanes + BM - 1) / BM;
+  const bool stats = p.epi == MM_EPI_STATS || p.epi == MM_EPI_SCORE;
+  const int lanes = p.epi == MM_EPI_GLU ? 2 * p.lanes : p.lanes;  // (a gated block's features take two each)
+  const int64_t lanes128 = (lanes + BM - 1) / BM;
   const int blocks = (p.red + BK - 1) / BK;
   const int split_bn = p.cols <= 32 && p.b.red_major ? 32 : 64;
   // tiles of that width (ragged columns: where they all fit one, each group with rows has one)
   const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
-  if (p.rag != MM_RAG_RED && p.epi == MM_EPI_STORE && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
+  if (p.rag != MM_RAG_RED && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
     a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
-  const int cg = !gen && p.rag != MM_RAG_RED && p.lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
+  const int cg = !gen && p.rag != MM_RAG_RED && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
   const int units = cg == 2 ? pairs : sms;
-  a.lane_tiles = (p.lanes + BM * cg - 1) / (BM * cg);
+  a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
   if (a.split > 1) {
     a.bn = split_bn;
@@ -1394,7 +1520,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
     const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
-  } else if (p.epi != MM_EPI_STATS) {
+  } else if (!stats) {
     const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 0, cg, units);
     a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;
   }
@@ -1413,13 +1539,13 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   a.by_lanes = Divider(a.lane_tiles), a.by_panel = Divider(a.lane_tiles * kPanel), a.by_matrix = Divider(a.lane_tiles * a.col_tiles);
   const MmEpiArgs& ep = p.e;
   const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
-  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
+  a.rows_out = p.epi != MM_EPI_GLU && !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
                by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   CUtensorMap ta = {}, tb = {};
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
     const uint64_t red = p.red;
-    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? p.lanes : red, groups, p.a.red_major ? BM : BK, a.a_blocks) &&
+    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? lanes : red, groups, p.epi == MM_EPI_GLU ? 16 : p.a.red_major ? BM : BK, a.a_blocks) &&
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK, a.b_blocks);
     if (!ok) return cudaErrorInvalidValue;
   }
@@ -1435,9 +1561,9 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   //    back. A longer d is added up as for 16 bits.
   a.seg = kSegFold;
   a.accs = 1;
-  if (p.epi == MM_EPI_STATS && (cg == 2 || p.red > 2 * kSegStats))
+  if (stats && (cg == 2 || p.red > 2 * kSegStats))
     a.seg = kSegStats, a.fold = cg == 1;
-  else if (p.epi == MM_EPI_STATS && p.red > kSegStats)
+  else if (stats && p.red > kSegStats)
     a.seg = (p.red + 2 * BK - 1) / (2 * BK) * BK, a.accs = 2;
   else if (ep.out_f32 && !ep.acc_in && p.rag == MM_RAG_RED)
     a.seg = kSegStore;

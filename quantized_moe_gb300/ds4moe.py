@@ -35,6 +35,9 @@ EXPORTED = ("ds4moe_create", "ds4moe_create_subset", "ds4moe_forward", "ds4moe_f
             "ds4moe_grouped_mm", "ds4moe_grouped_mm_dx", "ds4moe_grouped_mm_dw",
             "ds4moe_linear", "ds4moe_linear_grad", "ds4moe_linear_grad_workspace",
             "ds4moe_cross_entropy", "ds4moe_cross_entropy_grad", "ds4moe_cross_entropy_workspace",
+            "ds4moe_grouped_glu", "ds4moe_grouped_glu_grad",
+            "ds4moe_logprobs", "ds4moe_logprobs_workspace",
+            "ds4moe_distill", "ds4moe_distill_grad", "ds4moe_distill_workspace",
             "ds4moe_ops_status",
             "ds4moe_destroy", "ds4moe_last_error")
 DS4MOE_NOALLOC_MAX_LOGITS = 262144
@@ -120,14 +123,25 @@ def lib() -> ctypes.CDLL:
         L.ds4moe_linear_grad.argtypes = [vp] * 7 + [i32] * 5 + [i64] * 6 + [vp, i64, vp]
         L.ds4moe_cross_entropy.argtypes = [vp] * 5 + [i32] * 5 + [i64] * 2 + [vp, i64, vp]
         L.ds4moe_cross_entropy_grad.argtypes = [vp] * 7 + [i32] * 5 + [i64] * 4 + [vp, i64, vp]
+        f32 = ctypes.c_float
+        L.ds4moe_grouped_glu.argtypes = [vp] * 5 + [i32] * 6 + [i64] * 5 + [vp]
+        L.ds4moe_grouped_glu_grad.argtypes = [vp] * 8 + [i32] * 6 + [i64] * 9 + [vp]
+        L.ds4moe_logprobs.argtypes = [vp] * 8 + [i32] * 6 + [f32] + [i64] * 2 + [vp, i64, vp]
+        L.ds4moe_distill.argtypes = [vp] * 7 + [i32] * 5 + [f32] + [i64] * 2 + [vp, i64, vp]
+        L.ds4moe_distill_grad.argtypes = [vp] * 9 + [i32] * 5 + [f32] + [i64] * 4 + [vp, i64, vp]
         L.ds4moe_ops_status.argtypes = [ctypes.POINTER(i32)]
         for name in ("grouped_mm", "grouped_mm_dx", "grouped_mm_dw", "linear", "linear_grad", "cross_entropy",
-                     "cross_entropy_grad", "ops_status"):
+                     "cross_entropy_grad", "grouped_glu", "grouped_glu_grad", "logprobs", "distill", "distill_grad",
+                     "ops_status"):
             getattr(L, "ds4moe_" + name).restype = ctypes.c_int
         L.ds4moe_linear_grad_workspace.argtypes = [i32, i32, i32]
         L.ds4moe_linear_grad_workspace.restype = i64
         L.ds4moe_cross_entropy_workspace.argtypes = [i32, i32, i32]
         L.ds4moe_cross_entropy_workspace.restype = i64
+        L.ds4moe_logprobs_workspace.argtypes = [i32] * 4
+        L.ds4moe_logprobs_workspace.restype = i64
+        L.ds4moe_distill_workspace.argtypes = [i32] * 4
+        L.ds4moe_distill_workspace.restype = i64
         L.ds4moe_destroy.argtypes = [vp]
         L.ds4moe_destroy.restype = None
         L.ds4moe_last_error.argtypes = []
@@ -354,6 +368,64 @@ def ds4moe_cross_entropy_grad(x, w, labels, lse, dloss, dx, dw, rows: int, vocab
                                            _operand(dloss), _operand(dx, lddx), _operand(dw, lddw), rows, vocab, d,
                                            _enum(DTYPES, dtype), ignore_index, ldx, ldw, lddx, lddw,
                                            _operand(workspace), workspace_bytes, stream))
+
+
+def ds4moe_grouped_glu(x, w, offsets, h, rows: int, n: int, k: int, n_groups: int = 1, act="silu", dtype="bf16",
+                       zout=None, ldx: int = 0, ldw: int = 0, w_stride: int = 0, ldh: int = 0, ldz: int = 0,
+                       stream: int = 0) -> None:
+    """h[t] = act(G_g x[t]) * (U_g x[t]) for the rows t of each group g (offsets None: one dense block), w = [G_g; U_g];
+    zout receives both factors before the activation."""
+    _check(lib().ds4moe_grouped_glu(_operand(x, ldx), _operand(w, ldw, w_stride), _operand(offsets), _operand(h, ldh),
+                                    _operand(zout, ldz), rows, n, k, n_groups, _enum(ACTS, act), _enum(DTYPES, dtype),
+                                    ldx, ldw, w_stride, ldh, ldz, stream))
+
+
+def ds4moe_grouped_glu_grad(dh, x, w, offsets, z, dz, dx, dw, rows: int, n: int, k: int, n_groups: int = 1, act="silu",
+                            dtype="bf16", lddh: int = 0, ldx: int = 0, ldw: int = 0, w_stride: int = 0, ldz: int = 0,
+                            lddz: int = 0, lddx: int = 0, lddw: int = 0, dw_stride: int = 0, stream: int = 0) -> None:
+    """Gradients of ds4moe_grouped_glu: dz (of zout), dx and dw (each of these two may be None)."""
+    _check(lib().ds4moe_grouped_glu_grad(_operand(dh, lddh), _operand(x, ldx), _operand(w, ldw, w_stride),
+                                         _operand(offsets), _operand(z, ldz), _operand(dz, lddz), _operand(dx, lddx),
+                                         _operand(dw, lddw, dw_stride), rows, n, k, n_groups, _enum(ACTS, act),
+                                         _enum(DTYPES, dtype), lddh, ldx, ldw, w_stride, ldz, lddz, lddx, lddw, dw_stride,
+                                         stream))
+
+
+def ds4moe_logprobs_workspace(rows: int, vocab: int, n_tokens: int, top_k: int) -> int:
+    return lib().ds4moe_logprobs_workspace(rows, vocab, n_tokens, top_k)
+
+
+def ds4moe_logprobs(x, w, tokens, logprob, lse, entropy, top_index, top_logprob, rows: int, vocab: int, d: int,
+                    n_tokens: int = 1, top_k: int = 0, dtype="bf16", temperature: float = 1.0, workspace=None,
+                    workspace_bytes: int = 0, ldx: int = 0, ldw: int = 0, stream: int = 0) -> None:
+    """Log probabilities of the tokens under softmax(W x / temperature), its lse and entropy, and the top_k best words."""
+    _check(lib().ds4moe_logprobs(_operand(x, ldx), _operand(w, ldw), _operand(tokens), _operand(logprob), _operand(lse),
+                                 _operand(entropy), _operand(top_index), _operand(top_logprob), rows, vocab, d, n_tokens,
+                                 top_k, _enum(DTYPES, dtype), temperature, ldx, ldw, _operand(workspace),
+                                 workspace_bytes, stream))
+
+
+def ds4moe_distill_workspace(rows: int, vocab: int, d: int, top_k: int) -> int:
+    return lib().ds4moe_distill_workspace(rows, vocab, d, top_k)
+
+
+def ds4moe_distill(x, w, ids, teacher, loss, lse, logq, rows: int, vocab: int, d: int, top_k: int, dtype="bf16",
+                   temperature: float = 1.0, workspace=None, workspace_bytes: int = 0, ldx: int = 0, ldw: int = 0,
+                   stream: int = 0) -> None:
+    """loss[t] = sum_j p_j (log p_j - logq[t][j]) of a teacher's top_k logits against softmax(W x / temperature)."""
+    _check(lib().ds4moe_distill(_operand(x, ldx), _operand(w, ldw), _operand(ids), _operand(teacher), _operand(loss),
+                                _operand(lse), _operand(logq), rows, vocab, d, top_k, _enum(DTYPES, dtype), temperature,
+                                ldx, ldw, _operand(workspace), workspace_bytes, stream))
+
+
+def ds4moe_distill_grad(x, w, ids, teacher, lse, logq, dloss, dx, dw, rows: int, vocab: int, d: int, top_k: int,
+                        dtype="bf16", temperature: float = 1.0, workspace=None, workspace_bytes: int = 0, ldx: int = 0,
+                        ldw: int = 0, lddx: int = 0, lddw: int = 0, stream: int = 0) -> None:
+    """Gradients of sum_t dloss[t] loss[t] of ds4moe_distill with respect to x and w (each may be None)."""
+    _check(lib().ds4moe_distill_grad(_operand(x, ldx), _operand(w, ldw), _operand(ids), _operand(teacher), _operand(lse),
+                                     _operand(logq), _operand(dloss), _operand(dx, lddx), _operand(dw, lddw), rows, vocab,
+                                     d, top_k, _enum(DTYPES, dtype), temperature, ldx, ldw, lddx, lddw,
+                                     _operand(workspace), workspace_bytes, stream))
 
 
 def ds4moe_ops_status() -> int:
