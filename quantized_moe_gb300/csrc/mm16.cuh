@@ -9,7 +9,8 @@
 //   dW = dy^T x   lanes = input features (A = x, l contiguous),  cols = output features (B = dy, c contiguous)
 // and, of the cross entropy over a vocabulary with weights W, where dz is kept transposed ([v][t]):
 //   z          lanes = tokens (A = x, r contiguous), cols = words (B = W, r contiguous): a thread owns a
-//              token, so that its softmax needs no exchange between threads
+//              token, so that its softmax needs no exchange between threads. Scores of few tokens have them the
+//              other way round: no lane is idle, and all of shared memory holds W on its way
 //   dx = dz W  lanes = features (A = W, l contiguous), cols = tokens (B = dz, c contiguous)
 //   dW = dz x  lanes = features (A = x, l contiguous), cols = words (B = dz, r contiguous)
 // and, of the gated block with weights W = [gate; up] ([2 n][k]):
@@ -32,7 +33,8 @@ enum MmEpi : int {
   MM_EPI_STATS = 1,     // per lane: max and sum of exponentials over the tile's columns; the label's value
   MM_EPI_SOFTGRAD = 2,  // out = (exp(v / T - lse) - [column is the label]) * g
   MM_EPI_GLU = 3,       // out = act(gate) * up; lanes are the features of out, A has twice as many rows
-  MM_EPI_SCORE = 4      // per lane: as STATS of v / T, and the entropy's sum; the logits of listed words; the logits
+  MM_EPI_SCORE = 4,     // per lane: as STATS of v / T, and the entropy's sum; the logits of listed words; the logits
+  MM_EPI_SCORE_FEW = 5  // the same of few tokens: lanes are words, columns (up to kMmFewRows) tokens, a tile 32 words
 };
 enum MmAct : int { MM_ACT_NONE = 0, MM_ACT_RELU = 1, MM_ACT_SILU = 2, MM_ACT_GELU = 3 };
 
@@ -66,12 +68,14 @@ struct MmEpiArgs {
   float2* part;          // [column tiles][lanes] (max, sum)
   float* zlab;           // [lanes] the label's logit
   float inv_t;           // 1 / T
-  // scores: lanes are tokens, columns the vocabulary
-  float* ent;            // [column tiles][lanes] sum of (v - max) exp((v - max) / T)
-  const int2* want;      // [lanes][n_want] (word, place), ascending; words that there are not come last
+  // scores, of tokens against the vocabulary in tiles of kMmStatTile words (few tokens: kMmStatChunk)
+  float* ent;            // [tiles][tokens] sum of (v - max) exp((v - max) / T)
+  const int2* want;      // [tokens][n_want] (word, place), ascending; words that there are not come last
+  const uint16_t* first; // [tokens][tiles] the first entry of want in or behind a tile
   int n_want;
-  float* zwant;          // [lanes][n_want] the listed words' logits, by place
-  float* logits;         // [cols][lanes], or null
+  float* zwant;          // [tokens][n_want] the listed words' logits, by place
+  float* logits;         // [vocab][tokens], or null
+  float* chunk_max;      // [vocab / kMmStatChunk][tokens]; with logits, where tiles are larger
 };
 
 struct MmProblem {
@@ -162,6 +166,8 @@ inline bool mm_aligned(const MmOperand& o) {
 }
 // Words of one softmax partial: part[] has ceil(vocab / kMmStatTile) rows of one entry per token.
 constexpr int kMmStatTile = 256;
+constexpr int kMmStatChunk = 32;  // words of one chunk's maximum
+constexpr int kMmFewRows = 32;    // tokens of MM_EPI_SCORE_FEW
 
 // Sets kernel attributes on the current device (once per device).
 cudaError_t mm_prepare();
@@ -186,13 +192,14 @@ cudaError_t mm_grad_scale(const float* g, const int* labels, int ignore, int voc
 cudaError_t mm_glu_grad(const void* dh, int64_t lddh, const void* z, int64_t ldz, void* dz, int64_t lddz, const int* offsets,
                         int groups, int rows, int n, int act, int f16, cudaStream_t s);
 
-// Sorts each row's n words for the scores' epilogue (MmEpiArgs::want): a word outside the vocabulary comes last.
-cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int2* want, cudaStream_t s);
+// Sorts each row's n words for the scores' epilogue (MmEpiArgs::want, first): a word outside the vocabulary comes last.
+constexpr int kMmListed = 256, kMmTop = 64;  // most given words, and best words, of a row
+cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile, int2* want, uint16_t* first, cudaStream_t s);
 // What the scores' partials say of each row (temperature T = 1 / inv_t).
 struct MmScores {
   const float2* part;
   const float* ent;
-  int tiles, rows, vocab;
+  int tile, tiles, rows, vocab;  // words of a tile
   float inv_t;
   const float* zwant;   // [rows][n] logits of the listed words
   const int* words;     // [rows][n]
@@ -203,6 +210,7 @@ struct MmScores {
   float* logprob;       // [rows][n]
   float* entropy;       // [rows], or null
   const float* logits;  // [vocab][rows]
+  const float* chunk_max;
   int top_k;
   int* top_index;       // [rows][top_k]
   float* top_logprob;

@@ -17,7 +17,7 @@ constexpr int kMaxDevices = 64;
 constexpr int64_t kMaxWidth = 1 << 24;
 constexpr int kMaxGroups = 1024;
 constexpr int kPieceMax = 16384, kPieceMin = 256;  // words of one piece of the vocabulary
-constexpr int kMaxListed = 256, kMaxTop = 64;      // given words, and best words, of one row of scores
+constexpr int kMaxListed = ds4::kMmListed, kMaxTop = ds4::kMmTop;
 constexpr int kScoreRows = 128;                    // scores take blocks of so many rows at least, whatever the workspace
 
 static __device__ int g_mm_err;  // flags of ds4moe_ops_status
@@ -454,17 +454,20 @@ void block_groups(Check& c, const void* offsets, int n_groups) {
   if (!offsets && n_groups > 1) c.invalid("offsets is NULL with n_groups=" + std::to_string(n_groups) + " (a dense block has one)");
 }
 
-// Workspace of the scores of `rows` rows: softmax partials, sorted lists with their logits, all logits where the best
-// words are asked for.
+// Workspace of the scores of `rows` rows: softmax partials, sorted lists with their logits; where the best words are asked
+// for all logits, and the largest of each chunk.
 struct ScoreSpace {
-  int64_t part, ent, want, zwant, logits, total;
+  int64_t part, ent, want, first, zwant, chunk_max, logits, total;
   ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
-    const int64_t tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile;
+    const int tile = rows <= ds4::kMmFewRows ? ds4::kMmStatChunk : ds4::kMmStatTile;
+    const int64_t tiles = (vocab + tile - 1) / tile;
     part = 0;
     ent = up(8 * rows * tiles, 16);
     want = ent + up(4 * rows * tiles, 16);
-    zwant = want + up(8 * rows * n, 16);
-    logits = zwant + up(4 * rows * n, 16);
+    first = want + up(8 * rows * n, 16);
+    zwant = first + (n ? up(2 * rows * tiles, 16) : 0);
+    chunk_max = zwant + up(4 * rows * n, 16);
+    logits = chunk_max + (top_k ? up(4 * rows * ((vocab + ds4::kMmStatChunk - 1) / ds4::kMmStatChunk), 16) : 0);
     total = logits + (top_k ? up(4 * rows * vocab, 16) : 0);
   }
 };
@@ -492,7 +495,10 @@ int score_rows(Check& c, int rows, int vocab, int n, int top_k, int64_t bytes) {
 }
 cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, char* ws, cudaStream_t s) {
   const int vocab = call.vocab;
-  a.vocab = vocab, a.tiles = (vocab + ds4::kMmStatTile - 1) / ds4::kMmStatTile, a.err = call.err;
+  const ds4::MmOperand ox = {call.x, call.ldx, 0, 1}, ow = {call.w, call.ldw, 0, 1};
+  const bool few = block <= ds4::kMmFewRows && ds4::mm_aligned(ox) && ds4::mm_aligned(ow);
+  a.tile = few ? ds4::kMmStatChunk : ds4::kMmStatTile;
+  a.vocab = vocab, a.tiles = (vocab + a.tile - 1) / a.tile, a.err = call.err;
   const ScoreSpace at(block, vocab, a.n, a.top_k);
   cudaError_t e = cudaSuccess;
   for (int64_t t0 = 0; t0 < rows && e == cudaSuccess; t0 += block) {
@@ -502,15 +508,18 @@ cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, 
     const auto move = [&](auto*& p, int64_t per_row) { if (p) p += t0 * per_row; };
     move(b.words, a.n), move(b.lse, 1), move(b.logprob, a.n), move(b.entropy, 1), move(b.top_index, a.top_k);
     move(b.top_logprob, a.top_k), move(b.teacher, a.n), move(b.loss, 1);
-    ds4::MmProblem p = product(static_cast<const char*>(call.x) + 2 * t0 * call.ldx, call.ldx, true, call.w, call.ldw, true, nr, vocab,
-                               call.d, call.dtype, nullptr, 0, call.err);
-    p.epi = ds4::MM_EPI_SCORE;
+    const char* x = static_cast<const char*>(call.x) + 2 * t0 * call.ldx;
+    ds4::MmProblem p = few ? product(call.w, call.ldw, true, x, call.ldx, true, vocab, nr, call.d, call.dtype, nullptr, 0, call.err)
+                           : product(x, call.ldx, true, call.w, call.ldw, true, nr, vocab, call.d, call.dtype, nullptr, 0, call.err);
+    p.epi = few ? ds4::MM_EPI_SCORE_FEW : ds4::MM_EPI_SCORE;
     p.e.inv_t = a.inv_t;
     p.e.part = reinterpret_cast<float2*>(ws + at.part), p.e.ent = reinterpret_cast<float*>(ws + at.ent);
     p.e.want = reinterpret_cast<int2*>(ws + at.want), p.e.n_want = a.n, p.e.zwant = reinterpret_cast<float*>(ws + at.zwant);
+    p.e.first = reinterpret_cast<uint16_t*>(ws + at.first);
     p.e.logits = a.top_k ? reinterpret_cast<float*>(ws + at.logits) : nullptr;
-    b.part = p.e.part, b.ent = p.e.ent, b.zwant = p.e.zwant, b.logits = p.e.logits;
-    if (a.n) e = ds4::mm_sort_words(b.words, a.n, vocab, nr, reinterpret_cast<int2*>(ws + at.want), s);
+    p.e.chunk_max = reinterpret_cast<float*>(ws + at.chunk_max);
+    b.part = p.e.part, b.ent = p.e.ent, b.zwant = p.e.zwant, b.logits = p.e.logits, b.chunk_max = p.e.chunk_max;
+    if (a.n) e = ds4::mm_sort_words(b.words, a.n, vocab, nr, a.tile, reinterpret_cast<int2*>(ws + at.want), reinterpret_cast<uint16_t*>(ws + at.first), s);
     if (e == cudaSuccess) e = ds4::mm_launch(p, s);
     if (e == cudaSuccess) e = ds4::mm_score_join(b, s);
   }

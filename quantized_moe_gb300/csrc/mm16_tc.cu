@@ -46,7 +46,8 @@ constexpr int A_BYTES = BM * BK * 2;      // 16 KB
 constexpr int kMaxStages = 12;
 constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulator where the result is fp32
 constexpr int kSegFold = 16384;           // and where it has 16 bits
-constexpr int kEpiPlain = 5;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
+constexpr int kEpiPlain = 6;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
+constexpr int kEpiScoreOne = 7;           // MM_EPI_SCORE where one accumulator takes a logit's whole sum
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -73,6 +74,7 @@ struct TcArgs {
   MmProblem p;
   int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
   int a_blocks, b_blocks;     // boxes of 64 x 64 that one copy of an MN-major operand brings
+  int glu_whole;              // one copy brings a gated block's 64 gate and 64 up rows (else 16 rows each)
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
   int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
@@ -115,6 +117,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
         "[%6];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(g), "r"(bar)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load5(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int u, int g, uint32_t bar) {
+  if (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(g), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, "
+        "%6}], [%7];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(u), "r"(g), "r"(bar)
         : "memory");
 }
 
@@ -548,6 +566,44 @@ __device__ __forceinline__ void frag_out(uint32_t stage, int quad, int lane, con
                  "r"(pack16(f.v[j][2][0], f.v[j][2][1], f16)), "r"(pack16(f.v[j][3][0], f.v[j][3][1], f16))
                  : "memory");
 }
+// The gated block's fragments: the warp's lanes are 16 features' gates and their ups, so that a thread holds both factors of
+// its results. z: a staged row is the tile's 64 gates and then their 64 ups; h: its 64 features.
+__device__ __forceinline__ void glu_frag_out(uint32_t stage, int quad, int lane, const Frag& f, int f16) {
+  const uint32_t at = stage + (uint32_t)((lane & 7) * kRowBytes + (lane >> 4) * 128 + quad * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at + 8 * j * kRowBytes),
+                 "r"(pack16(f.v[j][0][0], f.v[j][0][1], f16)), "r"(pack16(f.v[j][1][0], f.v[j][1][1], f16)),
+                 "r"(pack16(f.v[j][2][0], f.v[j][2][1], f16)), "r"(pack16(f.v[j][3][0], f.v[j][3][1], f16))
+                 : "memory");
+}
+__device__ __forceinline__ void glu_frag_act(Frag& f, int act) {
+  const auto each = [&](auto fn) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) f.v[j][r][q] = fn(f.v[j][r][q]) * f.v[j][r + 2][q];
+  };
+  if (act == MM_ACT_SILU)
+    each([](float v) { return mm_silu(v); });
+  else if (act == MM_ACT_GELU)
+    each([](float v) { return mm_gelu(v); });
+  else if (act == MM_ACT_RELU)
+    each([](float v) { return mm_relu(v); });
+  else
+    each([](float v) { return v; });
+}
+__device__ __forceinline__ void glu_frag_out_h(uint32_t stage, int quad, int lane, const Frag& f, int f16) {
+  const uint32_t at = stage + (uint32_t)((8 * (lane >> 4) + (lane & 7)) * kRowBytes + quad * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+  for (int j = 0; j < 4; j += 2)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(at + 8 * j * kRowBytes),
+                 "r"(pack16(f.v[j][0][0], f.v[j][0][1], f16)), "r"(pack16(f.v[j][1][0], f.v[j][1][1], f16)),
+                 "r"(pack16(f.v[j + 1][0][0], f.v[j + 1][0][1], f16)), "r"(pack16(f.v[j + 1][1][0], f.v[j + 1][1][1], f16))
+                 : "memory");
+}
 __device__ __forceinline__ void frag_add(uint32_t stage, int quad, int lane, Frag& f, int f16) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -620,35 +676,60 @@ __device__ __forceinline__ float exp2_fast(float v) {
   asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ void epi_score(const float (&v)[32], int nv, float c, float& m, float& s, float& u) {
-  float top = m;
+// Words from nv on are made -inf: they add nothing, and no word's arithmetic hangs on a branch (written with a condition for
+// each word the chunk ran one word after the other, 4.5 thousand cycles where this takes one). Returns the chunk's largest.
+__device__ __forceinline__ float epi_score(float (&v)[32], int nv, float c, float& m, float& s, float& u) {
+  if (nv < 32) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < nv) top = fmaxf(top, v[j]);
-  if (top == -INFINITY) {
+    for (int j = 0; j < 32; ++j) v[j] = j < nv ? v[j] : -INFINITY;
+  }
+  float q[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int j = 4; j < 32; ++j) q[j & 3] = fmaxf(q[j & 3], v[j]);
+  const float chunk = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), top = fmaxf(m, chunk);
+  if (top == -INFINITY) {  // only words of probability zero so far (NaN logits still reach the sum)
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) bad |= j < nv && v[j] != v[j];
+    for (int j = 0; j < 32; ++j) bad |= v[j] != v[j];
     if (bad) s = NAN;
-    return;
+    return -INFINITY;
   }
-  if (m != top) {
-    const float d = fmaxf(m - top, -1e30f), r = exp2_fast(d * c);  // (m = -inf: s and u are 0, or NaN)
-    u = (u + d * s) * r;
-    s *= r;
-    m = top;
-  }
-  float t = 0.f, w = 0.f;
+  const float d = fmaxf(m - top, -1e30f), r = exp2_fast(d * c);  // (m = -inf: s and u are 0, or NaN)
+  float t[4] = {s * r, 0.f, 0.f, 0.f}, w[4] = {(u + d * s) * r, 0.f, 0.f, 0.f};
+  m = top;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
-    if (j < nv) {
-      const float d = v[j] - top, e = exp2_fast(d * c);
-      t += e;
-      w += fmaxf(d, -1e30f) * e;  // (words of probability zero add nothing)
-    }
+    const float dj = v[j] - top, e = exp2_fast(dj * c);
+    t[j & 3] += e;
+    w[j & 3] += fmaxf(dj, -1e30f) * e;  // (words of probability zero add nothing)
   }
-  s += t;
-  u += w;
+  s = (t[0] + t[1]) + (t[2] + t[3]);
+  u = (w[0] + w[1]) + (w[2] + w[3]);
+  return chunk;
+}
+
+// One chunk of few tokens' scores: thread's token t of `tokens`, 32 words from w0 (nv exist).
+__device__ __forceinline__ void score_few(const MmEpiArgs& e, float (&v)[32], int w0, int nv, int t, int tokens, int tiles) {
+  const int64_t tile = w0 / kMmStatChunk;
+  int at = 0, next = INT32_MAX;
+  if (e.n_want > 0) {
+    at = *(e.first + (int64_t)t * tiles + tile);
+    if (at < e.n_want) next = (e.want + (int64_t)t * e.n_want + at)->x;
+  }
+  float m = -INFINITY, s = 0.f, u = 0.f;
+  epi_score(v, nv, e.inv_t * 1.4426950408889634f, m, s, u);
+  e.part[tile * tokens + t] = make_float2(m, s);
+  e.ent[tile * tokens + t] = u;
+  if (e.logits) store_col(e.logits + (int64_t)w0 * tokens + t, tokens, nv, v);
+  while (next < w0 + nv) {
+    float own = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j == next - w0) own = v[j];
+    const int2* q = e.want + (int64_t)t * e.n_want + at;
+    e.zwant[(int64_t)t * e.n_want + q->y] = own;
+    next = ++at < e.n_want ? q[1].x : INT32_MAX;
+  }
 }
 
 template <int CG, int EPI, bool GEN>
@@ -738,7 +819,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int a_boxes = EPI == MM_EPI_GLU ? BM / 16 : a_red ? 1 : 2 / a.a_blocks;
+    const int a_boxes = EPI == MM_EPI_GLU ? (a.glu_whole ? 1 : BM / 16) : a_red ? 1 : 2 / a.a_blocks;
     Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -757,7 +838,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (of_a) {
           if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);  // (copies may report before it)
           if (lane < a_boxes) {
-            if (EPI == MM_EPI_GLU)  // 16 rows of the gate, the same 16 of up, and so on
+            if (EPI == MM_EPI_GLU && a.glu_whole)  // 16 rows of the gate, the same 16 of up, and so on
+              tma_load5<CG>(st, &ta, r, 0, 0, la / 32, ga, bar);
+            else if (EPI == MM_EPI_GLU)
               tma_load<CG>(st + lane * 2048, &ta, r, la / 2 + 16 * (lane >> 1) + (lane & 1 ? p.lanes : 0), 0, ga, bar);
             else if (a_red)
               tma_load<CG>(st, &ta, r, la, 0, ga, bar);
@@ -1004,7 +1087,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.live = false;
     }
     const int c_first = 32 * half, c_step = 64;
-    constexpr bool kStats = EPI == MM_EPI_STATS || EPI == MM_EPI_SCORE;
+    constexpr bool kScore = EPI == MM_EPI_SCORE || EPI == kEpiScoreOne, kStats = EPI == MM_EPI_STATS || kScore;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
     Walk<CG> walk;
@@ -1014,7 +1097,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
       // what the tile needs besides its sums is fetched before they are waited for
-      const bool by_rows = !kStats && a.rows_out;
+      const bool by_rows = !kStats && EPI != MM_EPI_SCORE_FEW && a.rows_out;
       const int64_t group_out = p.rag == MM_RAG_RED ? o.g * e.group_stride : 0;
       const void* add = e.accumulate ? e.out : e.residual;
       const int64_t add_ld = e.accumulate ? e.ld : e.ldr;
@@ -1048,20 +1131,14 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       // the listed words of the thread's token: the first one from the tile's start on
       const int2* want = nullptr;
       int want_left = 0, want_next = INT32_MAX;
-      if (EPI == MM_EPI_SCORE && e.n_want > 0 && l0 + 32 * quad + lane < p.lanes) {
-        want = e.want + (int64_t)(l0 + 32 * quad + lane) * e.n_want;
-        want_left = e.n_want;
-        while (want_left > 0) {  // (halves: the first that is not below)
-          const int mid = want_left >> 1;
-          if (want[mid].x < o.c0)
-            want += mid + 1, want_left -= mid + 1;
-          else
-            want_left = mid;
-        }
-        want_left = (int)(e.want + (int64_t)(l0 + 32 * quad + lane + 1) * e.n_want - want);
+      if (kScore && e.n_want > 0 && l0 + 32 * quad + lane < p.lanes) {
+        const int64_t t_at = l0 + 32 * quad + lane;
+        const int at = *(e.first + t_at * a.col_tiles + o.c0 / kMmStatTile);
+        want = e.want + t_at * e.n_want + at;
+        want_left = e.n_want - at;
         if (want_left > 0) want_next = want->x;
       }
-      constexpr bool kHold = kStats && CG == 2;  // sums over accumulators are held in registers
+      constexpr bool kHold = kStats && CG == 2 && EPI != kEpiScoreOne;  // sums over accumulators are held in registers
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       const bool folds = a.fold && o.red > a.seg;
       bool ok = true;
@@ -1113,7 +1190,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (part > 0) ok = false;
         }
         if (!ok) break;
-        const bool two = kStats && !kHold && a.accs > 1;
+        const bool two = kStats && !kHold && EPI != kEpiScoreOne && a.accs > 1;
         if (two) {  // fold the first accumulator into the second and hand it back: the next tile's first half needs it soon
           for (int c = c_first; o.red > a.seg && c < o.n && l0 + 32 * quad < p.lanes; c += c_step) {
             float v[32], more[32];
@@ -1131,7 +1208,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
         if (kStats) {
           const uint32_t sums = two && o.red > a.seg ? taddr + acc_stride : taddr;
-#pragma unroll
+#pragma unroll(EPI == kEpiScoreOne ? 1 : 4)
           for (int i = 0; i < 4; ++i) {
             const int c = c_first + i * c_step;
             if (c >= o.n || l0 + 32 * quad >= p.lanes) break;  // (no words, or no tokens)
@@ -1144,10 +1221,12 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
               if (k + a.seg < o.red) continue;
             }
             const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
-            if (EPI == MM_EPI_SCORE) {
-              epi_score(y, nv, e.inv_t * 1.4426950408889634f, m, total, spread);
-              if (e.logits && l0 + 32 * quad + lane < p.lanes)
+            if (kScore) {
+              const float most = epi_score(y, nv, e.inv_t * 1.4426950408889634f, m, total, spread);
+              if (e.logits && l0 + 32 * quad + lane < p.lanes) {
                 store_col(e.logits + (int64_t)(o.c0 + c) * p.lanes + l0 + 32 * quad + lane, p.lanes, nv, y);
+                e.chunk_max[(int64_t)((o.c0 + c) / kMmStatChunk) * p.lanes + l0 + 32 * quad + lane] = most;
+              }
               while (want_next < o.c0 + c + nv) {
                 const int j_at = want_next - (o.c0 + c);
                 if (j_at >= 0) {  // (the other half's words are passed over)
@@ -1170,6 +1249,59 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
                 if (j == at) own = y[j];
               e.zlab[l0 + 32 * quad + lane] = own;
             }
+          }
+        } else if (EPI == MM_EPI_SCORE_FEW) {
+          const int w0 = l0 + 32 * quad;  // the warp's words; a thread has one of them for every token, and takes one token's
+          if (half == 0 && w0 < p.lanes) {
+            float v[32];
+            float* x = reinterpret_cast<float*>(out_stage) + quad * (32 * 33);
+            tmem_ld32(taddr, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j * 33 + lane] = v[j];
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = x[lane * 33 + j];
+            __syncwarp();
+            if (lane < o.n) score_few(e, v, w0, min(32, p.lanes - w0), lane, p.cols, (p.lanes + kMmStatChunk - 1) / kMmStatChunk);
+          }
+        } else if (by_rows && EPI == MM_EPI_GLU) {
+          for (int c = c_first; c < o.n; c += c_step) {
+            Frag f;
+            tmem_ld_frag(taddr + c, f);
+            if (CG == 1) {
+              for (int k = 1; k < a.split; ++k) {
+                const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) {
+                    f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
+                    f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
+                  }
+              }
+            }
+            const int i = threadIdx.x & 127;
+            const int64_t row0 = o.c0 + c;
+            if (e.z) {
+              glu_frag_out(stage, quad, lane, f, p.f16);
+              named_bar(2 + half, 128);
+              const int feature = l0 / 2 + (i & 7) * 8;
+              rows.live = feature < p.lanes;
+              rows.store(e.z, (row0 + rows.row) * e.ldz + ((i & 8) ? p.lanes : 0) + feature, e.ldz, o.n - c);
+              named_bar(2 + half, 128);
+            }
+            glu_frag_act(f, e.act);
+            glu_frag_out_h(stage, quad, lane, f, p.f16);
+            named_bar(2 + half, 128);
+            const int feature = l0 / 2 + (i & 7) * 8;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // a row's 64 features are eight pieces of 16 bytes
+              const int row = (i >> 3) + 16 * k;
+              if (feature < p.lanes && c + row < o.n)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(e.out) + (row0 + row) * e.ld + feature) =
+                    lds128(stage + (uint32_t)(row * kRowBytes + (i & 7) * 16));
+            }
+            named_bar(2 + half, 128);
           }
         } else if (by_rows) {
           for (int c = c_first; c < o.n; c += c_step) {
@@ -1301,7 +1433,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
       }
       if (!ok) break;
-      if (EPI == MM_EPI_SCORE) {
+      if (kScore) {
         float4* x = reinterpret_cast<float4*>(out_stage) + 32 * quad + lane;
         const int l = l0 + 32 * quad + lane;
         if (half) *x = make_float4(m, total, spread, 0.f);
@@ -1354,6 +1486,19 @@ int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be
 // 4D map with boxes of 64 contiguous elements, 128-byte swizzle: (contiguous index, row, -, group) with box_rows rows;
 // or, for an MN-major operand whose width is a multiple of 64, (index in a block of 64, row, block, group) with
 // `blocks` blocks of BK rows, which one copy lays one after the other.
+// A gated block's weights, n a multiple of 16: (reduction, row of 16, gate or up, 16 rows, group); one copy brings four times 16
+// gate rows and the same 16 up rows.
+bool make_glu_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t red, uint64_t n, uint64_t groups) {
+  const cuuint64_t row = (cuuint64_t)o.ld * 2;
+  const cuuint64_t dims[5] = {red, 16, 2, n / 16, groups};
+  const cuuint64_t strides[4] = {row, row * n, row * 16, groups > 1 ? (cuuint64_t)o.group_stride * 2 : row};
+  const cuuint32_t box[5] = {BK, 16, 2, BM / 32, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return g_encode(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(o.p),
+                  dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows, int blocks) {
   const cuuint64_t row = (cuuint64_t)o.ld * 2;
   const cuuint64_t dims[4] = {blocks > 1 ? 64 : inner, rows, blocks > 1 ? inner / 64 : 1, groups};
@@ -1394,7 +1539,10 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
     case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SOFTGRAD: return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
     case MM_EPI_GLU: return launch<CG, MM_EPI_GLU, GEN>(ta, tb, a, grid, s);
-    case MM_EPI_SCORE: return launch<CG, MM_EPI_SCORE, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_SCORE:
+      if (!GEN && a.p.red <= kSegStats) return launch<CG, kEpiScoreOne, false>(ta, tb, a, grid, s);
+      return launch<CG, MM_EPI_SCORE, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_SCORE_FEW: return CG == 1 && !GEN ? launch<1, MM_EPI_SCORE_FEW, false>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
     default: break;
   }
   const MmEpiArgs& e = a.p.e;
@@ -1467,6 +1615,9 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_epi<1, true>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiPlain, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlain, false>();
+  if (e == cudaSuccess) e = prepare_one<1, kEpiScoreOne, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiScoreOne, false>();
+  if (e == cudaSuccess) e = prepare_one<1, MM_EPI_SCORE_FEW, false>();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
@@ -1509,12 +1660,16 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
-  const int cg = !gen && p.rag != MM_RAG_RED && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
+  const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
+  const int cg = !gen && !few_tokens && p.rag != MM_RAG_RED && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
   const int units = cg == 2 ? pairs : sms;
   a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
   if (a.split > 1) {
     a.bn = split_bn;
+  } else if (few_tokens) {
+    if (gen || p.cols > kMmFewRows) return cudaErrorInvalidValue;
+    a.bn = kMmFewRows;
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
     // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
@@ -1539,13 +1694,15 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   a.by_lanes = Divider(a.lane_tiles), a.by_panel = Divider(a.lane_tiles * kPanel), a.by_matrix = Divider(a.lane_tiles * a.col_tiles);
   const MmEpiArgs& ep = p.e;
   const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
-  a.rows_out = p.epi != MM_EPI_GLU && !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
+  a.glu_whole = p.epi == MM_EPI_GLU && p.lanes % 16 == 0 && p.a.ld < ((int64_t)1 << 38) / p.lanes;  // (a map's strides end at 2^40 bytes)
+  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
                by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   CUtensorMap ta = {}, tb = {};
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
     const uint64_t red = p.red;
-    const bool ok = make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? lanes : red, groups, p.epi == MM_EPI_GLU ? 16 : p.a.red_major ? BM : BK, a.a_blocks) &&
+    const bool ok = (a.glu_whole ? make_glu_map(&ta, p.a, p.f16, red, p.lanes, groups) :
+                     make_map(&ta, p.a, p.f16, p.a.red_major ? red : p.lanes, p.a.red_major ? lanes : red, groups, p.epi == MM_EPI_GLU ? 16 : p.a.red_major ? BM : BK, a.a_blocks)) &&
                     make_map(&tb, p.b, p.f16, p.b.red_major ? red : p.cols, p.b.red_major ? p.cols : red, 1, p.b.red_major ? a.b_box : BK, a.b_blocks);
     if (!ok) return cudaErrorInvalidValue;
   }
@@ -1561,7 +1718,9 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   //    back. A longer d is added up as for 16 bits.
   a.seg = kSegFold;
   a.accs = 1;
-  if (stats && (cg == 2 || p.red > 2 * kSegStats))
+  if (few_tokens)  // (the sums of 32 tokens are added up in no time)
+    a.seg = kSegStats, a.fold = 1;
+  else if (stats && (cg == 2 || p.red > 2 * kSegStats))
     a.seg = kSegStats, a.fold = cg == 1;
   else if (stats && p.red > kSegStats)
     a.seg = (p.red + 2 * BK - 1) / (2 * BK) * BK, a.accs = 2;
