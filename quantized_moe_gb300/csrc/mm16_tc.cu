@@ -48,6 +48,7 @@ constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulato
 constexpr int kSegFold = 16384;           // and where it has 16 bits
 constexpr int kEpiPlain = 6;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kEpiScoreOne = 7;           // MM_EPI_SCORE where one accumulator takes a logit's whole sum
+constexpr int kAccCols = 256;             // columns of one accumulator, the widest MMA
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -72,7 +73,7 @@ struct Divider {
 
 struct TcArgs {
   MmProblem p;
-  int bn, stages, b_box;      // column tile, pipeline depth, rows of a column-operand box
+  int bn, stages, b_box;      // column tile (above kAccCols: tiles that need it take both accumulators), pipeline depth, rows of a column-operand box
   int a_blocks, b_blocks;     // boxes of 64 x 64 that one copy of an MN-major operand brings
   int glu_whole;              // one copy brings a gated block's 64 gate and 64 up rows (else 16 rows each)
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
@@ -755,9 +756,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
-  const int acc_stride = max(a.bn, 32);
+  const int acc_stride = min(max(a.bn, 32), kAccCols);
+  // Tiles wider than an accumulator: their columns run on into the other one, so that one pass over A serves up to 512.
+  constexpr bool kWide = CG == 2 && !GEN && (EPI == kEpiPlain || EPI == MM_EPI_STORE || EPI == MM_EPI_GLU);
   uint32_t tmem_cols = 32;
-  while (tmem_cols < 2u * max(a.bn, 32)) tmem_cols *= 2;
+  while (tmem_cols < 2u * acc_stride) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
@@ -824,8 +827,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
-      const int nb = mma_n<CG>(p, o.n) / CG;  // columns that this CTA stages
-      const int b_boxes = b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
+      const bool wide = kWide && o.n > kAccCols;
+      const int nb = mma_n<CG>(p, wide ? o.n - kAccCols : o.n) / CG;  // columns that this CTA stages (of the second part)
+      const int b_boxes = kWide && wide ? kAccCols / CG / a.b_box + (nb + a.b_box - 1) / a.b_box : b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
       const int b_box_bytes = b_red ? a.b_box * 128 : a.b_blocks * 8192;
       const uint32_t bytes = CG * (A_BYTES + b_boxes * b_box_bytes);
       const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
@@ -851,7 +855,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         } else if (lane < b_boxes) {
           const uint32_t to = st + A_BYTES + lane * b_box_bytes;
-          if (b_red)
+          if (kWide && wide) {
+            const int c = lane * a.b_box, first_part = kAccCols / CG;  // of the CTA's columns
+            tma_load<CG>(to, &tb, r, c < first_part ? o.c0 + first_part * rank + c : cb + kAccCols - first_part + c, 0, 0, bar);
+          } else if (b_red)
             tma_load<CG>(to, &tb, r, cb + lane * a.b_box, 0, 0, bar);
           else if (a.b_blocks > 1)
             tma_load<CG>(to, &tb, 0, r, cb / 64 + lane * a.b_blocks, 0, bar);
@@ -914,19 +921,22 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       for (int t = first; t < tiles && ok; t += step) {
         const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
         if (o.red <= 0 || o.n <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
-        const int n = mma_n<CG>(p, o.n);
+        const bool wide = kWide && o.n > kAccCols;
+        const int n = wide ? kAccCols : mma_n<CG>(p, o.n);
         const uint32_t idesc = (1u << 4) | type << 7 | type << 10 | (p.a.red_major ? 0u : 1u << 15) |
                                (p.b.red_major ? 0u : 1u << 16) | (uint32_t)(n >> 3) << 17 | (uint32_t)(BM * CG >> 4) << 24;
         // Accumulators take turns from tile to tile (or, of a result added up in memory, from seg to seg). A tile that is
         // summed up in tensor memory stays with its own one, seg after seg, and so does the tile after it: the other
         // one holds the sum, which the epilogue is done with when it hands the last seg's accumulator back.
         const bool folds = a.fold && o.red > a.seg;
+        const uint32_t idesc_rest = wide ? (idesc & ~(0x3fu << 17)) | (uint32_t)(mma_n<CG>(p, o.n - kAccCols) >> 3) << 17 : 0u;
         uint32_t d = 0;
         int in_seg = 0;  // reduction already in this accumulator
         for (int k = 0; k < o.red; k += BK) {
           if (in_seg == 0) {
-            const int b = a.accs == 1 || k == 0 ? buf : 1;  // (1: the second accumulator of the same tile)
-            if (!mbar_wait(acc_empty + b, (used >> b & 1) ^ 1, abort_flag, p.err, 6)) {
+            const int b = wide ? 0 : a.accs == 1 || k == 0 ? buf : 1;  // (1: the second accumulator of the same tile)
+            if (!mbar_wait(acc_empty + b, (used >> b & 1) ^ 1, abort_flag, p.err, 6) ||
+                (kWide && wide && !mbar_wait(acc_empty + 1, (used >> 1 & 1) ^ 1, abort_flag, p.err, 6))) {
               ok = false;
               break;
             }
@@ -942,7 +952,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (left & 15) cleaned ^= 1u << s;
           tc_fence_after();
           const uint64_t da = a_desc + (uint32_t)(s * stage_bytes >> 4), db = b_desc + (uint32_t)(s * stage_bytes >> 4);
-          if (left > 48) {
+          if (kWide && wide) {
+            const uint64_t rest = db + (kAccCols / CG * BK * 2 >> 4);
+            for (int i = 0; 16 * i < left; ++i) {
+              mma<CG>(d, da + i * a_step, db + i * b_step, idesc, in_seg | i);
+              mma<CG>(d + kAccCols, da + i * a_step, rest + i * b_step, idesc_rest, in_seg | i);
+            }
+          } else if (left > 48) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, in_seg | i);
           } else {
@@ -952,7 +968,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (++s == a.stages) s = 0, ph ^= 1;
           in_seg += BK;
           if (in_seg == a.seg || k + BK >= o.red) {
-            if (a.accs == 1) {
+            if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
+              commit<CG>(acc_full);
+              commit<CG>(acc_full + 1);
+              used ^= 3u;
+            } else if (a.accs == 1) {
               commit<CG>(acc_full + buf);
               used ^= 1u << buf;
               if (!folds) buf ^= 1;
@@ -1012,14 +1032,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       if (o.n <= 0) continue;
       const bool sum = o.red > 0;
       const int l = o.l0 + BM * rank + 8 * piece;
-      uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+      const bool wide = kWide && o.n > kAccCols;
+      uint32_t taddr = tmem + (uint32_t)(wide ? 0 : buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
       int left = l < p.lanes ? o.n - 32 * half - row : 0;  // rows from the thread's first to the tile's end
       uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e.out) + (p.rag == MM_RAG_RED ? o.g * p.e.group_stride : 0) +
                                           (o.c0 + 32 * half + row) * ld + l);
       const bool folds = a.fold && o.red > a.seg;
       const uint32_t held = tmem + (uint32_t)((buf ^ 1) * acc_stride) + ((uint32_t)(32 * quad) << 16);
       bool ok = true;
-      for (int k = 0; ok && k < o.red; k += a.seg) {  // (one round unless the tile folds)
+      if (kWide && wide && sum) {
+        ok = mbar_wait(acc_full, used & 1, abort_flag, p.err, 5) && mbar_wait(acc_full + 1, used >> 1 & 1, abort_flag, p.err, 5);
+        __syncwarp();
+        tc_fence_after();
+        used ^= 3u;
+      }
+      for (int k = 0; !wide && ok && k < o.red; k += a.seg) {  // (one round unless the tile folds)
         ok = mbar_wait(acc_full + buf, used >> buf & 1, abort_flag, p.err, 5);
         __syncwarp();
         tc_fence_after();
@@ -1064,12 +1091,15 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {  // the MMA may overwrite this buffer
-          if (CG == 2)
+          if (kWide && wide) {
+            mbar_arrive_cluster(mapa(su32(acc_empty), 0));
+            mbar_arrive_cluster(mapa(su32(acc_empty + 1), 0));
+          } else if (CG == 2)
             mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
           else
             mbar_arrive(acc_empty + buf);
         }
-        if (!folds) buf ^= 1;
+        if (!folds && !wide) buf ^= 1;
       }
     }
   } else if (EPI != kEpiPlain && warp >= 4 && warp < kFirstLoader) {
@@ -1140,11 +1170,16 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       }
       constexpr bool kHold = kStats && CG == 2 && EPI != kEpiScoreOne;  // sums over accumulators are held in registers
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
-      const bool folds = a.fold && o.red > a.seg;
+      const bool folds = a.fold && o.red > a.seg, wide = kWide && o.n > kAccCols;
       bool ok = true;
       for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
-        uint32_t taddr = tmem + (uint32_t)(buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
-        if (sum) {
+        uint32_t taddr = tmem + (uint32_t)(wide ? 0 : buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
+        if (kWide && wide && sum) {
+          ok = mbar_wait(acc_full, used & 1, abort_flag, p.err, 5) && mbar_wait(acc_full + 1, used >> 1 & 1, abort_flag, p.err, 5);
+          __syncwarp();
+          tc_fence_after();
+          used ^= 3u;
+        } else if (sum) {
           ok = mbar_wait(acc_full + buf, used >> buf & 1, abort_flag, p.err, 5);
           __syncwarp();
           tc_fence_after();
@@ -1424,12 +1459,15 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {  // the MMA may overwrite this buffer
-            if (CG == 2)
+            if (kWide && wide) {
+              mbar_arrive_cluster(mapa(su32(acc_empty), 0));
+              mbar_arrive_cluster(mapa(su32(acc_empty + 1), 0));
+            } else if (CG == 2)
               mbar_arrive_cluster(mapa(su32(acc_empty + buf), 0));
             else
               mbar_arrive(acc_empty + (two ? 1 : buf));
           }
-          if (a.accs == 1 && !folds) buf ^= 1;
+          if (a.accs == 1 && !folds && !wide) buf ^= 1;
         }
       }
       if (!ok) break;
@@ -1673,8 +1711,13 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
     // leaves room for more stages in flight; a group beyond it takes several tiles, which share its weights in L2)
-    const int64_t typical = std::min<int64_t>(2 * (((int64_t)p.cols + p.groups - 1) / p.groups), p.cols);
+    const int64_t average = ((int64_t)p.cols + p.groups - 1) / p.groups, typical = std::min<int64_t>(2 * average, p.cols);
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
+    // Groups around 256 rows: those above would pass over their weights once more for a few rows (64 groups of 264, 4096 x
+    // 4096: 677 us, 462 in one pass). Where there are tiles for every pair of SMs, the tile holds half as much again as the average.
+    if (cg == 2 && p.red <= kSegFold && p.b.red_major && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && 3 * average > 2 * kAccCols &&
+        average <= 448 && a.lane_tiles * (int64_t)std::min(p.groups, p.cols) >= units)
+      a.bn = (int)std::min<int64_t>(2 * kAccCols, (3 * average / 2 + 63) / 64 * 64);
   } else if (!stats) {
     const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 0, cg, units);
     a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;

@@ -207,6 +207,27 @@ def test_larger_blocks(rows, n, k, groups):
         assert torch.equal(z[lo:hi], ref.to(z.dtype)) and torch.equal(h[lo:hi], (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("counts", [[300, 257, 256, 420, 255, 0, 310, 400], [288, 1, 512, 513, 33, 320, 257, 900, 100, 230], [256 + 31 * (i % 3) for i in range(12)]])
+def test_groups_around_the_width_of_an_accumulator(dtype, counts):
+    """Tiles of up to 512 columns take both accumulators, narrower ones in between take turns: blocks, and both products that
+    share the kernel. Whole numbers stay exact."""
+    rows, g, n, k = sum(counts), len(counts), 1288, 200
+    x, w = whole((rows, k), dtype, 1), whole((g, 2 * n, k), dtype, 2)
+    off = offsets(counts)
+    h, z, clean = block(x, w, off, n, "relu", dtype)
+    y, dx = full((rows, 2 * n), dtype), full((rows, 2 * n), dtype)
+    api.ds4moe_grouped_mm(x, w, off, y, rows, 2 * n, k, g, dtype, stream=stream())
+    wt = w.transpose(1, 2).contiguous()  # [k x 2n]: dx = W^T dy has 2n features
+    api.ds4moe_grouped_mm_dx(x, wt, off, dx, rows, k, 2 * n, g, dtype, stream=stream())
+    assert clean and torch.equal(z, y) and torch.equal(z, dx)
+    for e, lo, hi in groups_of(counts):
+        ref = x[lo:hi].double() @ w[e].double().T
+        assert torch.equal(z[lo:hi], ref.to(z.dtype)), e
+        assert torch.equal(h[lo:hi], (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype)), e
+    assert api.ds4moe_ops_status() == 0
+
+
 def test_block_offsets_out_of_order_or_range_reach_nothing_outside():
     n, k, rows = 40, 64, 40
     x, w, dh, z = whole((rows, k), "bf16", 1), whole((4, 2 * n, k), "bf16", 2), whole((rows, n), "bf16", 3), whole((rows, 2 * n), "bf16", 4)
