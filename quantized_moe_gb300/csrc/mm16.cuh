@@ -72,6 +72,7 @@ struct MmEpiArgs {
   float* ent;            // [tiles][tokens] sum of (v - max) exp((v - max) / T)
   const int2* want;      // [tokens][n_want] (word, place), ascending; words that there are not come last
   const uint16_t* first; // [tokens][tiles] the first entry of want in or behind a tile
+  const int* words;      // the caller's [tokens][n_want] instead of both: one, of few tokens up to kMmDirect of them
   int n_want;
   float* zwant;          // [tokens][n_want] the listed words' logits, by place
   float* logits;         // [vocab][tokens], or null
@@ -194,6 +195,7 @@ cudaError_t mm_glu_grad(const void* dh, int64_t lddh, const void* z, int64_t ldz
 
 // Sorts each row's n words for the scores' epilogue (MmEpiArgs::want, first): a word outside the vocabulary comes last.
 constexpr int kMmListed = 256, kMmTop = 64;  // most given words, and best words, of a row
+constexpr int kMmDirect = 4;  // given words of few tokens that need no sorting: 4 us of a launch
 cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile, int2* want, uint16_t* first, cudaStream_t s);
 // What the scores' partials say of each row (temperature T = 1 / inv_t).
 struct MmScores {

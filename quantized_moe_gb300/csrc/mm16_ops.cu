@@ -519,7 +519,11 @@ cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, 
     p.e.logits = a.top_k ? reinterpret_cast<float*>(ws + at.logits) : nullptr;
     p.e.chunk_max = reinterpret_cast<float*>(ws + at.chunk_max);
     b.part = p.e.part, b.ent = p.e.ent, b.zwant = p.e.zwant, b.logits = p.e.logits, b.chunk_max = p.e.chunk_max;
-    if (a.n) e = ds4::mm_sort_words(b.words, a.n, vocab, nr, a.tile, reinterpret_cast<int2*>(ws + at.want), reinterpret_cast<uint16_t*>(ws + at.first), s);
+    p.e.vocab = vocab;
+    if (a.n <= (few ? ds4::kMmDirect : 1))
+      p.e.words = b.words;
+    else
+      e = ds4::mm_sort_words(b.words, a.n, vocab, nr, a.tile, reinterpret_cast<int2*>(ws + at.want), reinterpret_cast<uint16_t*>(ws + at.first), s);
     if (e == cudaSuccess) e = ds4::mm_launch(p, s);
     if (e == cudaSuccess) e = ds4::mm_score_join(b, s);
   }

@@ -60,18 +60,66 @@ __global__ void __launch_bounds__(kThreads) sort_words_kernel(const int* words, 
   }
 }
 
-// The teacher's probabilities of one row, thread j's entry: softmax(logit / T) over the entries in the vocabulary. No
-// entries, or none that is above -inf, leave `taught` false; a NaN among them makes every p NaN.
+// The G threads (a block or a warp) that work on one row, and what they do together; every thread has the results.
+template <int G>
+struct Team;
+template <>
+struct Team<32> {
+  static constexpr int kRows = kThreads / 32;  // rows of a block
+  __device__ __forceinline__ int id() const { return threadIdx.x & 31; }
+  __device__ __forceinline__ int row() const { return threadIdx.x >> 5; }
+  __device__ __forceinline__ float max(float v) { return warp_max(v); }
+  __device__ __forceinline__ float sum(float v) { return warp_sum(v); }
+  __device__ __forceinline__ int count(int v) { return __reduce_add_sync(0xffffffffu, v); }
+  __device__ __forceinline__ bool any(bool v) { return __any_sync(0xffffffffu, v); }
+  __device__ __forceinline__ void sync() { __syncwarp(); }
+};
+template <>
+struct Team<kThreads> {
+  static constexpr int kRows = 1;
+  float (&f)[2][kWarps];
+  int (&n)[2][kWarps];
+  int turn = 0;
+  __device__ __forceinline__ int id() const { return threadIdx.x; }
+  __device__ __forceinline__ int row() const { return 0; }
+  __device__ __forceinline__ float max(float v) { return block_reduce<true>(f, turn, v); }
+  __device__ __forceinline__ float sum(float v) { return block_reduce<false>(f, turn, v); }
+  __device__ __forceinline__ int count(int v) {
+    v = __reduce_add_sync(0xffffffffu, v);
+    int(&mine)[kWarps] = n[turn & 1];
+    ++turn;
+    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int r = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) r += mine[i];
+    return r;
+  }
+  __device__ __forceinline__ bool any(bool v) { return __syncthreads_or(v); }
+  __device__ __forceinline__ void sync() { __syncthreads(); }
+};
+
+// The teacher's probabilities of one row: softmax(logit / T) over the entries in the vocabulary, item(j) = (there, logit), j <
+// n. No entries, or none that is above -inf, leave `taught` false; a NaN among them makes every p NaN.
 struct Teacher {
   float top, sum;
   bool taught;
+  __device__ __forceinline__ float p(float logit, float inv_t) const { return expf((logit - top) * inv_t) / sum; }
 };
-__device__ __forceinline__ Teacher teach(float (&s)[2][kWarps], int& turn, bool there, float logit, float inv_t) {
+template <class T, class There>
+__device__ __forceinline__ Teacher teach(T& team, const There& there, const float* logits, int n, float inv_t, int g) {
   Teacher r;
-  const bool bad = __syncthreads_or(there && logit != logit);
-  r.top = block_reduce<true>(s, turn, there ? logit : -INFINITY);
+  float m = -INFINITY;
+  bool bad = false;
+  for (int j = team.id(); j < n; j += g)
+    if (there(j)) m = fmaxf(m, logits[j]), bad |= logits[j] != logits[j];
+  bad = team.any(bad);
+  r.top = team.max(m);
   r.taught = bad || r.top > -INFINITY;
-  r.sum = block_reduce<false>(s, turn, there && r.top > -INFINITY ? expf((logit - r.top) * inv_t) : 0.f);
+  float s = 0.f;
+  for (int j = team.id(); j < n; j += g)
+    if (there(j) && r.top > -INFINITY) s += expf((logits[j] - r.top) * inv_t);
+  r.sum = team.sum(s);
   if (bad) r.sum = NAN;
   return r;
 }
@@ -92,60 +140,50 @@ __device__ __forceinline__ int index_of(unsigned long long k) { return (int)~(ui
 
 // Leaves the k largest keys of item(0..n-1) (all, if there are fewer) in `list`, in any order, and returns their number. The
 // k-th largest key is found bit by bit from the top, counting the items that reach a candidate; it ends as soon as
-// exactly k do. Called by all threads; list and count are shared.
-template <int HELD, class Item>
-__device__ __forceinline__ int best_of(int n, int k, unsigned long long* list, int* count, const Item& item) {
+// exactly k do. `list` and `count` are the team's; what item() reads may not be `list`.
+template <int HELD, int G, class Item>
+__device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned long long* list, int* count, const Item& item) {
   unsigned long long mine[HELD];  // a thread's items stay in registers up to that many
-  const bool held = n <= HELD * kThreads;
+  const bool held = n <= HELD * G;
   if (held) {
 #pragma unroll
     for (int u = 0; u < HELD; ++u) {
-      const int i = threadIdx.x + u * kThreads;
+      const int i = team.id() + u * G;
       mine[u] = i < n ? item(i) : 0;
     }
   }
-  const auto reach = [&](unsigned long long least) {  // of a thread's own
-    int c = 0;
-    if (held) {
-#pragma unroll
-      for (int u = 0; u < HELD; ++u) c += mine[u] >= least;
-    } else {
-      for (int i = threadIdx.x; i < n; i += kThreads) c += item(i) >= least;
-    }
-    return c;
-  };
-  __shared__ int sums[2][kWarps];
   unsigned long long least = 1;
   if (n > k) {
     unsigned long long found = 0;
     for (int bit = 63; bit >= 0; --bit) {
       const unsigned long long to = found | 1ull << bit;
-      const int c = __reduce_add_sync(0xffffffffu, reach(to));
-      if ((threadIdx.x & 31) == 0) sums[bit & 1][threadIdx.x >> 5] = c;
-      __syncthreads();
-      int total = 0;
+      int c = 0;
+      if (held) {
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) total += sums[bit & 1][i];
+        for (int u = 0; u < HELD; ++u) c += mine[u] >= to;
+      } else {
+        for (int i = team.id(); i < n; i += G) c += item(i) >= to;
+      }
+      const int total = team.count(c);
       if (total >= k) found = to;
       if (total == k) break;
     }
     least = found > 1 ? found : 1;
   }
-  if (threadIdx.x == 0) *count = 0;
-  __syncthreads();
+  if (team.id() == 0) *count = 0;
+  team.sync();
+  const auto keep = [&](unsigned long long q) {
+    if (q >= least) list[atomicAdd(count, 1)] = q;
+  };
   if (held) {
 #pragma unroll
-    for (int u = 0; u < HELD; ++u)
-      if (mine[u] >= least) list[atomicAdd(count, 1)] = mine[u];
+    for (int u = 0; u < HELD; ++u) keep(mine[u]);
   } else {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      const unsigned long long q = item(i);
-      if (q >= least) list[atomicAdd(count, 1)] = q;
-    }
+    for (int i = team.id(); i < n; i += G) keep(item(i));
   }
-  __syncthreads();
+  team.sync();
   const int got = *count;
-  __syncthreads();
+  team.sync();
   return got;
 }
 
@@ -153,94 +191,118 @@ __device__ __forceinline__ int best_of(int n, int k, unsigned long long* list, i
 // with r_i = exp((m_i - M) / T): lse = M / T + log S, entropy = log S - U / (T S).
 // The k best words lie in the k tiles with the largest maxima (a word of any other tile has k words ahead of it, one in
 // each of these), and there in the k chunks of 32 words with the largest: three selections of k.
-__global__ void __launch_bounds__(kThreads) score_join_kernel(const MmScores a) {
-  __shared__ float red[2][kWarps];
-  __shared__ unsigned long long list[2][kMmTop];
-  __shared__ int count;
-  begin();
-  const int64_t t = blockIdx.x;
-  const int j = threadIdx.x;
-  int turn = 0;
+template <int G>
+__device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsigned long long (*list)[kMmTop], int* count) {
+  const int64_t t = blockIdx.x * (int64_t)Team<G>::kRows + team.row();
+  if (t >= a.rows) return;  // (whole teams)
+  const int id = team.id();
   const float c = a.inv_t;
+  const float2* part = a.part + t;
+  const int64_t rows = a.rows;
   float m = -INFINITY;
-  for (int i = j; i < a.tiles; i += kThreads) m = fmaxf(m, a.part[(int64_t)i * a.rows + t].x);
-  m = block_reduce<true>(red, turn, m);
+#pragma unroll 4
+  for (int i = id; i < a.tiles; i += G) m = fmaxf(m, part[i * rows].x);
+  m = team.max(m);
   float s = 0.f, u = 0.f;
-  for (int i = j; i < a.tiles; i += kThreads) {
-    const float2 q = a.part[(int64_t)i * a.rows + t];
+#pragma unroll 4
+  for (int i = id; i < a.tiles; i += G) {
+    const float2 q = part[i * rows];
     const float d = q.x == m ? 0.f : fmaxf(q.x - m, -1e30f), r = q.x == m ? 1.f : expf(d * c);
     s += q.y * r;
-    u += (a.ent[(int64_t)i * a.rows + t] + d * q.y) * r;
+    u += (a.ent[i * rows + t] + d * q.y) * r;
   }
-  s = block_reduce<false>(red, turn, s), u = block_reduce<false>(red, turn, u);
+  s = team.sum(s), u = team.sum(u);
   const float log_s = logf(s);
-  if (j == 0) {
+  if (id == 0) {
     if (a.lse) a.lse[t] = m * c + log_s;
     if (a.entropy) {
       const float h = log_s - u * c / s;
       a.entropy[t] = h < 0.f ? 0.f : h;
     }
   }
-  const int word = j < a.n ? a.words[t * a.n + j] : -1;
-  const bool there = word >= 0 && word < a.vocab;
-  float logp = 0.f;
-  if (there) logp = (a.zwant[t * a.n + j] - m) * c - log_s;
-  if (j < a.n) a.logprob[t * a.n + j] = logp;
-  if (!there && word != -1) atomicOr(a.err, 1);
+  const int* words = a.words + t * a.n;
+  float* logprob = a.logprob + t * a.n;
+  const float* zwant = a.zwant + t * a.n;
+  const auto there = [&](int j) { return words[j] >= 0 && words[j] < a.vocab; };
+  const auto logp = [&](int j) { return there(j) ? (zwant[j] - m) * c - log_s : 0.f; };
+  for (int j = id; j < a.n; j += G) {
+    logprob[j] = logp(j);
+    if (!there(j) && words[j] != -1) atomicOr(a.err, 1);
+  }
   if (a.loss) {
-    const float logit = there ? a.teacher[t * a.n + j] : -INFINITY;
-    const Teacher of = teach(red, turn, there, logit, c);
-    const float p = there && of.taught ? expf((logit - of.top) * c) / of.sum : 0.f;
-    const float sum = block_reduce<false>(red, turn, p != 0.f ? p * ((logit - of.top) * c - logf(of.sum) - logp) : 0.f);
-    if (j == 0) a.loss[t] = sum;
+    const float* teacher = a.teacher + t * a.n;
+    const Teacher of = teach(team, there, teacher, a.n, c, G);
+    const float log_sum = logf(of.sum);
+    float sum = 0.f;
+    for (int j = id; j < a.n; j += G) {
+      const float p = there(j) && of.taught ? of.p(teacher[j], c) : 0.f;
+      if (p != 0.f) sum += p * ((teacher[j] - of.top) * c - log_sum - logp(j));
+    }
+    sum = team.sum(sum);
+    if (id == 0) a.loss[t] = sum;
   }
   if (a.top_k == 0) return;
   constexpr int kChunks = kMmStatTile / kMmStatChunk;
-  const auto tile_max = [&](int i) { return key_of(a.part[(int64_t)i * a.rows + t].x, i); };
+  const auto tile_max = [&](int i) { return key_of(part[i * rows].x, i); };
   const int chunks = (a.vocab + kMmStatChunk - 1) / kMmStatChunk;
   int n_chunks;
-  if (a.tile == kMmStatChunk) {
-    n_chunks = best_of<16>(a.tiles, a.top_k, list[1], &count, tile_max);
+  if (G == kThreads && a.tile == kMmStatChunk) {  // (few rows: a block each)
+    n_chunks = best_of<16>(team, a.tiles, a.top_k, list[1], count, tile_max);
   } else {
-    const int n_tiles = best_of<2>(a.tiles, a.top_k, list[0], &count, tile_max);
-    n_chunks = best_of<2>(n_tiles * kChunks, a.top_k, list[1], &count, [&](int i) {
+    const int n_tiles = best_of<512 / G>(team, a.tiles, a.top_k, list[0], count, tile_max);
+    n_chunks = best_of<kMmTop * kChunks / G>(team, n_tiles * kChunks, a.top_k, list[1], count, [&](int i) {
       const int chunk = index_of(list[0][i / kChunks]) * kChunks + i % kChunks;
-      return chunk < chunks ? key_of(a.chunk_max[(int64_t)chunk * a.rows + t], chunk) : 0ull;
+      return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull;
     });
   }
-  const int n_words = best_of<8>(n_chunks * kMmStatChunk, a.top_k, list[0], &count, [&](int i) {
+  const int n_words = best_of<1024 / G>(team, n_chunks * kMmStatChunk, a.top_k, list[0], count, [&](int i) {
     const int w = index_of(list[1][i / kMmStatChunk]) * kMmStatChunk + i % kMmStatChunk;
-    return w < a.vocab ? key_of(a.logits[(int64_t)w * a.rows + t], w) : 0ull;
+    return w < a.vocab ? key_of(a.logits[w * rows + t], w) : 0ull;
   });
-  if (j < a.top_k) {
+  for (int j = id; j < a.top_k; j += G) {
+    int to = j, word = -1;
+    float p = NAN;
     if (j < n_words) {
       const unsigned long long mine = list[0][j];
-      int ahead = 0;
-      for (int i = 0; i < n_words; ++i) ahead += list[0][i] > mine;
-      a.top_index[t * a.top_k + ahead] = index_of(mine);
-      a.top_logprob[t * a.top_k + ahead] = (value_of(mine) - m) * c - log_s;
-    } else {
-      a.top_index[t * a.top_k + j] = -1;
-      a.top_logprob[t * a.top_k + j] = NAN;
+      to = 0;
+      for (int i = 0; i < n_words; ++i) to += list[0][i] > mine;
+      word = index_of(mine), p = (value_of(mine) - m) * c - log_s;
     }
+    a.top_index[t * a.top_k + to] = word;
+    a.top_logprob[t * a.top_k + to] = p;
   }
+}
+
+__global__ void __launch_bounds__(kThreads) score_join_block_kernel(const MmScores a) {
+  __shared__ float f[2][kWarps];
+  __shared__ int n[2][kWarps];
+  __shared__ unsigned long long list[2][kMmTop];
+  __shared__ int count;
+  begin();
+  score_join<kThreads>(a, Team<kThreads>{f, n}, list, &count);
+}
+__global__ void __launch_bounds__(kThreads) score_join_warp_kernel(const MmScores a) {
+  __shared__ unsigned long long list[kWarps][2][kMmTop];
+  __shared__ int count[kWarps];
+  begin();
+  score_join<32>(a, Team<32>{}, list[threadIdx.x >> 5], count + (threadIdx.x >> 5));
 }
 
 __global__ void __launch_bounds__(kThreads) distill_prepare_kernel(const int* ids, const float* teacher, const float* logq,
                                                                    const float* dloss, int n, int vocab, float inv_t, float* g, float* at) {
-  __shared__ float red[2][kWarps];
+  __shared__ float f[2][kWarps];
+  __shared__ int c[2][kWarps];
   __shared__ int all[kThreads];
   __shared__ float p_of[kThreads];
   begin();
   const int64_t t = blockIdx.x;
   const int j = threadIdx.x, id = j < n ? ids[t * n + j] : -1;
   const bool there = id >= 0 && id < vocab;
-  const float logit = there ? teacher[t * n + j] : -INFINITY;
-  int turn = 0;
-  const Teacher of = teach(red, turn, there, logit, inv_t);
+  Team<kThreads> team{f, c};
+  const Teacher of = teach(team, [&](int) { return there; }, teacher + t * n, n, inv_t, kThreads);
   if (j == 0) g[t] = of.taught ? dloss[t] * inv_t : 0.f;
   all[j] = id;
-  p_of[j] = there && of.taught ? expf((logit - of.top) * inv_t) / of.sum : 0.f;
+  p_of[j] = there && of.taught ? of.p(teacher[t * n + j], inv_t) : 0.f;
   __syncthreads();
   if (!there) return;
   float p = 0.f;
@@ -268,11 +330,11 @@ cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile
   return launch(sort_words_kernel, dim3(rows), kThreads, s, words, n, vocab, tile, (vocab + tile - 1) / tile, want, first);
 }
 
-// In stream order, not as a programmatic dependent launch: blocks that wait for the product would all settle on the SMs that
-// it leaves first (2048 rows: 1340 us instead of 345, a block for eight rows).
+// A warp for each row where there are best words to find and rows enough to fill the SMs with warps: it needs no barriers (2048
+// rows of 129280 words, 20 best: 68 us, a block for each 83; but 512 rows of 32000 words, 8 best: 28 us, 22 by blocks).
 cudaError_t mm_score_join(const MmScores& a, cudaStream_t s) {
-  score_join_kernel<<<a.rows, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.top_k && a.rows >= 1024) return launch(score_join_warp_kernel, dim3((a.rows + kWarps - 1) / kWarps), kThreads, s, a);
+  return launch(score_join_block_kernel, dim3(a.rows), kThreads, s, a);
 }
 
 cudaError_t mm_distill_prepare(const int* ids, const float* teacher, const float* logq, const float* dloss, int n, int vocab,
