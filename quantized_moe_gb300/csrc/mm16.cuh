@@ -87,6 +87,7 @@ struct MmProblem {
   int rag, epi, f16;
   MmEpiArgs e;
   int* err;            // error word (bit 2 and a site bit: a pipeline wait gave up)
+  int may_spread;      // the result need not have the bits of an unsplit sum: wide tiles may share out a long reduction
 };
 
 // Loads of what earlier launches wrote are plain ones throughout, never through the non-coherent path: a launch may

@@ -209,6 +209,7 @@ cudaError_t soft_grad(const SoftGrad& q, cudaStream_t s) {
       p.e.out_f32 = !last;
       p.e.acc_in = v0 ? q.sum : nullptr, p.e.acc_ld = d;
       p.e.scale = last ? q.gs + 1 : nullptr;
+      p.may_spread = q.ids != nullptr;
       e = ds4::mm_launch(p, s);
     }
     if (e == cudaSuccess && q.dw) {

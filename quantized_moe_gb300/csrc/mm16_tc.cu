@@ -49,6 +49,7 @@ constexpr int kSegFold = 16384;           // and where it has 16 bits
 constexpr int kEpiPlain = 6;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kEpiScoreOne = 7;           // MM_EPI_SCORE where one accumulator takes a logit's whole sum
 constexpr int kAccCols = 256;             // columns of one accumulator, the widest MMA
+constexpr int kMaxSpread = 8;             // CTAs of a cluster that share out a tile's reduction and its columns
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -82,6 +83,7 @@ struct TcArgs {
   int accs;                   // accumulators of one tile that lie side by side in tensor memory (1: two take turns; 2: none is left to)
   int fold;                   // a tile with more reduction than seg is summed up in tensor memory (fold_acc), seg by seg
   int split;                  // CTAs (a cluster) that share a tile's reduction; 1: none
+  int spread;                 // they join their sums a share of the columns each (0: all in the first one); columns of a share
   int tail_from, tail_lg;     // tiles from here on are split into 2^tail_lg parts of their columns
   Divider by_lanes, by_panel, by_matrix;  // lane_tiles, lane_tiles * kPanel, lane_tiles * col_tiles
 };
@@ -767,7 +769,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const int stage_bytes = A_BYTES + a.bn / CG * BK * 2;
   uint8_t* out_stage = smem + a.stages * stage_bytes;  // [2][kOutBytes]
   float* parts = reinterpret_cast<float*>(out_stage + 2 * kOutBytes);  // [split - 1][bn][kPartLd], in the cluster's first CTA
-  uint8_t* ctrl = out_stage + 2 * kOutBytes + (a.split - 1) * a.bn * kPartLd * 4;
+  uint8_t* ctrl = out_stage + 2 * kOutBytes + (a.spread ? 0 : (a.split - 1) * a.bn * kPartLd * 4);
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
@@ -1142,6 +1144,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.live = false;
     }
     const int c_first = 32 * half, c_step = 64;
+    constexpr bool kSpread = CG == 1 && !GEN && EPI == MM_EPI_STORE;
+    const auto part_of = [&](int k, int c) -> const float* {  // the k-th other CTA's sums of columns c to c + 31
+      if (kSpread && a.spread) return reinterpret_cast<const float*>(smem) + ((k - 1) * a.spread + (c >> 5) / a.split * 32) * kPartLd;
+      return parts + ((k - 1) * a.bn + c) * kPartLd;
+    };
     constexpr bool kScore = EPI == MM_EPI_SCORE || EPI == kEpiScoreOne, kStats = EPI == MM_EPI_STATS || kScore;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
@@ -1233,7 +1240,23 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
         // (the warps that share barriers in what follows leave together)
         ok = kStats ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
-        if (CG == 1 && a.split > 1) {
+        if (kSpread && a.spread) {
+          // The CTAs of a cluster have each summed a share of the reduction, and each adds up the sums of every split-th chunk
+          // of 32 columns, its own and then the others' in order: these go where its stages were, once all are done with theirs.
+          cluster_sync();
+          for (int c = c_first; ok && c < o.n; c += c_step) {
+            const int owner = (c >> 5) % a.split;
+            if (owner == part) continue;
+            float v[32];
+            tmem_ld32(taddr + c, v);
+            const uint32_t to = mapa(su32(reinterpret_cast<float*>(smem) +
+                                          ((part < owner ? part : part - 1) * a.spread + (c >> 5) / a.split * 32) * kPartLd + 32 * quad + lane), owner);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to + j * kPartLd * 4), "f"(v[j]) : "memory");
+          }
+          cluster_sync();
+        } else if (CG == 1 && a.split > 1) {
           // the CTAs of a cluster have each summed a share of the reduction: the others hand theirs to the first one's
           // shared memory, which adds them in order
           if (part > 0 && ok) {
@@ -1335,7 +1358,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             tmem_ld_frag(taddr + c, f);
             if (CG == 1) {
               for (int k = 1; k < a.split; ++k) {
-                const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
+                const float* q = part_of(k, c) + 2 * (lane & 3) * kPartLd + 32 * quad + (lane >> 2);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -1370,6 +1393,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         } else if (by_rows) {
           for (int c = c_first; c < o.n; c += c_step) {
+            if (kSpread && a.spread && (c >> 5) % a.split != part) continue;
             Frag f;
             if (sum) {
               tmem_ld_frag(taddr + c, f);
@@ -1381,7 +1405,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             }
             if (CG == 1) {
               for (int k = 1; k < a.split; ++k) {
-                const float* q = parts + ((k - 1) * a.bn + c + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
+                const float* q = part_of(k, c) + 2 * (lane & 3) * kPartLd + 32 * quad + (lane >> 2);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -1457,6 +1481,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         } else {
           const int l = l0 + 32 * quad + lane;
           for (int c = c_first; c < o.n; c += c_step) {
+            if (kSpread && a.spread && (c >> 5) % a.split != part) continue;
             float v[32];
             if (sum) {
               tmem_ld32(taddr + c, v);
@@ -1466,7 +1491,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             }
             if (CG == 1) {
               for (int k = 1; k < a.split; ++k) {
-                const float* q = parts + ((k - 1) * a.bn + c) * kPartLd + 32 * quad + lane;
+                const float* q = part_of(k, c) + 32 * quad + lane;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += q[j * kPartLd];
               }
@@ -1532,7 +1557,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
   }
   __syncwarp();
-  if (CG == 1 && a.split > 1 && first < tiles && (warp < 4 || warp >= kFirstLoader)) cluster_sync();
+  if (CG == 1 && a.split > 1 && first < tiles && (warp < 4 || warp >= kFirstLoader)) {
+    cluster_sync();
+    if (a.spread) cluster_sync();
+  }
   if (*abort_flag) {  // after a timeout: let the copies and MMAs in flight finish (about a millisecond)
     const long long t0 = clock64();
     while (clock64() - t0 < 2000000ll) {
@@ -1550,6 +1578,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be resident at once
+int g_clusters[64][kMaxSpread + 1] = {};  // and clusters of so many CTAs
 
 // 4D map with boxes of 64 contiguous elements, 128-byte swizzle: (contiguous index, row, -, group) with box_rows rows;
 // or, for an MN-major operand whose width is a multiple of 64, (index in a block of 64, row, block, group) with
@@ -1578,7 +1607,7 @@ bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint6
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int smem_bytes(int cg, int bn, int stages, int split, const MmProblem& p) {
+int smem_bytes(int cg, int bn, int stages, int split, const MmProblem& p) {  // (split 1: also where it is spread)
   return 1024 + stages * (A_BYTES + bn / cg * BK * 2) + 2 * kOutBytes + (split - 1) * bn * kPartLd * 4 + ctrl_bytes(p.rag, p.groups);
 }
 
@@ -1587,7 +1616,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(GEN ? kThreads + 32 * kLoaders : kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.split, a.p);
+  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.spread ? 1 : a.split, a.p);
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1699,6 +1728,11 @@ cudaError_t mm_prepare() {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(&g_pairs[dev & 63], mm_tc_kernel<2, MM_EPI_STORE, false>, &cfg);
+    for (int n = 2; e == cudaSuccess && n <= kMaxSpread; ++n) {
+      cfg.gridDim = dim3(n);
+      attr[0].val.clusterDim.x = n;
+      e = cudaOccupancyMaxActiveClusters(&g_clusters[dev & 63][n], mm_tc_kernel<1, MM_EPI_STORE, false>, &cfg);
+    }
   }
   return e;
 }
@@ -1726,6 +1760,28 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
   if (p.rag != MM_RAG_RED && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
     a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
+  // Where that leaves a long reduction of several column tiles, tiles of 128 or 256 columns over clusters that also share out
+  // the joining of their sums, if they are estimated to take less time (cycles: a CTA's stage brings its operands at 64
+  // bytes a cycle, and so does the exchange at 32; dx of 512 rows, 16128 words, d 1024: 41 us, 31 so).
+  int spread_bn = 0;
+  if (p.may_spread && !gen && p.rag == MM_DENSE && p.epi == MM_EPI_STORE && !p.e.residual && !p.e.accumulate && p.cols > 64 && p.red <= kSegFold) {
+    const auto stage = [](int bn) { return 256 + 2 * bn; };
+    int64_t best = a.split > 1 ? (int64_t)(blocks + a.split - 1) / a.split * stage(64) : INT64_MAX;
+    if (a.split == 1) {
+      const int units = p.lanes > BM ? pairs : sms, cgs = p.lanes > BM ? 2 : 1;
+      best = schedule((p.lanes + BM * cgs - 1) / (BM * cgs), p.cols, p.b.red_major, 0, cgs, std::max(1, units)).cost * 2 * blocks;
+    }
+    for (int bn = 128; bn <= 256; bn *= 2) {
+      const int64_t tiles = lanes128 * ((p.cols + bn - 1) / bn);
+      int n = (int)std::min<int64_t>({sms / tiles, kMaxSpread, blocks / 6});
+      // (what a CTA receives has to fit where its stages were)
+      const int stage_bytes = A_BYTES + bn * BK * 2, held = (kSmemMax - smem_bytes(1, bn, 0, 1, p)) / stage_bytes * stage_bytes;
+      while (n > 1 && (n - 1) * ((bn / 32 + n - 1) / n * 32) * kPartLd * 4 > held) --n;
+      if (n < 2 || g_clusters[dev & 63][n] < tiles) continue;
+      const int64_t cost = (blocks + n - 1) / n * stage(bn) + bn * 16 + 3000;
+      if (cost < best) best = cost, spread_bn = bn, a.split = n;
+    }
+  }
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
   const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
@@ -1733,7 +1789,10 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const int units = cg == 2 ? pairs : sms;
   a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
-  if (a.split > 1) {
+  if (spread_bn) {
+    a.bn = spread_bn;
+    a.spread = (spread_bn / 32 + a.split - 1) / a.split * 32;
+  } else if (a.split > 1) {
     a.bn = split_bn;
   } else if (few_tokens) {
     if (gen || p.cols > kMmFewRows) return cudaErrorInvalidValue;
@@ -1753,7 +1812,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;
   }
   a.stages = 1;
-  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.split, p) <= kSmemMax) ++a.stages;
+  while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.spread ? 1 : a.split, p) <= kSmemMax) ++a.stages;
   // the rows of a copy divide what a CTA stages; large copies where the columns are not ragged (4096^3 with copies of
   // 128 rows 81.7 us, of 64 rows 83.8)
   const int staged = a.bn / cg;
