@@ -48,6 +48,12 @@ constexpr int kSegStats = 2048, kSegStore = 512;  // reduction of one accumulato
 constexpr int kSegFold = 16384;           // and where it has 16 bits
 constexpr int kEpiPlain = 6;              // MM_EPI_STORE of 16-bit rows with nothing to add: a kernel of its own (mm_launch)
 constexpr int kEpiScoreOne = 7;           // MM_EPI_SCORE where one accumulator takes a logit's whole sum
+// Pairs with more to do, in kernels of their own (their branches in the common ones cost 4096^3 3 %, its gradients 5 %):
+constexpr int kEpiPlainWide = 8, kEpiGluWide = 9;  // kEpiPlain, MM_EPI_GLU with tiles wider than an accumulator
+constexpr int kEpiPlainRag = 10;          // kEpiPlain of a ragged reduction
+__host__ __device__ constexpr bool is_plain(int epi) { return epi == kEpiPlain || epi == kEpiPlainWide || epi == kEpiPlainRag; }
+__host__ __device__ constexpr bool is_glu(int epi) { return epi == MM_EPI_GLU || epi == kEpiGluWide; }
+__host__ __device__ constexpr bool is_wide(int epi) { return epi == kEpiPlainWide || epi == kEpiGluWide; }
 constexpr int kAccCols = 256;             // columns of one accumulator, the widest MMA
 constexpr int kMaxSpread = 8;             // CTAs of a cluster that share out a tile's reduction and its columns
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
@@ -79,6 +85,7 @@ struct TcArgs {
   int glu_whole;              // one copy brings a gated block's 64 gate and 64 up rows (else 16 rows each)
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
+  int plain;                  // and nothing is to be added
   int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
   int accs;                   // accumulators of one tile that lie side by side in tensor memory (1: two take turns; 2: none is left to)
   int fold;                   // a tile with more reduction than seg is summed up in tensor memory (fold_acc), seg by seg
@@ -783,15 +790,15 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
   const int acc_stride = min(max(a.bn, 32), kAccCols);
   // Tiles wider than an accumulator: their columns run on into the other one, so that one pass over A serves up to 512.
-  constexpr bool kWide = CG == 2 && !GEN && (EPI == kEpiPlain || EPI == MM_EPI_STORE || EPI == MM_EPI_GLU);
+  constexpr bool kWide = is_wide(EPI);
   uint32_t tmem_cols = 32;
   while (tmem_cols < 2u * acc_stride) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < a.stages; ++i) {
       mbar_init(full + i, GEN ? kLoaders : 1);
-      mbar_init(empty + i, !GEN && p.rag == MM_RAG_RED ? 2 : 1);  // the MMAs' commit, and the cleaner
-      mbar_init(clean + i, 1);
+      mbar_init(empty + i, !GEN && p.rag == MM_RAG_RED && rank == 0 ? 2 : 1);  // the MMAs' commit, and the cleaner
+      mbar_init(clean + i, CG);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(acc_full + i, 1);
@@ -849,7 +856,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     bool ok = true;
-    const int a_boxes = EPI == MM_EPI_GLU ? (a.glu_whole ? 1 : BM / 16) : a_red ? 1 : 2 / a.a_blocks;
+    const int a_boxes = is_glu(EPI) ? (a.glu_whole ? 1 : BM / 16) : a_red ? 1 : 2 / a.a_blocks;
     Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -858,27 +865,34 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const int nb = mma_n<CG>(p, wide ? o.n - kAccCols : o.n) / CG;  // columns that this CTA stages (of the second part)
       const int b_boxes = kWide && wide ? kAccCols / CG / a.b_box + (nb + a.b_box - 1) / a.b_box : b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
       const int b_box_bytes = b_red ? a.b_box * 128 : a.b_blocks * 8192;
-      const uint32_t bytes = CG * (A_BYTES + b_boxes * b_box_bytes);
+      const uint32_t bytes = A_BYTES + b_boxes * b_box_bytes;
       const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
       const int ga = p.rag == MM_RAG_COLS ? o.g : 0;
       for (int k = 0; k < o.red; k += BK) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1));
         if (!ok) break;
-        const uint32_t st = su32(smem + s * stage_bytes), bar = CG == 2 ? mapa(su32(full + s), 0) : su32(full + s);
+        const bool own = EPI == kEpiPlainRag && o.red - k < BK && ((o.red - k) & 15);
+        const auto load = [&](uint32_t dst, const CUtensorMap* map, int x, int y, int z, int g, uint32_t bar) {
+          if (own)  // the copies of a pair's ragged end report to their own CTA's barrier, for its cleaner
+            tma_load<1>(dst, map, x, y, z, g, bar);
+          else
+            tma_load<CG>(dst, map, x, y, z, g, bar);
+        };
+        const uint32_t st = su32(smem + s * stage_bytes), bar = CG == 2 && !own ? mapa(su32(full + s), 0) : su32(full + s);
         const int r = o.r0 + k;
         if (of_a) {
-          if (lane == 0 && rank == 0) mbar_expect_tx(full + s, bytes);  // (copies may report before it)
+          if (lane == 0 && (rank == 0 || own)) mbar_expect_tx(full + s, CG == 2 && !own ? 2 * bytes : bytes);  // (copies may report before it)
           if (lane < a_boxes) {
-            if (EPI == MM_EPI_GLU && a.glu_whole)  // 16 rows of the gate, the same 16 of up, and so on
+            if (is_glu(EPI) && a.glu_whole)  // 16 rows of the gate, the same 16 of up, and so on
               tma_load5<CG>(st, &ta, r, 0, 0, la / 32, ga, bar);
-            else if (EPI == MM_EPI_GLU)
+            else if (is_glu(EPI))
               tma_load<CG>(st + lane * 2048, &ta, r, la / 2 + 16 * (lane >> 1) + (lane & 1 ? p.lanes : 0), 0, ga, bar);
             else if (a_red)
               tma_load<CG>(st, &ta, r, la, 0, ga, bar);
             else if (a.a_blocks > 1)
-              tma_load<CG>(st, &ta, 0, r, la / 64, ga, bar);
+              load(st, &ta, 0, r, la / 64, ga, bar);
             else
-              tma_load<CG>(st + lane * 8192, &ta, la + 64 * lane, r, 0, ga, bar);
+              load(st + lane * 8192, &ta, la + 64 * lane, r, 0, ga, bar);
           }
         } else if (lane < b_boxes) {
           const uint32_t to = st + A_BYTES + lane * b_box_bytes;
@@ -888,9 +902,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           } else if (b_red)
             tma_load<CG>(to, &tb, r, cb + lane * a.b_box, 0, 0, bar);
           else if (a.b_blocks > 1)
-            tma_load<CG>(to, &tb, 0, r, cb / 64 + lane * a.b_blocks, 0, bar);
+            load(to, &tb, 0, r, cb / 64 + lane * a.b_blocks, 0, bar);
           else
-            tma_load<CG>(to, &tb, cb + 64 * lane, r, 0, 0, bar);
+            load(to, &tb, cb + 64 * lane, r, 0, 0, bar);
         }
         if (++s == a.stages) s = 0, ph ^= 1;
       }
@@ -908,7 +922,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const int nb = mma_n<CG>(p, o.n);
       Loader la, lb;
-      if (EPI == MM_EPI_GLU)
+      if (is_glu(EPI))
         la.start_glu(pa, p.a.ld, p.lanes * p.a.ld, o.l0 / 2, p.lanes, o.r0, o.r0 + o.red, tid);
       else
         la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
@@ -1016,19 +1030,28 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     // ------------------------------------------------------------------ cleaner of ragged ends
     // Where a group ends inside a step of 16, the rows of the next group that the boxes also brought are
     // cleared in both operands before the MMA reads them (0 * NaN would not vanish). A row is 128 bytes of a box.
-    // The warp passes every stage in turn and arrives on its empty barrier too, so that the ring cannot lap it.
+    // The warp passes every stage in turn and arrives on its empty barrier too, so that the ring cannot lap it. In a pair
+    // the other CTA's full barriers see ragged ends alone, and its cleaner waits for nothing else: neither can lap the other.
+    // The MMA waits for both cleaners (64 groups around 256 rows, 4096 x 4096: 642 us on single CTAs, 566 on pairs; 256 rows
+    // each 499, 455). Their arrival releases nothing: a cleared end is in shared memory once the proxy fence is passed
+    // (with a release at cluster scope 615).
     int s = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, cleaned = 0;
     bool ok = true;
     Walk<CG> walk;
     for (int t = first; t < tiles && ok; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
       for (int k = 0; k < o.red; k += BK) {
-        ok = __all_sync(0xffffffffu, mbar_wait(full + s, ph, abort_flag, p.err, 2));
-        if (!ok) break;
         const int left = min(BK, o.red - k);
+        if (CG == 2 && rank && !(left & 15)) {
+          if (++s == a.stages) s = 0;
+          continue;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(full + s, CG == 2 && rank ? cleaned >> s & 1 : ph, abort_flag, p.err, 2));
+        if (!ok) break;
+        cleaned ^= 1u << s;
         if (left & 15) {
-          const int boxes = 2 + mma_n<CG>(p, o.n) / 64, from = left + (lane >> 3), end = (left + 15) & ~15;
+          const int boxes = 2 + mma_n<CG>(p, o.n) / CG / 64, from = left + (lane >> 3), end = (left + 15) & ~15;
           uint8_t* st = smem + s * stage_bytes + from * 128 + (lane & 7) * 16;
 #pragma unroll
           for (int box = 0; box < 6; ++box) {
@@ -1040,13 +1063,17 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) {
-          if (left & 15) mbar_arrive(clean + s);
-          mbar_arrive(empty + s);
+          if (CG == 2 && rank) {
+            mbar_arrive_cluster(mapa(su32(clean + s), 0));
+          } else {
+            if (left & 15) mbar_arrive(clean + s);
+            mbar_arrive(empty + s);
+          }
         }
         if (++s == a.stages) s = 0, ph ^= 1;
       }
     }
-  } else if (EPI == kEpiPlain && warp >= 4 && warp < kFirstLoader) {
+  } else if (is_plain(EPI) && warp >= 4 && warp < kFirstLoader) {
     // ------------------------------------------------------------------ epilogue without anything to add
     const int quad = warp & 3, half = (warp - 4) >> 2, piece = threadIdx.x & 15, row = (threadIdx.x & 127) >> 4;
     const uint32_t stage = su32(out_stage) + half * kOutBytes, from = stage + (uint32_t)(row * kRowBytes + piece * 16);
@@ -1129,7 +1156,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         if (!folds && !wide) buf ^= 1;
       }
     }
-  } else if (EPI != kEpiPlain && warp >= 4 && warp < kFirstLoader) {
+  } else if (!is_plain(EPI) && warp >= 4 && warp < kFirstLoader) {
     // ------------------------------------------------------------------ epilogue
     // Two warps per lane quadrant take the tile's 32-column chunks in turn; the four warps of a half work on the same
     // chunk.
@@ -1352,7 +1379,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             __syncwarp();
             if (lane < o.n) score_few(e, v, w0, min(32, p.lanes - w0), lane, p.cols, (p.lanes + kMmStatChunk - 1) / kMmStatChunk);
           }
-        } else if (by_rows && EPI == MM_EPI_GLU) {
+        } else if (by_rows && is_glu(EPI)) {
           for (int c = c_first; c < o.n; c += c_step) {
             Frag f;
             tmem_ld_frag(taddr + c, f);
@@ -1497,7 +1524,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
               }
             }
             const int nv = min(32, o.n - c);
-            if (EPI == MM_EPI_GLU) {
+            if (is_glu(EPI)) {
               glu_out(p, l, o.c0 + c, nv, v);
             } else if (EPI == MM_EPI_STORE) {
               epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
@@ -1635,16 +1662,18 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   switch (a.p.epi) {
     case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SOFTGRAD: return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
-    case MM_EPI_GLU: return launch<CG, MM_EPI_GLU, GEN>(ta, tb, a, grid, s);
+    case MM_EPI_GLU:
+      if (a.bn > kAccCols) return CG == 2 && !GEN ? launch<2, kEpiGluWide, false>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
+      return launch<CG, MM_EPI_GLU, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SCORE:
       if (!GEN && a.p.red <= kSegStats) return launch<CG, kEpiScoreOne, false>(ta, tb, a, grid, s);
       return launch<CG, MM_EPI_SCORE, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SCORE_FEW: return CG == 1 && !GEN ? launch<1, MM_EPI_SCORE_FEW, false>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
     default: break;
   }
-  const MmEpiArgs& e = a.p.e;
-  const bool plain = a.rows_out && a.split == 1 && !e.scale && !e.bias && !e.z && !e.residual && !e.accumulate && e.act == MM_ACT_NONE;
-  if (!GEN && plain) return launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
+  if (CG == 2 && a.bn > kAccCols) return launch<2, kEpiPlainWide, false>(ta, tb, a, grid, s);
+  if (CG == 2 && a.p.rag == MM_RAG_RED) return launch<2, kEpiPlainRag, false>(ta, tb, a, grid, s);
+  if (!GEN && a.plain && a.split == 1) return launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
   return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
 }
 
@@ -1665,8 +1694,8 @@ cudaError_t prepare_epi() {
 // The column tile with the shortest schedule: rounds over the SMs times a tile's columns (and what a tile costs
 // whatever its width, about 24 columns' time). Widths that are no multiple of 64 run at the next larger one's rate
 // (4096^3, main loop alone: 256 74 us, 192 74 us, 224 100 us). Groups of a ragged reduction (0: a dense product, the only
-// one whose last round is split) run on single CTAs, where a tile costs 200 columns more, the loads of its 128 lanes
-// (one group, 8192 rows, 4096 x 4096: 256 columns 189 us in 4 rounds, 192 194 us in 5, 128 238 us in 7).
+// one whose last round is split) have tiles that cost 200 columns more, the loads of their lanes (measured on single CTAs;
+// one group, 8192 rows, 4096 x 4096: 256 columns 189 us in 4 rounds, 192 194 us in 5, 128 238 us in 7).
 struct Schedule {
   int64_t cost;  // columns' time
   int bn, tail_lg, tail_from;
@@ -1712,6 +1741,9 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_epi<1, true>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiPlain, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlain, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiPlainWide, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiGluWide, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiPlainRag, false>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<1, MM_EPI_SCORE_FEW, false>();
@@ -1782,10 +1814,15 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
       if (cost < best) best = cost, spread_bn = bn, a.split = n;
     }
   }
+  const MmEpiArgs& ep = p.e;
+  const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
+  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
+               by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
+  a.plain = a.rows_out && p.epi == MM_EPI_STORE && !ep.scale && !ep.bias && !ep.z && !ep.residual && !ep.accumulate && ep.act == MM_ACT_NONE;
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
-  // narrow product) and the reduction is not ragged (a group's end has to be cleared in both CTAs).
+  // narrow product); of ragged reductions those whose results leave by rows.
   const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
-  const int cg = !gen && !few_tokens && p.rag != MM_RAG_RED && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
+  const int cg = !gen && !few_tokens && (p.rag != MM_RAG_RED || a.plain) && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
   const int units = cg == 2 ? pairs : sms;
   a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
@@ -1804,7 +1841,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
     // Groups around 256 rows: those above would pass over their weights once more for a few rows (64 groups of 264, 4096 x
     // 4096: 677 us, 462 in one pass). Where there are tiles for every pair of SMs, the tile holds half as much again as the average.
-    if (cg == 2 && p.red <= kSegFold && p.b.red_major && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && 3 * average > 2 * kAccCols &&
+    if (cg == 2 && p.red <= kSegFold && p.b.red_major && (a.plain || p.epi == MM_EPI_GLU) && 3 * average > 2 * kAccCols &&
         average <= 448 && a.lane_tiles * (int64_t)std::min(p.groups, p.cols) >= units)
       a.bn = (int)std::min<int64_t>(2 * kAccCols, (3 * average / 2 + 63) / 64 * 64);
   } else if (!stats) {
@@ -1824,11 +1861,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   if (a.tail_lg == 0) a.tail_from = (int)tiles;
   a.by_lanes = Divider(a.lane_tiles), a.by_panel = Divider(a.lane_tiles * kPanel), a.by_matrix = Divider(a.lane_tiles * a.col_tiles);
-  const MmEpiArgs& ep = p.e;
-  const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
   a.glu_whole = p.epi == MM_EPI_GLU && p.lanes % 16 == 0 && p.a.ld < ((int64_t)1 << 38) / p.lanes;  // (a map's strides end at 2^40 bytes)
-  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
-               by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   CUtensorMap ta = {}, tb = {};
   if (!gen) {
     const uint64_t groups = p.rag == MM_RAG_COLS ? p.groups : 1;
