@@ -51,6 +51,8 @@ constexpr int kEpiScoreOne = 7;           // MM_EPI_SCORE where one accumulator 
 // Pairs with more to do, in kernels of their own (their branches in the common ones cost 4096^3 3 %, its gradients 5 %):
 constexpr int kEpiPlainWide = 8, kEpiGluWide = 9;  // kEpiPlain, MM_EPI_GLU with tiles wider than an accumulator
 constexpr int kEpiPlainRag = 10;          // kEpiPlain of a ragged reduction
+constexpr int kEpiSpread = 11;            // MM_EPI_STORE of tiles whose sums are joined a share of the columns in each CTA
+__host__ __device__ constexpr bool is_store(int epi) { return epi == MM_EPI_STORE || epi == kEpiSpread; }
 __host__ __device__ constexpr bool is_plain(int epi) { return epi == kEpiPlain || epi == kEpiPlainWide || epi == kEpiPlainRag; }
 __host__ __device__ constexpr bool is_glu(int epi) { return epi == MM_EPI_GLU || epi == kEpiGluWide; }
 __host__ __device__ constexpr bool is_wide(int epi) { return epi == kEpiPlainWide || epi == kEpiGluWide; }
@@ -1171,9 +1173,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       rows.live = false;
     }
     const int c_first = 32 * half, c_step = 64;
-    constexpr bool kSpread = CG == 1 && !GEN && EPI == MM_EPI_STORE;
+    constexpr bool kSpread = EPI == kEpiSpread;
     const auto part_of = [&](int k, int c) -> const float* {  // the k-th other CTA's sums of columns c to c + 31
-      if (kSpread && a.spread) return reinterpret_cast<const float*>(smem) + ((k - 1) * a.spread + (c >> 5) / a.split * 32) * kPartLd;
+      if (kSpread) return reinterpret_cast<const float*>(smem) + ((k - 1) * a.spread + (c >> 5) / a.split * 32) * kPartLd;
       return parts + ((k - 1) * a.bn + c) * kPartLd;
     };
     constexpr bool kScore = EPI == MM_EPI_SCORE || EPI == kEpiScoreOne, kStats = EPI == MM_EPI_STATS || kScore;
@@ -1204,7 +1206,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         const int l = l0 + 32 * quad + (by_rows ? (lane >> 2) + 8 * r : lane);
         lse[r] = 0.f, gw[r] = 0.f, bias[r] = 0.f, lab[r] = -1;
         if (l >= p.lanes || (!by_rows && r)) continue;
-        if (EPI == MM_EPI_STORE) {
+        if (is_store(EPI)) {
           if (e.bias) bias[r] = ld16(e.bias, l, p.f16);
         } else if (EPI == MM_EPI_STATS || EPI == MM_EPI_SOFTGRAD) {
           if (EPI == MM_EPI_STATS || e.labels) lab[r] = max(*(e.labels + l), -1);
@@ -1267,7 +1269,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
         // (the warps that share barriers in what follows leave together)
         ok = kStats ? named_bar_all(1, 32 * kEpiWarps, ok) : named_bar_all(2 + half, 128, ok);
-        if (kSpread && a.spread) {
+        if (kSpread) {
           // The CTAs of a cluster have each summed a share of the reduction, and each adds up the sums of every split-th chunk
           // of 32 columns, its own and then the others' in order: these go where its stages were, once all are done with theirs.
           cluster_sync();
@@ -1420,7 +1422,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         } else if (by_rows) {
           for (int c = c_first; c < o.n; c += c_step) {
-            if (kSpread && a.spread && (c >> 5) % a.split != part) continue;
+            if (kSpread && (c >> 5) % a.split != part) continue;
             Frag f;
             if (sum) {
               tmem_ld_frag(taddr + c, f);
@@ -1508,7 +1510,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         } else {
           const int l = l0 + 32 * quad + lane;
           for (int c = c_first; c < o.n; c += c_step) {
-            if (kSpread && a.spread && (c >> 5) % a.split != part) continue;
+            if (kSpread && (c >> 5) % a.split != part) continue;
             float v[32];
             if (sum) {
               tmem_ld32(taddr + c, v);
@@ -1526,7 +1528,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             const int nv = min(32, o.n - c);
             if (is_glu(EPI)) {
               glu_out(p, l, o.c0 + c, nv, v);
-            } else if (EPI == MM_EPI_STORE) {
+            } else if (is_store(EPI)) {
               epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
               put(p, o.g, l, o.c0 + c, nv, v);
             } else {
@@ -1586,7 +1588,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   __syncwarp();
   if (CG == 1 && a.split > 1 && first < tiles && (warp < 4 || warp >= kFirstLoader)) {
     cluster_sync();
-    if (a.spread) cluster_sync();
+    if (EPI == kEpiSpread) cluster_sync();
   }
   if (*abort_flag) {  // after a timeout: let the copies and MMAs in flight finish (about a millisecond)
     const long long t0 = clock64();
@@ -1673,6 +1675,7 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   }
   if (CG == 2 && a.bn > kAccCols) return launch<2, kEpiPlainWide, false>(ta, tb, a, grid, s);
   if (CG == 2 && a.p.rag == MM_RAG_RED) return launch<2, kEpiPlainRag, false>(ta, tb, a, grid, s);
+  if (CG == 1 && a.spread) return launch<1, kEpiSpread, false>(ta, tb, a, grid, s);
   if (!GEN && a.plain && a.split == 1) return launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
   return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
 }
@@ -1744,6 +1747,7 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlainWide, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiGluWide, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlainRag, false>();
+  if (e == cudaSuccess) e = prepare_one<1, kEpiSpread, false>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<1, MM_EPI_SCORE_FEW, false>();
@@ -1763,7 +1767,7 @@ cudaError_t mm_prepare() {
     for (int n = 2; e == cudaSuccess && n <= kMaxSpread; ++n) {
       cfg.gridDim = dim3(n);
       attr[0].val.clusterDim.x = n;
-      e = cudaOccupancyMaxActiveClusters(&g_clusters[dev & 63][n], mm_tc_kernel<1, MM_EPI_STORE, false>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&g_clusters[dev & 63][n], mm_tc_kernel<1, kEpiSpread, false>, &cfg);
     }
   }
   return e;
