@@ -68,8 +68,9 @@ struct MmEpiArgs {
   float2* part;          // [column tiles][lanes] (max, sum)
   float* zlab;           // [lanes] the label's logit
   float inv_t;           // 1 / T
-  // scores, of tokens against the vocabulary in tiles of kMmStatTile words (few tokens: kMmStatChunk)
-  float* ent;            // [tiles][tokens] sum of (v - max) exp((v - max) / T)
+  // scores, of tokens against the vocabulary in tiles of so many words (mm_score_tile)
+  int tile;
+  float* ent;            // [tiles][tokens] sum of (v - max) exp((v - max) / T), or null
   const int2* want;      // [tokens][n_want] (word, place), ascending; words that there are not come last
   const uint16_t* first; // [tokens][tiles] the first entry of want in or behind a tile
   const int* words;      // the caller's [tokens][n_want] instead of both: one, of few tokens up to kMmDirect of them
@@ -175,6 +176,10 @@ constexpr int kMmFewRows = 32;    // tokens of MM_EPI_SCORE_FEW
 cudaError_t mm_prepare();
 // An estimate of a dense product's time (columns of a tile times stages of the reduction, by rounds over the SMs).
 int64_t mm_cost(int lanes, int cols, int red, bool b_red);
+// Words of a tile of scores. Up to 128 rows a call is one pass over W, for which smaller tiles leave more of it in flight (64
+// rows of 129280 words, d 4096: 168 us, in tiles of 256 178); beyond, on pairs of CTAs, tiles of 128 would load x
+// once more for every word (333 rows of 32003 words, d 1000: 42 us, 33).
+inline int mm_score_tile(int rows, bool few) { return few ? kMmStatChunk : rows <= 128 ? 128 : kMmStatTile; }
 // Launches one product. Nothing to do (no lanes or columns) is not an error.
 cudaError_t mm_launch(const MmProblem& p, cudaStream_t s);
 

@@ -460,7 +460,7 @@ void block_groups(Check& c, const void* offsets, int n_groups) {
 struct ScoreSpace {
   int64_t part, ent, want, first, zwant, chunk_max, logits, total;
   ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
-    const int tile = rows <= ds4::kMmFewRows ? ds4::kMmStatChunk : ds4::kMmStatTile;
+    const int tile = ds4::mm_score_tile(1, rows <= ds4::kMmFewRows);  // (the smallest: more rows never need less)
     const int64_t tiles = (vocab + tile - 1) / tile;
     part = 0;
     ent = up(8 * rows * tiles, 16);
@@ -498,7 +498,7 @@ cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, 
   const int vocab = call.vocab;
   const ds4::MmOperand ox = {call.x, call.ldx, 0, 1}, ow = {call.w, call.ldw, 0, 1};
   const bool few = block <= ds4::kMmFewRows && ds4::mm_aligned(ox) && ds4::mm_aligned(ow);
-  a.tile = few ? ds4::kMmStatChunk : ds4::kMmStatTile;
+  a.tile = ds4::mm_score_tile(rows, few);  // (of the call, so that blocks do not change its bits)
   a.vocab = vocab, a.tiles = (vocab + a.tile - 1) / a.tile, a.err = call.err;
   const ScoreSpace at(block, vocab, a.n, a.top_k);
   cudaError_t e = cudaSuccess;
@@ -514,7 +514,8 @@ cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, 
                            : product(x, call.ldx, true, call.w, call.ldw, true, nr, vocab, call.d, call.dtype, nullptr, 0, call.err);
     p.epi = few ? ds4::MM_EPI_SCORE_FEW : ds4::MM_EPI_SCORE;
     p.e.inv_t = a.inv_t;
-    p.e.part = reinterpret_cast<float2*>(ws + at.part), p.e.ent = reinterpret_cast<float*>(ws + at.ent);
+    p.e.tile = a.tile;
+    p.e.part = reinterpret_cast<float2*>(ws + at.part), p.e.ent = a.entropy ? reinterpret_cast<float*>(ws + at.ent) : nullptr;
     p.e.want = reinterpret_cast<int2*>(ws + at.want), p.e.n_want = a.n, p.e.zwant = reinterpret_cast<float*>(ws + at.zwant);
     p.e.first = reinterpret_cast<uint16_t*>(ws + at.first);
     p.e.logits = a.top_k ? reinterpret_cast<float*>(ws + at.logits) : nullptr;

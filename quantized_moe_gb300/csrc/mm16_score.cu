@@ -1,7 +1,7 @@
 // The small kernels around the head's scores: the lists of wanted words before the product, what its partials
 // say of each row after it (log probabilities, entropy, best words; the distillation's loss), and the places that the
 // distillation's gradient has at the listed words. One block of 256 threads for each row throughout: a row has up to 256
-// listed words, and 505 tiles of a vocabulary of 129280 (4040 where few tokens have tiles of 32 words).
+// listed words, and 505 tiles of a vocabulary of 129280 (1010 or 4040 smaller ones where there are few rows).
 #include "mm16_small.cuh"
 
 namespace ds4 {
@@ -209,7 +209,7 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
     const float2 q = part[i * rows];
     const float d = q.x == m ? 0.f : fmaxf(q.x - m, -1e30f), r = q.x == m ? 1.f : expf(d * c);
     s += q.y * r;
-    u += (a.ent[i * rows + t] + d * q.y) * r;
+    if (a.entropy) u += (a.ent[i * rows + t] + d * q.y) * r;
   }
   s = team.sum(s), u = team.sum(u);
   const float log_s = logf(s);
@@ -242,16 +242,16 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
     if (id == 0) a.loss[t] = sum;
   }
   if (a.top_k == 0) return;
-  constexpr int kChunks = kMmStatTile / kMmStatChunk;
+  const int per_tile = a.tile / kMmStatChunk;
   const auto tile_max = [&](int i) { return key_of(part[i * rows].x, i); };
   const int chunks = (a.vocab + kMmStatChunk - 1) / kMmStatChunk;
   int n_chunks;
   if (G == kThreads && a.tile == kMmStatChunk) {  // (few rows: a block each)
     n_chunks = best_of<16>(team, a.tiles, a.top_k, list[1], count, tile_max);
   } else {
-    const int n_tiles = best_of<512 / G>(team, a.tiles, a.top_k, list[0], count, tile_max);
-    n_chunks = best_of<kMmTop * kChunks / G>(team, n_tiles * kChunks, a.top_k, list[1], count, [&](int i) {
-      const int chunk = index_of(list[0][i / kChunks]) * kChunks + i % kChunks;
+    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.tiles, a.top_k, list[0], count, tile_max);
+    n_chunks = best_of<kMmTop * 8 / G>(team, n_tiles * per_tile, a.top_k, list[1], count, [&](int i) {
+      const int chunk = index_of(list[0][i / per_tile]) * per_tile + i % per_tile;
       return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull;
     });
   }

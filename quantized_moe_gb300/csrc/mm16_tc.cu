@@ -690,6 +690,7 @@ __device__ __forceinline__ float exp2_fast(float v) {
 }
 // Words from nv on are made -inf: they add nothing, and no word's arithmetic hangs on a branch (written with a condition for
 // each word the chunk ran one word after the other, 4.5 thousand cycles where this takes one). Returns the chunk's largest.
+template <bool ENT>
 __device__ __forceinline__ float epi_score(float (&v)[32], int nv, float c, float& m, float& s, float& u) {
   if (nv < 32) {
 #pragma unroll
@@ -713,10 +714,10 @@ __device__ __forceinline__ float epi_score(float (&v)[32], int nv, float c, floa
   for (int j = 0; j < 32; ++j) {
     const float dj = v[j] - top, e = exp2_fast(dj * c);
     t[j & 3] += e;
-    w[j & 3] += fmaxf(dj, -1e30f) * e;  // (words of probability zero add nothing)
+    if (ENT) w[j & 3] += fmaxf(dj, -1e30f) * e;  // (words of probability zero add nothing)
   }
   s = (t[0] + t[1]) + (t[2] + t[3]);
-  u = (w[0] + w[1]) + (w[2] + w[3]);
+  if (ENT) u = (w[0] + w[1]) + (w[2] + w[3]);
   return chunk;
 }
 
@@ -760,9 +761,9 @@ __device__ __forceinline__ void score_few(const MmEpiArgs& e, float (&v)[32], in
   Wanted wanted;
   if (e.n_want > 0) wanted.start(e, t, (int)tile, tiles, w0);
   float m = -INFINITY, s = 0.f, u = 0.f;
-  epi_score(v, nv, e.inv_t * 1.4426950408889634f, m, s, u);
+  epi_score<true>(v, nv, e.inv_t * 1.4426950408889634f, m, s, u);
   e.part[tile * tokens + t] = make_float2(m, s);
-  e.ent[tile * tokens + t] = u;
+  if (e.ent) e.ent[tile * tokens + t] = u;
   if (e.logits) store_col(e.logits + (int64_t)w0 * tokens + t, tokens, nv, v);
   wanted.take(e, v, w0, nv, t);
 }
@@ -1228,7 +1229,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           want_left = 1, want_next = *(e.words + token);
           if (want_next < o.c0 || want_next >= e.vocab) want_next = INT32_MAX;
         } else {
-          const int at = *(e.first + token * a.col_tiles + o.c0 / kMmStatTile);
+          const int at = *(e.first + token * a.col_tiles + o.c0 / a.bn);
           want = e.want + token * e.n_want + at;
           want_left = e.n_want - at;
           if (want_left > 0) want_next = want->x;
@@ -1339,7 +1340,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             }
             const int nv = min(32, o.n - c), at = lab[0] - (o.c0 + c);
             if (kScore) {
-              const float most = epi_score(y, nv, e.inv_t * 1.4426950408889634f, m, total, spread);
+              const float scale = e.inv_t * 1.4426950408889634f;
+              const float most = e.ent ? epi_score<true>(y, nv, scale, m, total, spread) : epi_score<false>(y, nv, scale, m, total, spread);
               if (e.logits && l0 + 32 * quad + lane < p.lanes) {
                 store_col(e.logits + (int64_t)(o.c0 + c) * p.lanes + l0 + 32 * quad + lane, p.lanes, nv, y);
                 e.chunk_max[(int64_t)((o.c0 + c) / kMmStatChunk) * p.lanes + l0 + 32 * quad + lane] = most;
@@ -1567,7 +1569,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           const float r0 = exp2_fast(d0 * c), r1 = exp2_fast(d1 * c);
           const int64_t at = (int64_t)(o.c0 / a.bn) * p.lanes + l;
           e.part[at] = make_float2(top, total * r0 + q.y * r1);
-          e.ent[at] = (spread + d0 * total) * r0 + (q.z + d1 * q.y) * r1;
+          if (e.ent) e.ent[at] = (spread + d0 * total) * r0 + (q.z + d1 * q.y) * r1;
         }
       }
       if (EPI == MM_EPI_STATS) {  // the two halves' partials are joined
@@ -1848,6 +1850,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     if (cg == 2 && p.red <= kSegFold && p.b.red_major && (a.plain || p.epi == MM_EPI_GLU) && 3 * average > 2 * kAccCols &&
         average <= 448 && a.lane_tiles * (int64_t)std::min(p.groups, p.cols) >= units)
       a.bn = (int)std::min<int64_t>(2 * kAccCols, (3 * average / 2 + 63) / 64 * 64);
+  } else if (p.epi == MM_EPI_SCORE) {
+    a.bn = p.e.tile;
   } else if (!stats) {
     const Schedule w = schedule(a.lane_tiles, p.cols, p.b.red_major, p.rag == MM_RAG_RED ? p.groups : 0, cg, units);
     a.bn = w.bn, a.tail_lg = w.tail_lg, a.tail_from = w.tail_from;
