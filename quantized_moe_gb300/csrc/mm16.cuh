@@ -77,7 +77,7 @@ struct MmEpiArgs {
   int n_want;
   float* zwant;          // [tokens][n_want] the listed words' logits, by place
   float* logits;         // [vocab][tokens], or null
-  float* chunk_max;      // [vocab / kMmStatChunk][tokens]; with logits, where tiles are larger
+  float* chunk_max;      // [vocab / kMmStatChunk][tokens]; with logits
 };
 
 struct MmProblem {
@@ -171,6 +171,7 @@ inline bool mm_aligned(const MmOperand& o) {
 constexpr int kMmStatTile = 256;
 constexpr int kMmStatChunk = 32;  // words of one chunk's maximum
 constexpr int kMmFewRows = 32;    // tokens of MM_EPI_SCORE_FEW
+constexpr int kMmFewWidth = 16384;  // and its longest sums: eight accumulators of 2048
 
 // Sets kernel attributes on the current device (once per device).
 cudaError_t mm_prepare();
@@ -180,6 +181,9 @@ int64_t mm_cost(int lanes, int cols, int red, bool b_red);
 // rows of 129280 words, d 4096: 168 us, in tiles of 256 178); beyond, on pairs of CTAs, tiles of 128 would load x
 // once more for every word (333 rows of 32003 words, d 1000: 42 us, 33).
 inline int mm_score_tile(int rows, bool few) { return few ? kMmStatChunk : rows <= 128 ? 128 : kMmStatTile; }
+// Softmax partials of each of few tokens: one for every epilogue warp.
+int mm_few_parts(int vocab);
+constexpr int kMmFewParts = 1024;  // at most
 // Launches one product. Nothing to do (no lanes or columns) is not an error.
 cudaError_t mm_launch(const MmProblem& p, cudaStream_t s);
 
@@ -207,7 +211,8 @@ cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile
 struct MmScores {
   const float2* part;
   const float* ent;
-  int tile, tiles, rows, vocab;  // words of a tile
+  int parts, rows, vocab;
+  int tile;             // words of a partial; kMmStatChunk: partials are not of tiles (few rows)
   float inv_t;
   const float* zwant;   // [rows][n] logits of the listed words
   const int* words;     // [rows][n]

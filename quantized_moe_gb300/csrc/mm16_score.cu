@@ -1,7 +1,7 @@
 // The small kernels around the head's scores: the lists of wanted words before the product, what its partials
 // say of each row after it (log probabilities, entropy, best words; the distillation's loss), and the places that the
 // distillation's gradient has at the listed words. One block of 256 threads for each row throughout: a row has up to 256
-// listed words, and 505 tiles of a vocabulary of 129280 (1010 or 4040 smaller ones where there are few rows).
+// listed words, and 505 to 1010 partials of a vocabulary of 129280.
 #include "mm16_small.cuh"
 
 namespace ds4 {
@@ -187,7 +187,7 @@ __device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned lon
   return got;
 }
 
-// Joins the tiles' (max, sum, spread) as M = max m_i, S = sum s_i r_i, U = sum (u_i + (m_i - M) s_i) r_i
+// Joins the partials (max, sum, spread) as M = max m_i, S = sum s_i r_i, U = sum (u_i + (m_i - M) s_i) r_i
 // with r_i = exp((m_i - M) / T): lse = M / T + log S, entropy = log S - U / (T S).
 // The k best words lie in the k tiles with the largest maxima (a word of any other tile has k words ahead of it, one in
 // each of these), and there in the k chunks of 32 words with the largest: three selections of k.
@@ -201,11 +201,11 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
   const int64_t rows = a.rows;
   float m = -INFINITY;
 #pragma unroll 4
-  for (int i = id; i < a.tiles; i += G) m = fmaxf(m, part[i * rows].x);
+  for (int i = id; i < a.parts; i += G) m = fmaxf(m, part[i * rows].x);
   m = team.max(m);
   float s = 0.f, u = 0.f;
 #pragma unroll 4
-  for (int i = id; i < a.tiles; i += G) {
+  for (int i = id; i < a.parts; i += G) {
     const float2 q = part[i * rows];
     const float d = q.x == m ? 0.f : fmaxf(q.x - m, -1e30f), r = q.x == m ? 1.f : expf(d * c);
     s += q.y * r;
@@ -243,16 +243,15 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
   }
   if (a.top_k == 0) return;
   const int per_tile = a.tile / kMmStatChunk;
-  const auto tile_max = [&](int i) { return key_of(part[i * rows].x, i); };
   const int chunks = (a.vocab + kMmStatChunk - 1) / kMmStatChunk;
+  const auto chunk_max = [&](int chunk) { return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull; };
   int n_chunks;
   if (G == kThreads && a.tile == kMmStatChunk) {  // (few rows: a block each)
-    n_chunks = best_of<16>(team, a.tiles, a.top_k, list[1], count, tile_max);
+    n_chunks = best_of<16>(team, chunks, a.top_k, list[1], count, chunk_max);
   } else {
-    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.tiles, a.top_k, list[0], count, tile_max);
+    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.parts, a.top_k, list[0], count, [&](int i) { return key_of(part[i * rows].x, i); });
     n_chunks = best_of<kMmTop * 8 / G>(team, n_tiles * per_tile, a.top_k, list[1], count, [&](int i) {
-      const int chunk = index_of(list[0][i / per_tile]) * per_tile + i % per_tile;
-      return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull;
+      return chunk_max(index_of(list[0][i / per_tile]) * per_tile + i % per_tile);
     });
   }
   const int n_words = best_of<1024 / G>(team, n_chunks * kMmStatChunk, a.top_k, list[0], count, [&](int i) {

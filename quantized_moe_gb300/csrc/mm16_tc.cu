@@ -756,15 +756,16 @@ struct Wanted {
 };
 
 // One chunk of few tokens' scores: thread's token t of `tokens`, 32 words from w0 (nv exist).
-__device__ __forceinline__ void score_few(const MmEpiArgs& e, float (&v)[32], int w0, int nv, int t, int tokens, int tiles) {
+__device__ __forceinline__ void score_few(const MmEpiArgs& e, float (&v)[32], int w0, int nv, int t, int tokens, int tiles, float& m,
+                                          float& s, float& u) {
   const int64_t tile = w0 / kMmStatChunk;
   Wanted wanted;
   if (e.n_want > 0) wanted.start(e, t, (int)tile, tiles, w0);
-  float m = -INFINITY, s = 0.f, u = 0.f;
-  epi_score<true>(v, nv, e.inv_t * 1.4426950408889634f, m, s, u);
-  e.part[tile * tokens + t] = make_float2(m, s);
-  if (e.ent) e.ent[tile * tokens + t] = u;
-  if (e.logits) store_col(e.logits + (int64_t)w0 * tokens + t, tokens, nv, v);
+  const float most = epi_score<true>(v, nv, e.inv_t * 1.4426950408889634f, m, s, u);
+  if (e.logits) {
+    store_col(e.logits + (int64_t)w0 * tokens + t, tokens, nv, v);
+    e.chunk_max[tile * tokens + t] = most;
+  }
   wanted.take(e, v, w0, nv, t);
 }
 
@@ -791,7 +792,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
-  const int acc_stride = min(max(a.bn, 32), kAccCols);
+  // Scores of few tokens: a tile's accumulators, one for every seg of the reduction, lie side by side, and the next tile's
+  // in the other half of tensor memory, so that the stream of W never waits for an epilogue (178 us, @FEW@ so).
+  constexpr bool kBeside = EPI == MM_EPI_SCORE_FEW;
+  const int acc_stride = kBeside ? kAccCols : min(max(a.bn, 32), kAccCols);
   // Tiles wider than an accumulator: their columns run on into the other one, so that one pass over A serves up to 512.
   constexpr bool kWide = is_wide(EPI);
   uint32_t tmem_cols = 32;
@@ -977,7 +981,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         uint32_t d = 0;
         int in_seg = 0;  // reduction already in this accumulator
         for (int k = 0; k < o.red; k += BK) {
-          if (in_seg == 0) {
+          if (kBeside && in_seg == 0 && k > 0) {
+            d += kMmFewRows;
+          } else if (in_seg == 0) {
             const int b = wide ? 0 : a.accs == 1 || k == 0 ? buf : 1;  // (1: the second accumulator of the same tile)
             if (!mbar_wait(acc_empty + b, (used >> b & 1) ^ 1, abort_flag, p.err, 6) ||
                 (kWide && wide && !mbar_wait(acc_empty + 1, (used >> 1 & 1) ^ 1, abort_flag, p.err, 6))) {
@@ -1012,7 +1018,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (++s == a.stages) s = 0, ph ^= 1;
           in_seg += BK;
           if (in_seg == a.seg || k + BK >= o.red) {
-            if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
+            if (kBeside && k + BK < o.red) {
+            } else if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
               commit<CG>(acc_full);
               commit<CG>(acc_full + 1);
               used ^= 3u;
@@ -1182,6 +1189,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     constexpr bool kScore = EPI == MM_EPI_SCORE || EPI == kEpiScoreOne, kStats = EPI == MM_EPI_STATS || kScore;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
+    float few_m = -INFINITY, few_s = 0.f, few_u = 0.f;  // few tokens: of all the warp's words
     Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -1239,7 +1247,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       const bool folds = a.fold && o.red > a.seg, wide = kWide && o.n > kAccCols;
       bool ok = true;
-      for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
+      for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 && !kBeside ? a.seg : o.red) {  // accumulators of the tile
         uint32_t taddr = tmem + (uint32_t)(wide ? 0 : buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
         if (kWide && wide && sum) {
           ok = mbar_wait(acc_full, used & 1, abort_flag, p.err, 5) && mbar_wait(acc_full + 1, used >> 1 & 1, abort_flag, p.err, 5);
@@ -1375,13 +1383,19 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             float v[32];
             float* x = reinterpret_cast<float*>(out_stage) + quad * (32 * 33);
             tmem_ld32(taddr, v);
+            for (int i = 1; i * a.seg < o.red; ++i) {
+              float more[32];
+              tmem_ld32(taddr + i * kMmFewRows, more);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] += more[j];
+            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j * 33 + lane] = v[j];
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = x[lane * 33 + j];
             __syncwarp();
-            if (lane < o.n) score_few(e, v, w0, min(32, p.lanes - w0), lane, p.cols, (p.lanes + kMmStatChunk - 1) / kMmStatChunk);
+            if (lane < o.n) score_few(e, v, w0, min(32, p.lanes - w0), lane, p.cols, (p.lanes + kMmStatChunk - 1) / kMmStatChunk, few_m, few_s, few_u);
           }
         } else if (by_rows && is_glu(EPI)) {
           for (int c = c_first; c < o.n; c += c_step) {
@@ -1586,6 +1600,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         }
       }
     }
+    if (EPI == MM_EPI_SCORE_FEW && half == 0 && lane < p.cols) {
+      const int64_t at = (int64_t)(blockIdx.x * 4 + quad) * p.cols + lane;
+      e.part[at] = make_float2(few_m, few_s);
+      if (e.ent) e.ent[at] = few_u;
+    }
   }
   __syncwarp();
   if (CG == 1 && a.split > 1 && first < tiles && (warp < 4 || warp >= kFirstLoader)) {
@@ -1722,6 +1741,12 @@ Schedule schedule(int64_t lane_tiles, int cols, bool b_red, int groups, int cg, 
 
 }  // namespace
 
+int mm_few_parts(int vocab) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return 4 * std::min({g_sms[dev & 63], kMmFewParts / 4, (vocab + BM - 1) / BM});
+}
+
 int64_t mm_cost(int lanes, int cols, int red, bool b_red) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
@@ -1829,7 +1854,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   // narrow product); of ragged reductions those whose results leave by rows.
   const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
   const int cg = !gen && !few_tokens && (p.rag != MM_RAG_RED || a.plain) && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
-  const int units = cg == 2 ? pairs : sms;
+  const int units = cg == 2 ? pairs : few_tokens ? std::min(sms, kMmFewParts / 4) : sms;
   a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;
   if (spread_bn) {
@@ -1838,7 +1863,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   } else if (a.split > 1) {
     a.bn = split_bn;
   } else if (few_tokens) {
-    if (gen || p.cols > kMmFewRows) return cudaErrorInvalidValue;
+    if (gen || p.cols > kMmFewRows || p.red > kMmFewWidth) return cudaErrorInvalidValue;
     a.bn = kMmFewRows;
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
@@ -1891,8 +1916,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   //    back. A longer d is added up as for 16 bits.
   a.seg = kSegFold;
   a.accs = 1;
-  if (few_tokens)  // (the sums of 32 tokens are added up in no time)
-    a.seg = kSegStats, a.fold = 1;
+  if (few_tokens)
+    a.seg = kSegStats;
   else if (stats && (cg == 2 || p.red > 2 * kSegStats))
     a.seg = kSegStats, a.fold = cg == 1;
   else if (stats && p.red > kSegStats)
