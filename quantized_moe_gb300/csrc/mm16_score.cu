@@ -8,6 +8,8 @@ namespace ds4 {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCandidates = 128;
+static_assert(kCandidates >= kMmTop, "the k best fit among the candidates");
 static_assert(kMmListed <= kThreads, "a thread for each listed word");
 
 // A block's sum or maximum, in a fixed order; every thread has the result. Two scratch rows take turns: a third call comes
@@ -71,6 +73,7 @@ struct Team<32> {
   __device__ __forceinline__ float max(float v) { return warp_max(v); }
   __device__ __forceinline__ float sum(float v) { return warp_sum(v); }
   __device__ __forceinline__ int count(int v) { return __reduce_add_sync(0xffffffffu, v); }
+  __device__ __forceinline__ int votes(bool v) { return __popc(__ballot_sync(0xffffffffu, v)); }
   __device__ __forceinline__ bool any(bool v) { return __any_sync(0xffffffffu, v); }
   __device__ __forceinline__ void sync() { __syncwarp(); }
 };
@@ -95,6 +98,7 @@ struct Team<kThreads> {
     for (int i = 0; i < kWarps; ++i) r += mine[i];
     return r;
   }
+  __device__ __forceinline__ int votes(bool v) { return __syncthreads_count(v); }
   __device__ __forceinline__ bool any(bool v) { return __syncthreads_or(v); }
   __device__ __forceinline__ void sync() { __syncthreads(); }
 };
@@ -138,80 +142,109 @@ __device__ __forceinline__ float value_of(unsigned long long k) {
 }
 __device__ __forceinline__ int index_of(unsigned long long k) { return (int)~(uint32_t)k; }
 
-// Leaves the k largest keys of item(0..n-1) (all, if there are fewer) in `list`, in any order, and returns their number. The
-// k-th largest key is found bit by bit from the top, counting the items that reach a candidate; it ends as soon as
-// exactly k do. `list` and `count` are the team's; what item() reads may not be `list`.
+// Leaves the k largest keys of item(0..n-1) (all, if there are fewer) in `list` in their order, and returns their number.
+// The k-th largest of the threads' largest values, found bit by bit from the top, is reached by at least k items and as a
+// rule by few more: those are ranked by counting. Where more than kCandidates reach it (equal values, or k above the number
+// of threads) the k-th largest key itself is found, bit by bit over all items (for all rows and sizes at first: 2048 rows,
+// 20 best, 68 us instead of 64). `list`, `cand` and `count` are the team's; what item() reads may not be `list`.
 template <int HELD, int G, class Item>
-__device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned long long* list, int* count, const Item& item) {
+__device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned long long* list, unsigned long long* cand, int* count,
+                                       const Item& item) {
   unsigned long long mine[HELD];  // a thread's items stay in registers up to that many
   const bool held = n <= HELD * G;
+  unsigned long long most = 0;
   if (held) {
 #pragma unroll
     for (int u = 0; u < HELD; ++u) {
       const int i = team.id() + u * G;
       mine[u] = i < n ? item(i) : 0;
+      most = mine[u] > most ? mine[u] : most;
+    }
+  } else {
+    for (int i = team.id(); i < n; i += G) {
+      const unsigned long long q = item(i);
+      most = q > most ? q : most;
     }
   }
-  unsigned long long least = 1;
-  if (n > k) {
+  const auto each = [&](const auto& fn) {
+    if (held) {
+#pragma unroll
+      for (int u = 0; u < HELD; ++u) fn(mine[u]);
+    } else {
+      for (int i = team.id(); i < n; i += G) fn(item(i));
+    }
+  };
+  const uint32_t top = (uint32_t)(most >> 32);
+  uint32_t reached = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t to = reached | 1u << bit;
+    const int c = team.votes(top >= to);
+    if (c >= k) reached = to;
+    if (c == k) break;
+  }
+  unsigned long long least = reached ? (unsigned long long)reached << 32 : 1;
+  int some = 0;
+  each([&](unsigned long long q) { some += q >= least; });
+  some = team.count(some);
+  if (some > kCandidates) {
     unsigned long long found = 0;
     for (int bit = 63; bit >= 0; --bit) {
       const unsigned long long to = found | 1ull << bit;
       int c = 0;
-      if (held) {
-#pragma unroll
-        for (int u = 0; u < HELD; ++u) c += mine[u] >= to;
-      } else {
-        for (int i = team.id(); i < n; i += G) c += item(i) >= to;
-      }
-      const int total = team.count(c);
-      if (total >= k) found = to;
-      if (total == k) break;
+      each([&](unsigned long long q) { c += q >= to; });
+      c = team.count(c);
+      if (c >= k) found = to;
+      if (c == k) break;
     }
-    least = found > 1 ? found : 1;
+    least = found;  // (there are k at least: kCandidates are more)
   }
   if (team.id() == 0) *count = 0;
   team.sync();
-  const auto keep = [&](unsigned long long q) {
-    if (q >= least) list[atomicAdd(count, 1)] = q;
-  };
-  if (held) {
-#pragma unroll
-    for (int u = 0; u < HELD; ++u) keep(mine[u]);
-  } else {
-    for (int i = team.id(); i < n; i += G) keep(item(i));
-  }
+  each([&](unsigned long long q) {
+    if (q >= least) cand[atomicAdd(count, 1)] = q;
+  });
   team.sync();
   const int got = *count;
+  for (int i = team.id(); i < got; i += G) {
+    const unsigned long long q = cand[i];
+    int ahead = 0;
+    for (int j = 0; j < got; ++j) ahead += cand[j] > q;
+    if (ahead < k) list[ahead] = q;
+  }
   team.sync();
-  return got;
+  return min(got, k);
 }
 
-// Joins the partials (max, sum, spread) as M = max m_i, S = sum s_i r_i, U = sum (u_i + (m_i - M) s_i) r_i
+// Joins the partials (max, sum, spread), whole sets of words each: M = max m_i, S = sum s_i r_i, U = sum (u_i + (m_i - M) s_i) r_i
 // with r_i = exp((m_i - M) / T): lse = M / T + log S, entropy = log S - U / (T S).
 // The k best words lie in the k tiles with the largest maxima (a word of any other tile has k words ahead of it, one in
 // each of these), and there in the k chunks of 32 words with the largest: three selections of k.
 template <int G>
-__device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsigned long long (*list)[kMmTop], int* count) {
+__device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsigned long long (*list)[kMmTop], unsigned long long* cand, int* count) {
   const int64_t t = blockIdx.x * (int64_t)Team<G>::kRows + team.row();
   if (t >= a.rows) return;  // (whole teams)
   const int id = team.id();
   const float c = a.inv_t;
   const float2* part = a.part + t;
   const int64_t rows = a.rows;
-  float m = -INFINITY;
-#pragma unroll 4
-  for (int i = id; i < a.parts; i += G) m = fmaxf(m, part[i * rows].x);
-  m = team.max(m);
-  float s = 0.f, u = 0.f;
+  // (a thread joins its partials one after the other, then the team's threads theirs)
+  float m = -INFINITY, s = 0.f, u = 0.f;
+  const auto shift = [&](float from, float to) { return from == to ? 0.f : fmaxf(from - to, -1e30f); };
 #pragma unroll 4
   for (int i = id; i < a.parts; i += G) {
     const float2 q = part[i * rows];
-    const float d = q.x == m ? 0.f : fmaxf(q.x - m, -1e30f), r = q.x == m ? 1.f : expf(d * c);
-    s += q.y * r;
-    if (a.entropy) u += (a.ent[i * rows + t] + d * q.y) * r;
+    const float e = a.entropy ? a.ent[i * rows + t] : 0.f;
+    const float top = fmaxf(m, q.x), d0 = shift(m, top), d1 = shift(q.x, top), r0 = expf(d0 * c), r1 = expf(d1 * c);
+    u = (u + d0 * s) * r0 + (e + d1 * q.y) * r1;
+    s = s * r0 + q.y * r1;
+    m = top;
   }
-  s = team.sum(s), u = team.sum(u);
+  {
+    const float top = team.max(m), d = shift(m, top), r = expf(d * c);
+    u = team.sum((u + d * s) * r);
+    s = team.sum(s * r);
+    m = top;
+  }
   const float log_s = logf(s);
   if (id == 0) {
     if (a.lse) a.lse[t] = m * c + log_s;
@@ -247,44 +280,37 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
   const auto chunk_max = [&](int chunk) { return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull; };
   int n_chunks;
   if (G == kThreads && a.tile == kMmStatChunk) {  // (few rows: a block each)
-    n_chunks = best_of<16>(team, chunks, a.top_k, list[1], count, chunk_max);
+    n_chunks = best_of<16>(team, chunks, a.top_k, list[1], cand, count, chunk_max);
   } else {
-    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.parts, a.top_k, list[0], count, [&](int i) { return key_of(part[i * rows].x, i); });
-    n_chunks = best_of<kMmTop * 8 / G>(team, n_tiles * per_tile, a.top_k, list[1], count, [&](int i) {
+    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.parts, a.top_k, list[0], cand, count, [&](int i) { return key_of(part[i * rows].x, i); });
+    n_chunks = best_of<kMmTop * 8 / G>(team, n_tiles * per_tile, a.top_k, list[1], cand, count, [&](int i) {
       return chunk_max(index_of(list[0][i / per_tile]) * per_tile + i % per_tile);
     });
   }
-  const int n_words = best_of<1024 / G>(team, n_chunks * kMmStatChunk, a.top_k, list[0], count, [&](int i) {
+  const int n_words = best_of<1024 / G>(team, n_chunks * kMmStatChunk, a.top_k, list[0], cand, count, [&](int i) {
     const int w = index_of(list[1][i / kMmStatChunk]) * kMmStatChunk + i % kMmStatChunk;
     return w < a.vocab ? key_of(a.logits[w * rows + t], w) : 0ull;
   });
   for (int j = id; j < a.top_k; j += G) {
-    int to = j, word = -1;
-    float p = NAN;
-    if (j < n_words) {
-      const unsigned long long mine = list[0][j];
-      to = 0;
-      for (int i = 0; i < n_words; ++i) to += list[0][i] > mine;
-      word = index_of(mine), p = (value_of(mine) - m) * c - log_s;
-    }
-    a.top_index[t * a.top_k + to] = word;
-    a.top_logprob[t * a.top_k + to] = p;
+    const unsigned long long mine = j < n_words ? list[0][j] : 0;
+    a.top_index[t * a.top_k + j] = mine ? index_of(mine) : -1;
+    a.top_logprob[t * a.top_k + j] = mine ? (value_of(mine) - m) * c - log_s : NAN;
   }
 }
 
 __global__ void __launch_bounds__(kThreads) score_join_block_kernel(const MmScores a) {
   __shared__ float f[2][kWarps];
   __shared__ int n[2][kWarps];
-  __shared__ unsigned long long list[2][kMmTop];
+  __shared__ unsigned long long list[2][kMmTop], cand[kCandidates];
   __shared__ int count;
   begin();
-  score_join<kThreads>(a, Team<kThreads>{f, n}, list, &count);
+  score_join<kThreads>(a, Team<kThreads>{f, n}, list, cand, &count);
 }
 __global__ void __launch_bounds__(kThreads) score_join_warp_kernel(const MmScores a) {
-  __shared__ unsigned long long list[kWarps][2][kMmTop];
+  __shared__ unsigned long long list[kWarps][2][kMmTop], cand[kWarps][kCandidates];
   __shared__ int count[kWarps];
   begin();
-  score_join<32>(a, Team<32>{}, list[threadIdx.x >> 5], count + (threadIdx.x >> 5));
+  score_join<32>(a, Team<32>{}, list[threadIdx.x >> 5], cand[threadIdx.x >> 5], count + (threadIdx.x >> 5));
 }
 
 __global__ void __launch_bounds__(kThreads) distill_prepare_kernel(const int* ids, const float* teacher, const float* logq,
@@ -305,9 +331,10 @@ __global__ void __launch_bounds__(kThreads) distill_prepare_kernel(const int* id
   __syncthreads();
   if (!there) return;
   float p = 0.f;
-  for (int i = 0; i < n; ++i)  // (a word named twice has the sum of its entries, in their order)
-    if (all[i] == id) p += p_of[i];
-  at[t * n + j] = expf(logq[t * n + j]) - p;
+  int first = n;
+  for (int i = 0; i < n; ++i)  // (a word named twice has the sum of its entries, in their order, and the first one's log q)
+    if (all[i] == id) p += p_of[i], first = min(first, i);
+  at[t * n + j] = expf(logq[t * n + first]) - p;
 }
 
 __global__ void __launch_bounds__(kThreads) distill_scatter_kernel(const int* ids, const float* at, const float* g, const float* gs,
@@ -330,7 +357,7 @@ cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile
 }
 
 // A warp for each row where there are best words to find and rows enough to fill the SMs with warps: it needs no barriers (2048
-// rows of 129280 words, 20 best: 68 us, a block for each 83; but 512 rows of 32000 words, 8 best: 28 us, 22 by blocks).
+// rows of 129280 words, 20 best: 64 us, a block for each 83; but 512 rows of 32000 words, 8 best: 28 us, 20 by blocks).
 cudaError_t mm_score_join(const MmScores& a, cudaStream_t s) {
   if (a.top_k && a.rows >= 1024) return launch(score_join_warp_kernel, dim3((a.rows + kWarps - 1) / kWarps), kThreads, s, a);
   return launch(score_join_block_kernel, dim3(a.rows), kThreads, s, a);

@@ -228,6 +228,25 @@ def test_groups_around_the_width_of_an_accumulator(dtype, counts):
     assert api.ds4moe_ops_status() == 0
 
 
+@pytest.mark.parametrize("counts", [[20005, 17, 0, 300], [1, 16384, 16385]])
+def test_long_ragged_weight_gradients(counts):
+    """Sums of more terms than an accumulator takes, on pairs of CTAs, with ragged ends: rows of other groups that are not finite stay out."""
+    n, k, g = 152, 264, len(counts)
+    rows = sum(counts) + 7
+    dh, x, z = whole((rows, n), "bf16", 1), whole((rows, k), "bf16", 2), whole((rows, 2 * n), "bf16", 3, 1)
+    dh[sum(counts):], x[sum(counts):] = NAN, NAN
+    if counts[1] > 1:
+        x[counts[0] + 1, 3] = math.inf  # in the second group
+    dz, dw = torch.empty_like(z), full((g, 2 * n, k), "bf16")
+    api.ds4moe_grouped_glu_grad(dh, x, None, offsets(counts), z, dz, None, dw, rows, n, k, g, "none", stream=stream())
+    for e, lo, hi in groups_of(counts):
+        if e == 1 and counts[1] > 1:
+            assert bool(dw[e][:, [c for c in range(k) if c != 3]].isfinite().all()) and not bool(dw[e][:, 3].isfinite().all())
+            continue
+        assert torch.equal(dw[e], (dz[lo:hi].double().T @ x[lo:hi].double()).to(dw.dtype)), e
+    assert api.ds4moe_ops_status() == 0
+
+
 def test_block_offsets_out_of_order_or_range_reach_nothing_outside():
     n, k, rows = 40, 64, 40
     x, w, dh, z = whole((rows, k), "bf16", 1), whole((4, 2 * n, k), "bf16", 2), whole((rows, n), "bf16", 3), whole((rows, 2 * n), "bf16", 4)
@@ -357,6 +376,19 @@ def test_scores_of_equal_and_of_sorted_logits():
     w[:, 0], w[:, 1] = (v // 128 * 128 / 256.0).to(w.dtype), (v % 128 / 256.0).to(w.dtype)  # index / 256, in two parts
     score_check(x, w, tokens, top, "bf16", 1.0, score(x, w, tokens, top))
     score_check(-x, w, tokens, top, "bf16", 0.01, score(-x, w, tokens, top, temperature=0.01))
+
+
+@pytest.mark.parametrize("rows,vocab,d,top", [(2, 140000, 64, 10), (40, 140000, 72, 64), (1030, 140000, 64, 9), (1100, 999, 72, 64),
+                                              (1025, 3000, 64, 33), (33, 20000, 4100, 5), (128, 700, 136, 3), (32, 5000, 16392, 7)])
+def test_scores_of_long_vocabularies_and_many_rows(rows, vocab, d, top):
+    """More partials and chunks than a team's threads hold, more best words than a warp has lanes, sums in several accumulators."""
+    x, w = grid((rows, d), "bf16", 1, 16, 2.0 ** -4), grid((vocab, d), "bf16", 2, 20, 2.0 ** -round(math.log2(10 * d ** 0.5)))
+    tokens = torch.randint(-1, vocab, (rows, 5), generator=gen(3), device="cuda", dtype=torch.int32)
+    score_check(x, w, tokens, top, "bf16", 1.0, score(x, w, tokens, top))
+    x[::3] = 0  # rows of equal logits
+    got = score(x, w, tokens, top)
+    assert torch.equal(got["top_index"][::3].cpu(), torch.arange(top, dtype=torch.int32).expand((rows + 2) // 3, top))
+    assert api.ds4moe_ops_status() == 0
 
 
 def test_scores_in_blocks_of_rows():
