@@ -2,6 +2,8 @@
 // say of each row after it (log probabilities, entropy, best words; the distillation's loss), and the places that the
 // distillation's gradient has at the listed words. One block of 256 threads for each row throughout: a row has up to 256
 // listed words, and 505 to 1010 partials of a vocabulary of 129280.
+#include <type_traits>
+
 #include "mm16_small.cuh"
 
 namespace ds4 {
@@ -142,16 +144,26 @@ __device__ __forceinline__ float value_of(unsigned long long k) {
 }
 __device__ __forceinline__ int index_of(unsigned long long k) { return (int)~(uint32_t)k; }
 
+// Shared memory of a team's selections.
+template <int G>
+struct Picks {
+  static constexpr int kKept = G == kThreads ? 4096 : 1;  // keys that are not fetched again (a warp has registers)
+  unsigned long long keys[kKept], cand[kCandidates], list[2][kMmTop];
+  int count;
+};
+
 // Leaves the k largest keys of item(0..n-1) (all, if there are fewer) in `list` in their order, and returns their number.
 // The k-th largest of the threads' largest values, found bit by bit from the top, is reached by at least k items and as a
 // rule by few more: those are ranked by counting. Where more than kCandidates reach it (equal values, or k above the number
 // of threads) the k-th largest key itself is found, bit by bit over all items (for all rows and sizes at first: 2048 rows,
-// 20 best, 68 us instead of 64). `list`, `cand` and `count` are the team's; what item() reads may not be `list`.
+// 20 best, 68 us instead of 64). What item() reads may not be `list`.
+// A warp's threads hold up to HELD items each in registers, unrolled. A block (HELD 0) keeps them in shared memory under
+// rolled loops: with few rows it runs its code once, and the product has driven that out of the caches (one row, 8 best of
+// 129280: a call 188 us with unrolled loops, 185 so; 256 rows of 32000 words, d 4096: 93 us, 80).
 template <int HELD, int G, class Item>
-__device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned long long* list, unsigned long long* cand, int* count,
-                                       const Item& item) {
-  unsigned long long mine[HELD];  // a thread's items stay in registers up to that many
-  const bool held = n <= HELD * G;
+__device__ __forceinline__ int best_of(Team<G>& team, Picks<G>& p, int n, int k, unsigned long long* list, const Item& item) {
+  unsigned long long mine[HELD ? HELD : 1];
+  const bool held = HELD && n <= HELD * G;
   unsigned long long most = 0;
   if (held) {
 #pragma unroll
@@ -161,8 +173,10 @@ __device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned lon
       most = mine[u] > most ? mine[u] : most;
     }
   } else {
+#pragma unroll 2
     for (int i = team.id(); i < n; i += G) {
       const unsigned long long q = item(i);
+      if (i < p.kKept) p.keys[i] = q;  // (read by the same thread only)
       most = q > most ? q : most;
     }
   }
@@ -171,11 +185,18 @@ __device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned lon
 #pragma unroll
       for (int u = 0; u < HELD; ++u) fn(mine[u]);
     } else {
-      for (int i = team.id(); i < n; i += G) fn(item(i));
+#pragma unroll 1
+      for (int i = team.id(); i < n; i += G) fn(i < p.kKept ? p.keys[i] : item(i));
     }
+  };
+  const auto reach = [&](unsigned long long least) {
+    int c = 0;
+    each([&](unsigned long long q) { c += q >= least; });
+    return team.count(c);
   };
   const uint32_t top = (uint32_t)(most >> 32);
   uint32_t reached = 0;
+#pragma unroll 1
   for (int bit = 31; bit >= 0; --bit) {
     const uint32_t to = reached | 1u << bit;
     const int c = team.votes(top >= to);
@@ -183,32 +204,28 @@ __device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned lon
     if (c == k) break;
   }
   unsigned long long least = reached ? (unsigned long long)reached << 32 : 1;
-  int some = 0;
-  each([&](unsigned long long q) { some += q >= least; });
-  some = team.count(some);
-  if (some > kCandidates) {
-    unsigned long long found = 0;
+  if (reach(least) > kCandidates) {
+    least = 0;  // (there are k at least: kCandidates are more)
+#pragma unroll 1
     for (int bit = 63; bit >= 0; --bit) {
-      const unsigned long long to = found | 1ull << bit;
-      int c = 0;
-      each([&](unsigned long long q) { c += q >= to; });
-      c = team.count(c);
-      if (c >= k) found = to;
+      const unsigned long long to = least | 1ull << bit;
+      const int c = reach(to);
+      if (c >= k) least = to;
       if (c == k) break;
     }
-    least = found;  // (there are k at least: kCandidates are more)
   }
-  if (team.id() == 0) *count = 0;
+  if (team.id() == 0) p.count = 0;
   team.sync();
   each([&](unsigned long long q) {
-    if (q >= least) cand[atomicAdd(count, 1)] = q;
+    if (q >= least) p.cand[atomicAdd(&p.count, 1)] = q;
   });
   team.sync();
-  const int got = *count;
+  const int got = p.count;
   for (int i = team.id(); i < got; i += G) {
-    const unsigned long long q = cand[i];
+    const unsigned long long q = p.cand[i];
     int ahead = 0;
-    for (int j = 0; j < got; ++j) ahead += cand[j] > q;
+#pragma unroll 4
+    for (int j = 0; j < got; ++j) ahead += p.cand[j] > q;
     if (ahead < k) list[ahead] = q;
   }
   team.sync();
@@ -220,7 +237,7 @@ __device__ __forceinline__ int best_of(Team<G>& team, int n, int k, unsigned lon
 // The k best words lie in the k tiles with the largest maxima (a word of any other tile has k words ahead of it, one in
 // each of these), and there in the k chunks of 32 words with the largest: three selections of k.
 template <int G>
-__device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsigned long long (*list)[kMmTop], unsigned long long* cand, int* count) {
+__device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, Picks<G>& picks) {
   const int64_t t = blockIdx.x * (int64_t)Team<G>::kRows + team.row();
   if (t >= a.rows) return;  // (whole teams)
   const int id = team.id();
@@ -275,24 +292,28 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
     if (id == 0) a.loss[t] = sum;
   }
   if (a.top_k == 0) return;
-  const int per_tile = a.tile / kMmStatChunk;
-  const int chunks = (a.vocab + kMmStatChunk - 1) / kMmStatChunk;
-  const auto chunk_max = [&](int chunk) { return chunk < chunks ? key_of(a.chunk_max[chunk * rows + t], chunk) : 0ull; };
-  int n_chunks;
-  if (G == kThreads && a.tile == kMmStatChunk) {  // (few rows: a block each)
-    n_chunks = best_of<16>(team, chunks, a.top_k, list[1], cand, count, chunk_max);
-  } else {
-    const int n_tiles = best_of<G == kThreads ? 4 : 512 / G>(team, a.parts, a.top_k, list[0], cand, count, [&](int i) { return key_of(part[i * rows].x, i); });
-    n_chunks = best_of<kMmTop * 8 / G>(team, n_tiles * per_tile, a.top_k, list[1], cand, count, [&](int i) {
-      return chunk_max(index_of(list[0][i / per_tile]) * per_tile + i % per_tile);
+  // The k best tiles, their k best chunks, these chunks' k best words; few rows have no tiles.
+  const int per_tile = a.tile / kMmStatChunk, chunks = (a.vocab + kMmStatChunk - 1) / kMmStatChunk;
+  int found = per_tile == 1 ? chunks : a.parts;
+  const auto pick = [&](auto held, int step) {
+    const unsigned long long* from = picks.list[step & 1];  // (of the step before)
+    const int each = step == 0 || (step == 1 && per_tile == 1) ? 1 : step == 1 ? per_tile : kMmStatChunk;
+    found = best_of<decltype(held)::value>(team, picks, found * each, a.top_k, picks.list[(step + 1) & 1], [&](int i) -> unsigned long long {
+      const int at = each == 1 ? i : index_of(from[i / each]) * each + i % each;
+      if (at >= (step == 0 ? a.parts : step == 1 ? chunks : a.vocab)) return 0;
+      return key_of(step == 0 ? part[at * rows].x : (step == 1 ? a.chunk_max : a.logits)[at * rows + t], at);
     });
+  };
+  if (G == kThreads) {
+#pragma unroll 1
+    for (int step = per_tile == 1 ? 1 : 0; step < 3; ++step) pick(std::integral_constant<int, 0>(), step);
+  } else {
+    pick(std::integral_constant<int, 16>(), 0);
+    pick(std::integral_constant<int, 16>(), 1);
+    pick(std::integral_constant<int, 32>(), 2);
   }
-  const int n_words = best_of<1024 / G>(team, n_chunks * kMmStatChunk, a.top_k, list[0], cand, count, [&](int i) {
-    const int w = index_of(list[1][i / kMmStatChunk]) * kMmStatChunk + i % kMmStatChunk;
-    return w < a.vocab ? key_of(a.logits[w * rows + t], w) : 0ull;
-  });
   for (int j = id; j < a.top_k; j += G) {
-    const unsigned long long mine = j < n_words ? list[0][j] : 0;
+    const unsigned long long mine = j < found ? picks.list[1][j] : 0;
     a.top_index[t * a.top_k + j] = mine ? index_of(mine) : -1;
     a.top_logprob[t * a.top_k + j] = mine ? (value_of(mine) - m) * c - log_s : NAN;
   }
@@ -301,16 +322,14 @@ __device__ __forceinline__ void score_join(const MmScores& a, Team<G> team, unsi
 __global__ void __launch_bounds__(kThreads) score_join_block_kernel(const MmScores a) {
   __shared__ float f[2][kWarps];
   __shared__ int n[2][kWarps];
-  __shared__ unsigned long long list[2][kMmTop], cand[kCandidates];
-  __shared__ int count;
+  __shared__ Picks<kThreads> picks;
   begin();
-  score_join<kThreads>(a, Team<kThreads>{f, n}, list, cand, &count);
+  score_join<kThreads>(a, Team<kThreads>{f, n}, picks);
 }
 __global__ void __launch_bounds__(kThreads) score_join_warp_kernel(const MmScores a) {
-  __shared__ unsigned long long list[kWarps][2][kMmTop], cand[kWarps][kCandidates];
-  __shared__ int count[kWarps];
+  __shared__ Picks<32> picks[kWarps];
   begin();
-  score_join<32>(a, Team<32>{}, list[threadIdx.x >> 5], cand[threadIdx.x >> 5], count + (threadIdx.x >> 5));
+  score_join<32>(a, Team<32>{}, picks[threadIdx.x >> 5]);
 }
 
 __global__ void __launch_bounds__(kThreads) distill_prepare_kernel(const int* ids, const float* teacher, const float* logq,
