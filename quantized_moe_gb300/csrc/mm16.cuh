@@ -171,7 +171,6 @@ inline bool mm_aligned(const MmOperand& o) {
 constexpr int kMmStatTile = 256;
 constexpr int kMmStatChunk = 32;  // words of one chunk's maximum
 constexpr int kMmFewRows = 32;    // tokens of MM_EPI_SCORE_FEW
-constexpr int kMmFewWidth = 16384;  // and its longest sums: eight accumulators of 2048
 
 // Sets kernel attributes on the current device (once per device).
 cudaError_t mm_prepare();

@@ -792,10 +792,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_ctarank() : 0;
-  // Scores of few tokens: a tile's accumulators, one for every seg of the reduction, lie side by side, and the next tile's
-  // in the other half of tensor memory, so that the stream of W never waits for an epilogue (178 us, @FEW@ so).
-  constexpr bool kBeside = EPI == MM_EPI_SCORE_FEW;
-  const int acc_stride = kBeside ? kAccCols : min(max(a.bn, 32), kAccCols);
+  const int acc_stride = min(max(a.bn, 32), kAccCols);
   // Tiles wider than an accumulator: their columns run on into the other one, so that one pass over A serves up to 512.
   constexpr bool kWide = is_wide(EPI);
   uint32_t tmem_cols = 32;
@@ -981,9 +978,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         uint32_t d = 0;
         int in_seg = 0;  // reduction already in this accumulator
         for (int k = 0; k < o.red; k += BK) {
-          if (kBeside && in_seg == 0 && k > 0) {
-            d += kMmFewRows;
-          } else if (in_seg == 0) {
+          if (in_seg == 0) {
             const int b = wide ? 0 : a.accs == 1 || k == 0 ? buf : 1;  // (1: the second accumulator of the same tile)
             if (!mbar_wait(acc_empty + b, (used >> b & 1) ^ 1, abort_flag, p.err, 6) ||
                 (kWide && wide && !mbar_wait(acc_empty + 1, (used >> 1 & 1) ^ 1, abort_flag, p.err, 6))) {
@@ -1018,8 +1013,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           if (++s == a.stages) s = 0, ph ^= 1;
           in_seg += BK;
           if (in_seg == a.seg || k + BK >= o.red) {
-            if (kBeside && k + BK < o.red) {
-            } else if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
+            if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
               commit<CG>(acc_full);
               commit<CG>(acc_full + 1);
               used ^= 3u;
@@ -1247,7 +1241,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       float z[kHold ? 4 : 1][32];                             // the logits of the thread's four chunks
       const bool folds = a.fold && o.red > a.seg, wide = kWide && o.n > kAccCols;
       bool ok = true;
-      for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 && !kBeside ? a.seg : o.red) {  // accumulators of the tile
+      for (int k = 0; k == 0 || k < o.red; k += a.accs == 1 ? a.seg : o.red) {  // accumulators of the tile
         uint32_t taddr = tmem + (uint32_t)(wide ? 0 : buf * acc_stride) + ((uint32_t)(32 * quad) << 16);
         if (kWide && wide && sum) {
           ok = mbar_wait(acc_full, used & 1, abort_flag, p.err, 5) && mbar_wait(acc_full + 1, used >> 1 & 1, abort_flag, p.err, 5);
@@ -1383,12 +1377,6 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             float v[32];
             float* x = reinterpret_cast<float*>(out_stage) + quad * (32 * 33);
             tmem_ld32(taddr, v);
-            for (int i = 1; i * a.seg < o.red; ++i) {
-              float more[32];
-              tmem_ld32(taddr + i * kMmFewRows, more);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += more[j];
-            }
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j * 33 + lane] = v[j];
             __syncwarp();
@@ -1863,7 +1851,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   } else if (a.split > 1) {
     a.bn = split_bn;
   } else if (few_tokens) {
-    if (gen || p.cols > kMmFewRows || p.red > kMmFewWidth) return cudaErrorInvalidValue;
+    if (gen || p.cols > kMmFewRows) return cudaErrorInvalidValue;
     a.bn = kMmFewRows;
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile
@@ -1916,8 +1904,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   //    back. A longer d is added up as for 16 bits.
   a.seg = kSegFold;
   a.accs = 1;
-  if (few_tokens)
-    a.seg = kSegStats;
+  if (few_tokens)  // (the sums of 32 tokens are added up while the ring fills: accumulators side by side were no faster)
+    a.seg = kSegStats, a.fold = 1;
   else if (stats && (cg == 2 || p.red > 2 * kSegStats))
     a.seg = kSegStats, a.fold = cg == 1;
   else if (stats && p.red > kSegStats)
