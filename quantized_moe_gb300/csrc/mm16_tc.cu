@@ -53,7 +53,8 @@ constexpr int kEpiPlainWide = 8, kEpiGluWide = 9;  // kEpiPlain, MM_EPI_GLU with
 constexpr int kEpiPlainRag = 10;          // kEpiPlain of a ragged reduction
 constexpr int kEpiSpread = 11;            // MM_EPI_STORE of tiles whose sums are joined a share of the columns in each CTA
 __host__ __device__ constexpr bool is_store(int epi) { return epi == MM_EPI_STORE || epi == kEpiSpread; }
-__host__ __device__ constexpr bool is_plain(int epi) { return epi == kEpiPlain || epi == kEpiPlainWide || epi == kEpiPlainRag; }
+constexpr int kEpiPlainScaled = 12;       // kEpiPlain times a number (a softmax loss's weight gradients of 256 rows, 32000 words, d 1024: 80 -> 72 us)
+__host__ __device__ constexpr bool is_plain(int epi) { return epi == kEpiPlain || epi == kEpiPlainScaled || epi == kEpiPlainWide || epi == kEpiPlainRag; }
 __host__ __device__ constexpr bool is_glu(int epi) { return epi == MM_EPI_GLU || epi == kEpiGluWide; }
 __host__ __device__ constexpr bool is_wide(int epi) { return epi == kEpiPlainWide || epi == kEpiGluWide; }
 constexpr int kAccCols = 256;             // columns of one accumulator, the widest MMA
@@ -87,7 +88,7 @@ struct TcArgs {
   int glu_whole;              // one copy brings a gated block's 64 gate and 64 up rows (else 16 rows each)
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
-  int plain;                  // and nothing is to be added
+  int plain;                  // and nothing is to be added (a dense one may be scaled)
   int seg;                    // reduction that one accumulator takes before its sums are added up in fp32 (a multiple of BK)
   int accs;                   // accumulators of one tile that lie side by side in tensor memory (1: two take turns; 2: none is left to)
   int fold;                   // a tile with more reduction than seg is summed up in tensor memory (fold_acc), seg by seg
@@ -1123,6 +1124,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       }
       if (folds) taddr = held;
       if (!named_bar_all(2 + half, 128, ok)) break;  // (the warps that share barriers leave together)
+      const float scale = EPI == kEpiPlainScaled ? *p.e.scale : 1.f;
       for (int c = 32 * half; c < o.n; c += 64) {
         Frag f;
         if (sum) {
@@ -1132,6 +1134,12 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
+        }
+        if (EPI == kEpiPlainScaled) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) f.v[j][r][0] *= scale, f.v[j][r][1] *= scale;
         }
         frag_out(stage, quad, lane, f, p.f16);
         named_bar(2 + half, 128);
@@ -1685,7 +1693,8 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   if (CG == 2 && a.bn > kAccCols) return launch<2, kEpiPlainWide, false>(ta, tb, a, grid, s);
   if (CG == 2 && a.p.rag == MM_RAG_RED) return launch<2, kEpiPlainRag, false>(ta, tb, a, grid, s);
   if (CG == 1 && a.spread) return launch<1, kEpiSpread, false>(ta, tb, a, grid, s);
-  if (!GEN && a.plain && a.split == 1) return launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
+  if (!GEN && a.plain && a.split == 1)
+    return a.p.e.scale ? launch<CG, kEpiPlainScaled, false>(ta, tb, a, grid, s) : launch<CG, kEpiPlain, false>(ta, tb, a, grid, s);
   return launch<CG, MM_EPI_STORE, GEN>(ta, tb, a, grid, s);
 }
 
@@ -1762,6 +1771,8 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlainWide, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiGluWide, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiPlainRag, false>();
+  if (e == cudaSuccess) e = prepare_one<1, kEpiPlainScaled, false>();
+  if (e == cudaSuccess) e = prepare_one<2, kEpiPlainScaled, false>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiSpread, false>();
   if (e == cudaSuccess) e = prepare_one<1, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiScoreOne, false>();
@@ -1811,18 +1822,18 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
   if (p.rag != MM_RAG_RED && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
     a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
-  // Where that leaves a long reduction of several column tiles, tiles of 128 or 256 columns over clusters that also share out
+  // Where that leaves a long reduction of more columns to few CTAs, tiles of 64 to 256 columns over clusters that also share out
   // the joining of their sums, if they are estimated to take less time (cycles: a CTA's stage brings its operands at 64
   // bytes a cycle, and so does the exchange at 32; dx of 512 rows, 16128 words, d 1024: 41 us, 31 so).
   int spread_bn = 0;
-  if (p.may_spread && !gen && p.rag == MM_DENSE && p.epi == MM_EPI_STORE && !p.e.residual && !p.e.accumulate && p.cols > 64 && p.red <= kSegFold) {
+  if (p.may_spread && !gen && p.rag == MM_DENSE && p.epi == MM_EPI_STORE && !p.e.residual && !p.e.accumulate && p.cols > 32 && p.red <= kSegFold) {
     const auto stage = [](int bn) { return 256 + 2 * bn; };
     int64_t best = a.split > 1 ? (int64_t)(blocks + a.split - 1) / a.split * stage(64) : INT64_MAX;
     if (a.split == 1) {
       const int units = p.lanes > BM ? pairs : sms, cgs = p.lanes > BM ? 2 : 1;
       best = schedule((p.lanes + BM * cgs - 1) / (BM * cgs), p.cols, p.b.red_major, 0, cgs, std::max(1, units)).cost * 2 * blocks;
     }
-    for (int bn = 128; bn <= 256; bn *= 2) {
+    for (int bn = 64; bn <= 256; bn *= 2) {
       const int64_t tiles = lanes128 * ((p.cols + bn - 1) / bn);
       int n = (int)std::min<int64_t>({sms / tiles, kMaxSpread, blocks / 6});
       // (what a CTA receives has to fit where its stages were)
@@ -1837,7 +1848,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
   a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
                by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
-  a.plain = a.rows_out && p.epi == MM_EPI_STORE && !ep.scale && !ep.bias && !ep.z && !ep.residual && !ep.accumulate && ep.act == MM_ACT_NONE;
+  a.plain = a.rows_out && p.epi == MM_EPI_STORE && (!ep.scale || p.rag == MM_DENSE) && !ep.bias && !ep.z && !ep.residual && !ep.accumulate && ep.act == MM_ACT_NONE;
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
   // narrow product); of ragged reductions those whose results leave by rows.
   const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
