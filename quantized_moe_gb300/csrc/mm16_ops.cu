@@ -462,7 +462,8 @@ struct ScoreSpace {
   ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
     const int tile = ds4::mm_score_tile(1, rows <= ds4::kMmFewRows);  // (the smallest: more rows never need less)
     const int64_t tiles = (vocab + tile - 1) / tile;
-    const int64_t parts = rows <= ds4::kMmFewRows ? std::max<int64_t>(ds4::kMmFewParts, (vocab + 127) / 128) : tiles;
+    const int64_t wide = (vocab + 127) / 128;  // (few rows whose operands are not aligned take tiles of 128 words)
+    const int64_t parts = rows <= ds4::kMmFewRows ? std::max(std::min<int64_t>(ds4::kMmFewParts, 4 * wide), wide) : tiles;
     part = 0;
     ent = up(8 * rows * parts, 16);
     want = ent + up(4 * rows * parts, 16);
