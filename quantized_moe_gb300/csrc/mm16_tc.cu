@@ -1,7 +1,7 @@
 // The 16-bit products on the 5th-generation tensor cores: out[c][l] = sum_r A(l, r) B(c, r).
 //
 // Persistent: one CTA (or pair of CTAs) per SM (or two SMs) loops over output tiles of 128 lanes per
-// CTA x up to 256 columns. The lanes are the contiguous index of the output, so that a tensor-memory
+// CTA x up to 256 columns (of groups around that size 512, in both accumulators). The lanes are the contiguous index of the output, so that a tensor-memory
 // lane is a lane of the output; the columns are rows of tokens (or of dW), of which a tile takes
 // exactly what its group has, rounded up to the MMA's granule, so that a group's weights cross HBM
 // once however ragged the counts are.
@@ -19,9 +19,12 @@
 // bytes, eight loader warps (12-19) read it with ordinary loads and write the same swizzled layout.
 // Few tiles share their reduction out over a cluster of CTAs, which join their sums in shared memory.
 //
+// The gated block is a product whose lanes are 16 gate features, the same 16 up features, and so on, so that a thread of the
+// epilogue holds both factors of its results. Scores have tokens as lanes, a thread each, or, few of them, as columns.
+//
 // What bounds it (GB300, measured): the experts' products stream their weights (256 experts, 32768
 // rows, n 2048, k 4096: 0.70-0.72 ms = 6.5-6.8 TB/s, 96-99 % of the copy bandwidth, for y and dx; the
-// weight gradients, 4.3 GB of results, 0.85 ms = 5.5 TB/s: their way through shared memory beside the MMAs' operands);
+// weight gradients, 4.3 GB of results, 0.80 ms = 5.9 TB/s: their way through shared memory beside the MMAs' operands);
 // large dense products the tensor pipe and the SMs' L2 reads (2048 x 129280 x 4096: 1.12 ms = 1.94
 // PFLOP/s, the rate of a large library product; 4096^3 with its epilogue 94 us = 1.46 PFLOP/s, of
 // which a seventh is the last, partial round and the launch); single tokens the launch and one pass of
