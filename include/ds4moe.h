@@ -358,12 +358,14 @@ int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const 
  *                                  (int32 and fp32 [rows x top_k], top_k 0..64 and at most vocab)
  * all fp32 but the indices, lists without gaps between rows. A place without a token holds -1 and has logprob 0; so has one
  * that lies outside the vocabulary otherwise, which also sets bit 0 of ds4moe_ops_status. lse and entropy may be NULL, the
- * lists where they have no places. A logit of -inf has probability 0; the entropy of a row with no other is NaN. A logit
+ * lists where they have no places. A logit of -inf has probability 0; a row with no other has lse -inf, its entropy and
+ * log probabilities are NaN. A logit
  * that is NaN makes lse, logprob and entropy of its row NaN and is listed nowhere; places of top_index that this leaves
  * hold -1 and NaN.
  * workspace: 16-byte aligned device memory. ds4moe_logprobs_workspace returns the bytes for all rows at once (with top_k the
  * logits in fp32 are in it); a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
- * which reads W, and less than a block of 128 (or all) rows needs returns DS4MOE_ERR_CAPACITY. */
+ * which reads W (the results are the same bits), and less than a block of 128 (or all) rows needs returns
+ * DS4MOE_ERR_CAPACITY. */
 int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k);
 int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* logprob, float* lse, float* entropy,
                     int32_t* top_index, float* top_logprob, int32_t rows, int32_t vocab, int32_t d, int32_t n_tokens,

@@ -111,6 +111,8 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
+// An arrival at a pair's leader. Without a release at cluster scope, which would wait for the warp's stores to global memory: what
+// it stands for is complete when it is issued (tensor memory read, tcgen05.wait::ld; a cleared end written, the proxy fence).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
 }
