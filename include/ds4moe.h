@@ -364,7 +364,7 @@ int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const 
  * hold -1 and NaN.
  * workspace: 16-byte aligned device memory. ds4moe_logprobs_workspace returns the bytes for all rows at once (with top_k the
  * logits in fp32 are in it); a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
- * which reads W (the results are the same bits), and less than a block of 128 (or all) rows needs returns
+ * which reads W (sums may then be joined in another order), and less than a block of 128 (or all) rows needs returns
  * DS4MOE_ERR_CAPACITY. */
 int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k);
 int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* logprob, float* lse, float* entropy,

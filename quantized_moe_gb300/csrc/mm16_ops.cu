@@ -500,7 +500,7 @@ cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, 
   const int vocab = call.vocab;
   const ds4::MmOperand ox = {call.x, call.ldx, 0, 1}, ow = {call.w, call.ldw, 0, 1};
   const bool few = block <= ds4::kMmFewRows && ds4::mm_aligned(ox) && ds4::mm_aligned(ow);
-  a.tile = ds4::mm_score_tile(rows, few);  // (of the call, so that blocks do not change its bits)
+  a.tile = ds4::mm_score_tile(rows, few);  // (of the call: its blocks take the same tiles)
   a.vocab = vocab, a.parts = few ? ds4::mm_few_parts(vocab) : (vocab + a.tile - 1) / a.tile, a.err = call.err;
   const ScoreSpace at(block, vocab, a.n, a.top_k);
   cudaError_t e = cudaSuccess;
