@@ -228,6 +228,21 @@ def test_groups_around_the_width_of_an_accumulator(dtype, counts):
     assert api.ds4moe_ops_status() == 0
 
 
+@pytest.mark.parametrize("counts,n,k", [([300, 257, 256, 420, 255, 0, 310, 400], 1289, 136), ([3], 129, 4096), ([2, 0, 5], 17, 1024), ([1], 2500, 8),
+                                        ([40] * 30, 16, 64), ([300, 290, 280], 3333, 72)])
+def test_blocks_of_odd_widths(counts, n, k):
+    """Aligned operands with results that are not: wide tiles and split sums stored a lane at a time."""
+    rows, g = sum(counts), len(counts)
+    x, w = whole((rows, k), "fp16", 1), whole((g, 2 * n, k), "fp16", 2, 1)
+    h, z, clean = block(x, w, offsets(counts), n, "relu", "fp16")
+    assert clean
+    for e, lo, hi in groups_of(counts):
+        ref = x[lo:hi].double() @ w[e].double().T
+        assert torch.equal(z[lo:hi], ref.to(z.dtype)), e
+        assert torch.equal(h[lo:hi], (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype)), e
+    assert api.ds4moe_ops_status() == 0
+
+
 @pytest.mark.parametrize("counts", [[20005, 17, 0, 300], [1, 16384, 16385]])
 def test_long_ragged_weight_gradients(counts):
     """Sums of more terms than an accumulator takes, on pairs of CTAs, with ragged ends: rows of other groups that are not finite stay out."""
