@@ -438,6 +438,7 @@ cudaError_t block_grad(const void* dz, int64_t lddz, const void* x, int64_t ldx,
     ds4::MmProblem p = product(w, ldw, false, dz, lddz, true, k, rows, n, dtype, dx, lddx, err);
     p.a.group_stride = w_stride;
     if (offsets) p.groups = n_groups, p.offsets = offsets, p.rag = ds4::MM_RAG_COLS;
+    p.may_spread = 1;
     e = ds4::mm_launch(p, s);
   }
   if (e == cudaSuccess && dw) {

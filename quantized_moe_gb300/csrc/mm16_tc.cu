@@ -1827,6 +1827,13 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   const int64_t few = lanes128 * (p.rag == MM_RAG_COLS ? std::min(p.groups, p.cols) : (p.cols + split_bn - 1) / split_bn);
   if (p.rag != MM_RAG_RED && (p.epi == MM_EPI_STORE || p.epi == MM_EPI_GLU) && (p.rag == MM_DENSE || p.cols <= 64) && 2 * few <= sms)
     a.split = (int)std::max<int64_t>(1, std::min<int64_t>({sms / few, blocks / 6, split_bn == 32 ? 8 : 4}));
+  // Clusters that do not all run at once take two rounds (1 token, a gated block of 1024 features, k 3664, 16 tiles: 16.4 us
+  // in eight shares, 9.3 in six). Not all that the device is said to hold always find room, but of two and of four (said 28 of
+  // five: 25 took 14.3 us, 24 10.5; 46 of three: 44 took 34 us, in two shares 26): an eighth is left. Products whose bits
+  // earlier callers rely on keep their shares.
+  const auto held_at_once = [&](int n) { return n == 2 || n == 4 ? g_clusters[dev & 63][n] : g_clusters[dev & 63][n] * 7 / 8; };
+  if (p.epi == MM_EPI_GLU || p.may_spread)
+    while (a.split > 1 && held_at_once(a.split) < few) --a.split;
   // Where that leaves a long reduction of more columns to few CTAs, tiles of 64 to 256 columns over clusters that also share out
   // the joining of their sums, if they are estimated to take less time (cycles: a CTA's stage brings its operands at 64
   // bytes a cycle, and so does the exchange at 32; dx of 512 rows, 16128 words, d 1024: 41 us, 31 so).
@@ -1844,7 +1851,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
       // (what a CTA receives has to fit where its stages were)
       const int stage_bytes = A_BYTES + bn * BK * 2, held = (kSmemMax - smem_bytes(1, bn, 0, 1, p)) / stage_bytes * stage_bytes;
       while (n > 1 && (n - 1) * ((bn / 32 + n - 1) / n * 32) * kPartLd * 4 > held) --n;
-      if (n < 2 || g_clusters[dev & 63][n] < tiles) continue;
+      if (n < 2 || held_at_once(n) < tiles) continue;
       const int64_t cost = (blocks + n - 1) / n * stage(bn) + bn * 16 + 3000;
       if (cost < best) best = cost, spread_bn = bn, a.split = n;
     }
