@@ -463,8 +463,7 @@ struct ScoreSpace {
   ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
     const int tile = ds4::mm_score_tile(1, rows <= ds4::kMmFewRows);  // (the smallest: more rows never need less)
     const int64_t tiles = (vocab + tile - 1) / tile;
-    const int64_t wide = (vocab + 127) / 128;  // (few rows whose operands are not aligned take tiles of 128 words)
-    const int64_t parts = rows <= ds4::kMmFewRows ? std::max(std::min<int64_t>(ds4::kMmFewParts, 4 * wide), wide) : tiles;
+    const int64_t parts = rows <= ds4::kMmFewRows ? std::min<int64_t>(ds4::kMmFewParts, 4 * ((vocab + 127) / 128)) : tiles;
     part = 0;
     ent = up(8 * rows * parts, 16);
     want = ent + up(4 * rows * parts, 16);
@@ -499,8 +498,7 @@ int score_rows(Check& c, int rows, int vocab, int n, int top_k, int64_t bytes) {
 }
 cudaError_t scores(const ScoreCall& call, ds4::MmScores a, int rows, int block, char* ws, cudaStream_t s) {
   const int vocab = call.vocab;
-  const ds4::MmOperand ox = {call.x, call.ldx, 0, 1}, ow = {call.w, call.ldw, 0, 1};
-  const bool few = block <= ds4::kMmFewRows && ds4::mm_aligned(ox) && ds4::mm_aligned(ow);
+  const bool few = block <= ds4::kMmFewRows;
   a.tile = ds4::mm_score_tile(rows, few);  // (of the call: its blocks take the same tiles)
   a.vocab = vocab, a.parts = few ? ds4::mm_few_parts(vocab) : (vocab + a.tile - 1) / a.tile, a.err = call.err;
   const ScoreSpace at(block, vocab, a.n, a.top_k);

@@ -1692,7 +1692,7 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
     case MM_EPI_SCORE:
       if (!GEN && a.p.red <= kSegStats) return launch<CG, kEpiScoreOne, false>(ta, tb, a, grid, s);
       return launch<CG, MM_EPI_SCORE, GEN>(ta, tb, a, grid, s);
-    case MM_EPI_SCORE_FEW: return CG == 1 && !GEN ? launch<1, MM_EPI_SCORE_FEW, false>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
+    case MM_EPI_SCORE_FEW: return CG == 1 ? launch<1, MM_EPI_SCORE_FEW, GEN>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
     default: break;
   }
   if (CG == 2 && a.bn > kAccCols) return launch<2, kEpiPlainWide, false>(ta, tb, a, grid, s);
@@ -1782,6 +1782,7 @@ cudaError_t mm_prepare() {
   if (e == cudaSuccess) e = prepare_one<1, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<2, kEpiScoreOne, false>();
   if (e == cudaSuccess) e = prepare_one<1, MM_EPI_SCORE_FEW, false>();
+  if (e == cudaSuccess) e = prepare_one<1, MM_EPI_SCORE_FEW, true>();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
@@ -1874,7 +1875,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   } else if (a.split > 1) {
     a.bn = split_bn;
   } else if (few_tokens) {
-    if (gen || p.cols > kMmFewRows) return cudaErrorInvalidValue;
+    if (p.cols > kMmFewRows) return cudaErrorInvalidValue;
     a.bn = kMmFewRows;
   } else if (p.rag == MM_RAG_COLS) {
     // the groups' sizes are only known on the device: a tile that holds twice the average (a smaller tile

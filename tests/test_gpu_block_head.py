@@ -243,6 +243,26 @@ def test_blocks_of_odd_widths(counts, n, k):
     assert api.ds4moe_ops_status() == 0
 
 
+@pytest.mark.parametrize("counts,n", [([3], 960), ([1], 1024), ([40], 1280), ([5], 1536), ([2], 1664), ([64], 2432), ([4, 4, 4, 4], 700), ([1, 0, 7], 800)])
+@pytest.mark.parametrize("k", [2048, 2001])
+def test_blocks_whose_sums_are_shared_out(counts, n, k):
+    """Few rows: clusters that fit the device at once or would not, forward and dx, with the shares' sums exact."""
+    rows, g = sum(counts), len(counts)
+    x, w, dz = whole((rows, k), "bf16", 1), whole((g, 2 * n, k), "bf16", 3), full((rows, 2 * n), "bf16")
+    off = None if g == 1 else offsets(counts)
+    h, z, clean = block(x, w, off, n, "none", "bf16")
+    assert clean
+    dx = full((rows, k), "bf16")
+    up = whole((rows, 2 * n), "bf16", 5)
+    api.ds4moe_grouped_glu_grad(whole((rows, n), "bf16", 6), x, w, off, up, dz, dx, None, rows, n, k, g, "none", "bf16", stream=stream())
+    for e, lo, hi in groups_of(counts):
+        ref = x[lo:hi].double() @ w[e].double().T
+        assert torch.equal(z[lo:hi], ref.to(torch.bfloat16)) and torch.equal(h[lo:hi], (ref[:, :n] * ref[:, n:]).to(torch.bfloat16))
+        ref, terms = dz[lo:hi].double() @ w[e].double(), dz[lo:hi].double().abs() @ w[e].double().abs()
+        assert bool(((dx[lo:hi].double() - ref).abs() <= _tolerance(ref, terms, 2 * n, "bf16")).all())
+    assert api.ds4moe_ops_status() == 0
+
+
 @pytest.mark.parametrize("counts", [[20005, 17, 0, 300], [1, 16384, 16385]])
 def test_long_ragged_weight_gradients(counts):
     """Sums of more terms than an accumulator takes, on pairs of CTAs, with ragged ends: rows of other groups that are not finite stay out."""
@@ -377,6 +397,23 @@ def test_scores(rows, vocab, d, n, top):
     x, w = normal((rows, d), "bf16", 1), normal((vocab, d), "bf16", 2, 2 * d ** -0.5)
     tokens = torch.randint(0, vocab, (rows, n), generator=gen(3), device="cuda", dtype=torch.int32)
     score_check(x, w, tokens, top, "bf16", 1.0, score(x, w, tokens, top), order=False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,vocab,d,n,top,pad,skew", [
+    (1, 40001, 77, 1, 8, 0, 0), (32, 25003, 130, 5, 64, 0, 0), (31, 129, 2051, 9, 3, 0, 0), (2, 140001, 64, 4, 10, 3, 1), (20, 900, 4201, 2, 10, 0, 1),
+    (7, 1, 9, 1, 1, 0, 0), (5, 33, 1, 200, 33, 0, 0), (17, 20000, 72, 3, 5, 8, 4)])
+def test_scores_of_few_rows_anywhere(dtype, rows, vocab, d, n, top, pad, skew):
+    """Rows that start at any element, words that fill none or several tiles of a CTA; a row of NaN beside the others."""
+    x, w = grid((rows, d), dtype, 1, 16, 2.0 ** -4), grid((vocab, d), dtype, 2, 20, 2.0 ** -round(math.log2(10 * d ** 0.5)))
+    tokens = torch.randint(-1, vocab, (rows, n), generator=gen(3), device="cuda", dtype=torch.int32)
+    score_check(x, w, tokens, top, dtype, 0.8, score(x, w, tokens, top, dtype, 0.8, pad, skew))
+    if rows > 1:
+        x[rows - 1] = NAN
+        got = score(x, w, tokens, top, dtype, 0.8, pad, skew)
+        score_check(x[:-1], w, tokens[:-1], top, dtype, 0.8, {name: v[:-1] for name, v in got.items()})
+        assert bool(got["lse"][-1].isnan())
+    assert api.ds4moe_ops_status() == 0
 
 
 def test_scores_of_equal_and_of_sorted_logits():
