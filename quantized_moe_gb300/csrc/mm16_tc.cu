@@ -67,7 +67,9 @@ constexpr int kMaxSpread = 8;             // CTAs of a cluster that share out a 
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
-constexpr int kLoaders = 8;               // loader warps of the unaligned form
+// Loader warps of the unaligned form: with 16 a thread's share of a stage is small enough to be held a whole stage ahead (with 8 a
+// stage's second half of B waited for its first: 1231 x 7770 x 3498 276 us, 211; 42 groups, 16356 rows, n 1696, k 3315 1880, 1378).
+constexpr int kLoaders = 16;
 constexpr int kThreads = 32 * kFirstLoader;
 constexpr int kRowBytes = 2 * BM + 16;    // a staged row of 128 lanes: 16 bytes on, so that eight rows' chunks hit all banks
 constexpr int kPartLd = BM + 4;           // floats from one column of a partial sum to the next (conflict-free as fragments)
@@ -328,70 +330,71 @@ __device__ __forceinline__ int mma_n(const MmProblem& p, int n) {
 
 // One operand's stages by ordinary loads, in the layout that the TMA's 128-byte swizzle gives (16-byte chunk index XOR
 // row mod 8). K-major: the rows of 64 elements are lanes or columns and their elements the reduction; MN-major the other
-// way round, in boxes of 64 x 64. A thread owns one 16-byte chunk of every 32nd row, so that neither its chunk nor the
+// way round, in boxes of 64 x 64. A thread owns one 16-byte chunk of every 64th row, so that neither its chunk nor the
 // parity of its addresses changes: it reads the aligned words that hold its eight elements and, where the row starts in
 // the middle of a word, shifts them by an element. Elements outside the matrix are zeros; their words are not read.
 struct Loader {
   const uint16_t* src;  // of the thread's chunk in its first row
-  int64_t step;         // elements to the chunk 32 rows on
+  int64_t step;         // elements to the chunk 64 rows on
   int odd, red_major, row, ch;
   int mn_left, r_left;  // lanes or columns, and reduction, from the thread's first element to their ends
   int pitch;            // lanes or columns from one of the thread's rows to the next (K-major)
   __device__ __forceinline__ void start(const uint16_t* base, int64_t ld, int red, int mn0, int mn_end, int r0, int r_end, int tid) {
     red_major = red;
-    row = tid >> 3, ch = tid & 7, pitch = 32;
+    row = tid >> 3, ch = tid & 7, pitch = 64;
     const int mn = red ? mn0 + row : mn0 + ch * 8, r = red ? r0 + ch * 8 : r0 + row;
     src = base + (red ? (int64_t)mn * ld + r : (int64_t)r * ld + mn);
-    step = 32 * ld;
+    step = red ? 64 * ld : 64;
     odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
     mn_left = mn_end - mn, r_left = r_end - r;
   }
   // The gated block's weights, `up` elements from a gate row to its up row: 16 gate rows, then the same 16 up rows.
   __device__ __forceinline__ void start_glu(const uint16_t* base, int64_t ld, int64_t up, int f0, int f_end, int r0, int r_end, int tid) {
-    start(base, ld, 1, f0 + ((tid >> 3) & 15), f_end, r0, r_end, tid & 7);
-    row = tid >> 3, pitch = 16;
+    start(base, ld, 1, f0 + ((tid >> 4 & 16) | (tid >> 3 & 15)), f_end, r0, r_end, tid & 7);
+    row = tid >> 3, pitch = 32;
     if (row & 16) src += up;
-    step = 16 * ld;
+    step = 32 * ld;
     odd = (int)(reinterpret_cast<uintptr_t>(src) >> 1) & 1;
   }
   __device__ __forceinline__ int valid(int u) const {
     if (red_major) return mn_left > pitch * u ? min(8, r_left) : 0;
-    return r_left > 32 * (u & 1) ? min(8, mn_left - 64 * (u >> 1)) : 0;
+    return r_left > 0 ? min(8, mn_left - 64 * u) : 0;
   }
-  // The words of the chunks in rows 32 u0 .. 32 u0 + 96 of the current stage, and their way into the stage: other work
-  // goes in between, while they are in flight.
-  __device__ __forceinline__ void load(int u0, int units, uint32_t (&w)[4][5]) const {
+  // The words of the thread's chunks of the current stage, up to the operand's row `rows`, and their way into the stage: other
+  // work goes in between, while they are in flight.
+  template <int N>
+  __device__ __forceinline__ void load(int rows, uint32_t (&w)[N][5]) const {
     const uint32_t* q = reinterpret_cast<const uint32_t*>(src - odd);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i, v = u < units ? valid(u) : 0;
-      const uint32_t* qu = q + (red_major ? u * step : (u & 1) * step + 64 * (u >> 1)) / 2;
+    for (int u = 0; u < N; ++u) {
+      const int v = 64 * u < rows ? valid(u) : 0;
+      const uint32_t* qu = q + u * step / 2;
       if (v >= 8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[i][k] = qu[k];
-        w[i][4] = odd ? qu[4] : 0u;
+        for (int k = 0; k < 4; ++k) w[u][k] = qu[k];
+        w[u][4] = odd ? qu[4] : 0u;
       } else {
 #pragma unroll
-        for (int k = 0; k < 5; ++k) w[i][k] = v > 0 && 2 * k < v + odd ? qu[k] : 0u;  // (a word with a wanted element)
+        for (int k = 0; k < 5; ++k) w[u][k] = v > 0 && 2 * k < v + odd ? qu[k] : 0u;  // (a word with a wanted element)
       }
     }
   }
-  __device__ __forceinline__ void put(uint8_t* dst, int u0, int units, const uint32_t (&w)[4][5]) const {
+  template <int N>
+  __device__ __forceinline__ void put(uint8_t* dst, int rows, const uint32_t (&w)[N][5]) const {
     const uint32_t sh = odd * 16;
     uint8_t* to = dst + row * 128 + ((ch ^ (row & 7)) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i;
-      if (u >= units) break;
+    for (int u = 0; u < N; ++u) {
+      if (64 * u + (red_major ? row : 0) >= rows) break;
       uint32_t r[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[i][k], w[i][k + 1], sh);
+      for (int k = 0; k < 4; ++k) r[k] = __funnelshift_r(w[u][k], w[u][k + 1], sh);
       const int v = valid(u);
       if (v < 8) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) r[k] = v - 2 * k < 1 ? 0u : v - 2 * k < 2 ? r[k] & 0xffffu : r[k];
       }
-      *reinterpret_cast<uint4*>(to + u * 4096) = make_uint4(r[0], r[1], r[2], r[3]);
+      *reinterpret_cast<uint4*>(to + u * 8192) = make_uint4(r[0], r[1], r[2], r[3]);
     }
   }
   __device__ __forceinline__ void next_stage(int64_t elements) {
@@ -939,23 +942,22 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       else
         la.start(pa, p.a.ld, p.a.red_major, o.l0, p.lanes, o.r0, o.r0 + o.red, tid);
       lb.start(static_cast<const uint16_t*>(p.b.p), p.b.ld, p.b.red_major, o.c0, o.c0 + o.n, o.r0, o.r0 + o.red, tid);
-      const int b_units = (nb + 31) / 32;
-      uint32_t wa[4][5], wb[4][5];
-      if (o.red > 0) la.load(0, BM / 32, wa);
+      const int b_rows = (nb + 31) / 32 * 32;  // (a stage has room for whole 32s)
+      uint32_t wa[BM / 64][5], wb[kAccCols / 64][5];  // a stage ahead
+      if (o.red > 0) {
+        la.load(BM, wa);
+        lb.load(b_rows, wb);
+      }
       for (int k = 0; k < o.red; k += BK) {
-        lb.load(0, b_units, wb);
         ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1));
         if (!ok) break;
         uint8_t* st = smem + s * stage_bytes;
-        la.put(st, 0, BM / 32, wa);
+        la.put(st, BM, wa);
         la.next_stage(p.a.red_major ? BK : BK * p.a.ld);
-        if (k + BK < o.red) la.load(0, BM / 32, wa);  // in flight over the next stage's wait
-        lb.put(st + A_BYTES, 0, b_units, wb);
-        if (b_units > 4) {
-          lb.load(4, b_units, wb);
-          lb.put(st + A_BYTES, 4, b_units, wb);
-        }
+        if (k + BK < o.red) la.load(BM, wa);
+        lb.put(st + A_BYTES, b_rows, wb);
         lb.next_stage(p.b.red_major ? BK : BK * p.b.ld);
+        if (k + BK < o.red) lb.load(b_rows, wb);
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s);
