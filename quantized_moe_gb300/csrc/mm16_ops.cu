@@ -160,7 +160,8 @@ int64_t best_piece(int64_t most, int rows, int vocab, int d, bool dx, bool dw) {
            (dw ? ds4::mm_cost(d, (int)words, rows, true) + launch : 0);
   };
   int64_t best = most, best_cost = INT64_MAX;
-  for (int64_t piece = most; 2 * piece > most && piece >= kPieceMin; piece -= kPieceMin) {
+  const int64_t step = up(most / 64, kPieceMin);  // (32 tries, a few microseconds)
+  for (int64_t piece = most; 2 * piece > most && piece >= kPieceMin; piece -= step) {
     const int64_t cost = vocab / piece * one(piece) + one(vocab % piece);
     if (cost < best_cost) best_cost = cost, best = piece;
   }
@@ -186,6 +187,7 @@ struct SoftGrad {
   const int* ids;
   const float* places;
   int listed;
+  int64_t piece_max;  // words of a piece
 };
 cudaError_t soft_grad(const SoftGrad& q, cudaStream_t s) {
   const char* wb = static_cast<const char*>(q.w);
@@ -193,7 +195,7 @@ cudaError_t soft_grad(const SoftGrad& q, cudaStream_t s) {
   const int64_t lddz = up(rows, 8), ldx = q.ldx, ldw = q.ldw;
   // the largest piece of the vocabulary that the workspace holds
   const int64_t fits = q.dz_bytes / (2 * lddz) / kPieceMin * kPieceMin;
-  const int64_t piece = best_piece(std::min<int64_t>({fits, kPieceMax, up(vocab, kPieceMin)}), rows, vocab, d, q.dx, q.dw);
+  const int64_t piece = best_piece(std::min<int64_t>({fits, q.piece_max, up(vocab, kPieceMin)}), rows, vocab, d, q.dx, q.dw);
   cudaError_t e = cudaSuccess;
   for (int64_t v0 = 0; v0 < vocab && e == cudaSuccess; v0 += piece) {
     const int pv = (int)std::min<int64_t>(piece, vocab - v0);
@@ -422,7 +424,7 @@ extern "C" int ds4moe_cross_entropy_grad(const void* x, const void* w, const int
     if (e != cudaSuccess) return c.cuda(e);
     SoftGrad q = {x, w, ldx, ldw, dx, dw, lddx, lddw, rows, vocab, d, dtype, err};
     q.gs = gs, q.sum = sum, q.dz = ws + held, q.dz_bytes = workspace_bytes - held;
-    q.lse = lse, q.g = dloss, q.inv_t = 1.f, q.labels = labels, q.ignore = ignore_index;
+    q.lse = lse, q.g = dloss, q.inv_t = 1.f, q.labels = labels, q.ignore = ignore_index, q.piece_max = kPieceMax;
     return c.cuda(soft_grad(q, s));
   });
 }
@@ -545,6 +547,12 @@ struct DistillSpace {
   }
   int64_t total(int64_t rows, int64_t piece) const { return dz + 2 * up(rows, 8) * piece; }
 };
+// Its pieces of the vocabulary: of up to 512 rows as many words as make 64 MB of dz, which still come from L2 (128 rows, 129280 words,
+// d 2048: 605 us in pieces of 16384, 383 in one; 512 rows, d 1024: 623, 497 in pieces of 32768 to 65536). Beyond, the longer sums of
+// dx, in several accumulators, cost more than fewer launches save (1024 rows, 64000 words, d 1024: 431 us, 505 in halves).
+int64_t distill_piece(int64_t rows) {
+  return rows > 512 ? kPieceMax : std::max<int64_t>(kPieceMax, ((int64_t)1 << 25) / up(rows, 8) / kPieceMin * kPieceMin);
+}
 
 }  // namespace
 
@@ -634,7 +642,7 @@ extern "C" int ds4moe_logprobs(const void* x, const void* w, const int32_t* toke
 extern "C" int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k) {
   if (rows <= 0 || vocab <= 0 || d <= 0 || top_k <= 0) return 16;
   return std::max<int64_t>(ScoreSpace(rows, vocab, top_k, 0).total,
-                           DistillSpace(rows, d, top_k).total(rows, std::min<int64_t>(kPieceMax, up(vocab, kPieceMin))));
+                           DistillSpace(rows, d, top_k).total(rows, std::min<int64_t>(distill_piece(rows), up(vocab, kPieceMin))));
 }
 
 extern "C" int ds4moe_distill(const void* x, const void* w, const int32_t* ids, const float* teacher, float* loss,
@@ -696,7 +704,7 @@ extern "C" int ds4moe_distill_grad(const void* x, const void* w, const int32_t* 
     if (e != cudaSuccess) return c.cuda(e);
     SoftGrad q = {x, w, ldx, ldw, dx, dw, lddx, lddw, rows, vocab, d, dtype, err};
     q.gs = gs, q.sum = reinterpret_cast<float*>(ws + at.sum), q.dz = ws + at.dz, q.dz_bytes = workspace_bytes - at.dz;
-    q.lse = lse, q.g = g, q.inv_t = inv_t, q.ids = ids, q.places = places, q.listed = top_k;
+    q.lse = lse, q.g = g, q.inv_t = inv_t, q.ids = ids, q.places = places, q.listed = top_k, q.piece_max = distill_piece(rows);
     return c.cuda(soft_grad(q, s));
   });
 }
