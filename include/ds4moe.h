@@ -363,7 +363,7 @@ int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const 
  * that is NaN makes lse, logprob and entropy of its row NaN and is listed nowhere; places of top_index that this leaves
  * hold -1 and NaN.
  * workspace: 16-byte aligned device memory. ds4moe_logprobs_workspace returns the bytes for all rows at once (with top_k the
- * logits in fp32 are in it); a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
+ * logits in fp32 are in it), and for any smaller number of rows; a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
  * which reads W (sums may then be joined in another order), and less than a block of 128 (or all) rows needs returns
  * DS4MOE_ERR_CAPACITY. */
 int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k);

@@ -463,7 +463,7 @@ void block_groups(Check& c, const void* offsets, int n_groups) {
 struct ScoreSpace {
   int64_t part, ent, want, first, zwant, chunk_max, logits, total;
   ScoreSpace(int64_t rows, int64_t vocab, int64_t n, int top_k) {
-    const int tile = ds4::mm_score_tile(1, rows <= ds4::kMmFewRows);  // (the smallest: more rows never need less)
+    const int tile = ds4::mm_score_tile(1, rows <= ds4::kMmFewRows);  // (the smallest of any number of rows, up to kMmFewRows or beyond)
     const int64_t tiles = (vocab + tile - 1) / tile;
     const int64_t parts = rows <= ds4::kMmFewRows ? std::min<int64_t>(ds4::kMmFewParts, 4 * ((vocab + 127) / 128)) : tiles;
     part = 0;
@@ -474,6 +474,11 @@ struct ScoreSpace {
     chunk_max = zwant + up(4 * rows * n, 16);
     logits = chunk_max + (top_k ? up(4 * rows * ((vocab + ds4::kMmStatChunk - 1) / ds4::kMmStatChunk), 16) : 0);
     total = logits + (top_k ? up(4 * rows * vocab, 16) : 0);
+  }
+  // What a query returns. Few rows have more partials and more entries of `first` each, so that 33 may take less than 32
+  // (129280 words, one token: 467056 bytes, 652160): a workspace for more rows has to serve fewer.
+  static int64_t bytes(int64_t rows, int64_t vocab, int64_t n, int top_k) {
+    return std::max(ScoreSpace(rows, vocab, n, top_k).total, ScoreSpace(std::min<int64_t>(rows, ds4::kMmFewRows), vocab, n, top_k).total);
   }
 };
 
@@ -609,7 +614,7 @@ extern "C" int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void
 
 extern "C" int64_t ds4moe_logprobs_workspace(int32_t rows, int32_t vocab, int32_t n_tokens, int32_t top_k) {
   if (rows <= 0 || vocab <= 0 || n_tokens < 0) return 16;
-  return std::max<int64_t>(16, ScoreSpace(rows, vocab, n_tokens, top_k).total);
+  return std::max<int64_t>(16, ScoreSpace::bytes(rows, vocab, n_tokens, top_k));
 }
 
 extern "C" int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* logprob, float* lse,
@@ -641,7 +646,7 @@ extern "C" int ds4moe_logprobs(const void* x, const void* w, const int32_t* toke
 
 extern "C" int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k) {
   if (rows <= 0 || vocab <= 0 || d <= 0 || top_k <= 0) return 16;
-  return std::max<int64_t>(ScoreSpace(rows, vocab, top_k, 0).total,
+  return std::max<int64_t>(ScoreSpace::bytes(rows, vocab, top_k, 0),
                            DistillSpace(rows, d, top_k).total(rows, std::min<int64_t>(distill_piece(rows), up(vocab, kPieceMin))));
 }
 
