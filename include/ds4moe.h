@@ -385,8 +385,8 @@ int ds4moe_logprobs(const void* x, const void* w, const int32_t* tokens, float* 
  *     dw[v] = sum_t dz[t][v] x[t], rounded to dtype. Either may be NULL. dz, the pieces of the vocabulary and what is not
  *     finite are as for ds4moe_cross_entropy_grad.
  * T is not applied to the loss once more (a caller who wants T^2 has it in dloss). workspace: as for the cross entropy;
- * ds4moe_distill_workspace returns the bytes that let either call run at full speed (pieces of 16384 words, and for up to 512
- * rows of as many as take 64 MB, or the vocabulary). The forward takes the rows in blocks as
+ * ds4moe_distill_workspace returns the bytes that let either call of so many rows, or of fewer, run at full speed (pieces of
+ * 16384 words, and for up to 512 rows of as many as take 64 MB, or the vocabulary). The forward takes the rows in blocks as
  * ds4moe_logprobs does; the gradient needs 16 + 4 rows (d + 1 + top_k) + 512 (rows rounded up to 8) and 48 for rounding. */
 int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k);
 int ds4moe_distill(const void* x, const void* w, const int32_t* ids, const float* teacher, float* loss, float* lse,

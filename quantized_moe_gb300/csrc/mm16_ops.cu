@@ -555,8 +555,14 @@ struct DistillSpace {
 // Its pieces of the vocabulary: of up to 512 rows as many words as make 64 MB of dz, which still come from L2 (128 rows, 129280 words,
 // d 2048: 605 us in pieces of 16384, 383 in one; 512 rows, d 1024: 623, 497 in pieces of 32768 to 65536). Beyond, the longer sums of
 // dx, in several accumulators, cost more than fewer launches save (1024 rows, 64000 words, d 1024: 431 us, 505 in halves).
+constexpr int64_t kDistillRows = 512, kDistillDz = (int64_t)1 << 26;
 int64_t distill_piece(int64_t rows) {
-  return rows > 512 ? kPieceMax : std::max<int64_t>(kPieceMax, ((int64_t)1 << 25) / up(rows, 8) / kPieceMin * kPieceMin);
+  return rows > kDistillRows ? kPieceMax : std::max<int64_t>(kPieceMax, kDistillDz / 2 / up(rows, 8) / kPieceMin * kPieceMin);
+}
+// The bytes of dz for which a workspace is made: such a piece of these rows and of any smaller number.
+int64_t distill_dz(int64_t rows, int64_t vocab) {
+  const int64_t words = up(vocab, kPieceMin);
+  return std::max(2 * up(rows, 8) * std::min<int64_t>(kPieceMax, words), std::min(kDistillDz, 2 * std::min(up(rows, 8), kDistillRows) * words));
 }
 
 }  // namespace
@@ -647,7 +653,7 @@ extern "C" int ds4moe_logprobs(const void* x, const void* w, const int32_t* toke
 extern "C" int64_t ds4moe_distill_workspace(int32_t rows, int32_t vocab, int32_t d, int32_t top_k) {
   if (rows <= 0 || vocab <= 0 || d <= 0 || top_k <= 0) return 16;
   return std::max<int64_t>(ScoreSpace::bytes(rows, vocab, top_k, 0),
-                           DistillSpace(rows, d, top_k).total(rows, std::min<int64_t>(distill_piece(rows), up(vocab, kPieceMin))));
+                           DistillSpace(rows, d, top_k).dz + distill_dz(rows, vocab));
 }
 
 extern "C" int ds4moe_distill(const void* x, const void* w, const int32_t* ids, const float* teacher, float* loss,

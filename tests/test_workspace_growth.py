@@ -22,7 +22,8 @@ def test_queries_never_fall(vocab):
     for n, top in itertools.product((0, 1, 4, 5, 100, 256), (0, 1, 8, 64)):
         if top <= vocab:
             assert rising([api.ds4moe_logprobs_workspace(r, vocab, n, top) for r in STEPS]), (n, top)
-    for d in (1, 72, 4096):
+    for d, k in itertools.product((1, 72, 4096), (1, 32, 256)):
+        assert rising([api.ds4moe_distill_workspace(r, vocab, d, k) for r in STEPS]), (d, k)
         assert rising([api.ds4moe_cross_entropy_workspace(r, vocab, d) for r in STEPS]), d
         assert rising([api.ds4moe_linear_grad_workspace(r, vocab, "silu") for r in STEPS])
 
@@ -42,3 +43,13 @@ def test_fewer_rows_are_not_refused(vocab, n, top):
                 with pytest.raises(api.Ds4MoeError) as ei:
                     api.ds4moe_distill(P, P, P, P, P, P, P, rows, vocab, 64, n, workspace=P, workspace_bytes=size_d)
                 assert ei.value.code != api.DS4MOE_ERR_CAPACITY, (most, rows)
+
+
+def test_a_gradient_of_fewer_rows_keeps_its_pieces():
+    """The distillation's gradient takes up to 512 rows in pieces of up to 64 MB: a workspace for more rows holds them."""
+    for vocab in VOCABS:
+        for rows in (8, 100, 264, 512):
+            wide = max(16384, (1 << 25) // ((rows + 7) // 8 * 8) // 256 * 256)
+            piece = 2 * ((rows + 7) // 8 * 8) * min(wide, (vocab + 255) // 256 * 256)
+            for most in (rows, 513, 700, 2000):
+                assert api.ds4moe_distill_workspace(most, vocab, 72, 9) >= piece + 16 + 4 * rows * (72 + 1 + 9)
