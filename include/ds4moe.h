@@ -359,9 +359,8 @@ int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const 
  * all fp32 but the indices, lists without gaps between rows. A place without a token holds -1 and has logprob 0; so has one
  * that lies outside the vocabulary otherwise, which also sets bit 0 of ds4moe_ops_status. lse and entropy may be NULL, the
  * lists where they have no places. A logit of -inf has probability 0; a row with no other has lse -inf, its entropy and
- * log probabilities are NaN. A logit
- * that is NaN makes lse, logprob and entropy of its row NaN and is listed nowhere; places of top_index that this leaves
- * hold -1 and NaN.
+ * log probabilities are NaN. A logit that is NaN makes lse, entropy and the log probabilities of its row NaN and is listed
+ * nowhere; places of top_index that this leaves hold -1 and NaN. One of +inf does the same to its row, but is listed.
  * workspace: 16-byte aligned device memory. ds4moe_logprobs_workspace returns the bytes for all rows at once (with top_k the
  * logits in fp32 are in it), and for any smaller number of rows; a call takes the rows in blocks of a multiple of 128 that its workspace holds, each of
  * which reads W (sums may then be joined in another order), and less than a block of 128 (or all) rows needs returns

@@ -234,6 +234,7 @@ __device__ __forceinline__ int best_of(Team<G>& team, Picks<G>& p, int n, int k,
 
 // Joins the partials (max, sum, spread), whole sets of words each: M = max m_i, S = sum s_i r_i, U = sum (u_i + (m_i - M) s_i) r_i
 // with r_i = exp((m_i - M) / T): lse = M / T + log S, entropy = log S - U / (T S).
+// (A set without a number has m_i = NaN: it adds its sum, 0 or NaN, and is nothing to the search.)
 // The k best words lie in the k tiles with the largest maxima (a word of any other tile has k words ahead of it, one in
 // each of these), and there in the k chunks of 32 words with the largest: three selections of k.
 template <int G>

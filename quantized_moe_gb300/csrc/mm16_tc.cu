@@ -701,6 +701,8 @@ __device__ __forceinline__ float exp2_fast(float v) {
 }
 // Words from nv on are made -inf: they add nothing, and no word's arithmetic hangs on a branch (written with a condition for
 // each word the chunk ran one word after the other, 4.5 thousand cycles where this takes one). Returns the chunk's largest.
+// It and the running maximum m, which starts as NaN, are NaN as long as there is no number: the search for the best words
+// may not take such tiles and chunks for closed words (-inf), which are listed after the open ones.
 template <bool ENT>
 __device__ __forceinline__ float epi_score(float (&v)[32], int nv, float c, float& m, float& s, float& u) {
   if (nv < 32) {
@@ -711,14 +713,15 @@ __device__ __forceinline__ float epi_score(float (&v)[32], int nv, float c, floa
 #pragma unroll
   for (int j = 4; j < 32; ++j) q[j & 3] = fmaxf(q[j & 3], v[j]);
   const float chunk = fmaxf(fmaxf(q[0], q[1]), fmaxf(q[2], q[3])), top = fmaxf(m, chunk);
-  if (top == -INFINITY) {  // only words of probability zero so far (NaN logits still reach the sum)
+  if (!(top > -INFINITY)) {  // only words of probability zero so far, or that are NaN (which still reach the sum)
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < 32; ++j) bad |= v[j] != v[j];
     if (bad) s = NAN;
-    return -INFINITY;
+    m = top;
+    return chunk;
   }
-  const float d = fmaxf(m - top, -1e30f), r = exp2_fast(d * c);  // (m = -inf: s and u are 0, or NaN)
+  const float d = fmaxf(m - top, -1e30f), r = exp2_fast(d * c);  // (m = -inf or NaN: s and u are 0, or NaN)
   float t[4] = {s * r, 0.f, 0.f, 0.f}, w[4] = {(u + d * s) * r, 0.f, 0.f, 0.f};
   m = top;
 #pragma unroll
@@ -1221,7 +1224,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     constexpr bool kScore = EPI == MM_EPI_SCORE || EPI == kEpiScoreOne, kStats = EPI == MM_EPI_STATS || kScore;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
-    float few_m = -INFINITY, few_s = 0.f, few_u = 0.f;  // few tokens: of all the warp's words
+    float few_m = NAN, few_s = 0.f, few_u = 0.f;  // few tokens: of all the warp's words
     Walk<CG> walk;
     for (int t = first; t < tiles; t += step) {
       const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
@@ -1259,7 +1262,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         }
       }
-      float m = -INFINITY, total = 0.f, spread = 0.f;
+      float m = kScore ? NAN : -INFINITY, total = 0.f, spread = 0.f;
       // the listed words of the thread's token: the first one from the tile's start on
       const int2* want = nullptr;
       int want_left = 0, want_next = INT32_MAX;

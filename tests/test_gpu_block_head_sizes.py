@@ -1,12 +1,14 @@
 """GPU: the gated block, the scores and the distillation at the sizes where they change their form: workspaces made for
 more rows, pieces of the vocabulary above 16384 words, selections among words that are not numbers, ragged weight gradients
 on pairs of CTAs, groups on both sides of a tile. Tolerances as in test_gpu_block_head."""
+import math
+
 import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
 from test_gpu_block_head import grid, score, score_check
-from test_gpu_mm16 import gen
+from test_gpu_mm16 import NAN, gen
 
 pytestmark = pytest.mark.gpu
 
@@ -20,4 +22,42 @@ def test_scores_of_fewer_rows_than_the_workspace_was_made_for(vocab, n, top, mos
     score_check(x, w, tokens, top, "bf16", 1.0, got)
     own = score(x, w, tokens, top)
     assert all(torch.equal(got[name], own[name]) for name in own)
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows", [1, 7, 40, 200, 1100])
+@pytest.mark.parametrize("top", [2, 5, 40])
+def test_best_words_among_words_that_are_not_numbers(rows, top):
+    """Whole tiles and chunks of NaN come before closed words (-inf) and a few open ones: the open words are listed first and
+    then the closed ones in their order, as if the others were not there."""
+    vocab, d = 13000, 64
+    x, w = grid((rows, d), "bf16", 1, 16, 2.0 ** -4), grid((vocab, d), "bf16", 2, 20, 2.0 ** -6)
+    x[:, 0] = 1.0
+    w[:, 0] = -math.inf
+    w[:11900] = NAN  # 46 tiles of 256, 371 chunks of 32, and part of the next
+    open_words = [11950, 12345, vocab - 1]
+    w[open_words, 0] = 0.0
+    w[12000:12300] = NAN
+    tokens = torch.zeros((rows, 1), dtype=torch.int32, device="cuda")
+    got = score(x, w, tokens, top)
+    z = x.double() @ w.double().T
+    z = torch.where(torch.arange(vocab, device="cuda") < 11900, NAN, z)
+    number = ~z[0].isnan()
+    places = number.nonzero().flatten()
+    want = places[torch.sort(z[:, number], dim=1, descending=True, stable=True).indices[:, :top]]
+    assert torch.equal(got["top_index"].long(), want)
+    assert bool(got["lse"].isnan().all()) and bool(got["top_logprob"].isnan().all())
+    # fewer words that are numbers than asked for
+    w[:, 0], w[11900:vocab - 1] = NAN, NAN
+    w[vocab - 1] = 1.0
+    got = score(x, w, tokens, top)
+    assert got["top_index"][0].tolist() == [vocab - 1] + [-1] * (top - 1)
+    # a word of infinite logit comes first, and the row has no log probabilities
+    w = grid((vocab, d), "bf16", 2, 20, 2.0 ** -6)
+    w[12345, 0] = math.inf
+    got = score(x, w, tokens, top)
+    assert bool((got["top_index"][:, 0] == 12345).all())
+    z = x.double() @ w.double().T
+    assert torch.equal(got["top_index"].long(), torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top])
+    assert all(bool(got[name].isnan().all()) for name in ("lse", "entropy", "logprob", "top_logprob"))
     assert api.ds4moe_ops_status() == 0
