@@ -340,7 +340,7 @@ int ds4moe_cross_entropy_grad(const void* x, const void* w, const int32_t* label
  *     dx[t] = W_g^T dz[t]                   [rows x k]
  *     dW_g  = sum_t dz[t] x[t]^T            [2n x k] at dw + g * dw_stride; zero for an empty group
  *   dx and dw may each be NULL (w is read only for dx, x only for dw): ds4moe_grouped_mm_dw takes dz where a gradient in
- *   fp32, or added to an older one, is wanted. dz may be z itself, rows as far apart. Where act'(a) is 0 the first part of dz is 0 whatever dh and b hold;
+ *   fp32, or added to an older one, is wanted. dz may be z itself, rows as far apart (else the call is refused). Where act'(a) is 0 the first part of dz is 0 whatever dh and b hold;
  *   act(a) is taken at its limit where a is infinite. rows == 0 writes zeros into dw. */
 int ds4moe_grouped_glu(const void* x, const void* w, const int32_t* offsets, void* h, void* zout, int32_t rows, int32_t n,
                        int32_t k, int32_t n_groups, int32_t act, int32_t dtype, int64_t ldx, int64_t ldw,

@@ -601,6 +601,8 @@ extern "C" int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void
     lddh = c.ld("lddh", lddh, n), ldx = c.ld("ldx", ldx, k), ldw = c.ld("ldw", ldw, k), ldz = c.ld("ldz", ldz, n2);
     lddz = c.ld("lddz", lddz, n2), lddx = c.ld("lddx", lddx, k), lddw = c.ld("lddw", lddw, k);
     w_stride = stride(c, "w_stride", w_stride, n2, ldw), dw_stride = stride(c, "dw_stride", dw_stride, n2, lddw);
+    if (dz && dz == z && rows > 1 && lddz != ldz)  // (a row would be written while another one is read there)
+      c.invalid("dz is z, but lddz=" + std::to_string(lddz) + " is not ldz=" + std::to_string(ldz));
     if (!c.ok()) return c.code;
     block_groups(c, offsets, n_groups);
     c.device();
