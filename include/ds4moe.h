@@ -353,10 +353,11 @@ int ds4moe_grouped_glu_grad(const void* dh, const void* x, const void* w, const 
 /* Scores of the logits z[t] = W x[t] at a temperature T (0.001..1000), x [rows x d], w [vocab x d]:
  *   lse[t]        = log sum_v exp(z[t][v] / T)
  *   logprob[t][j] = z[t][tokens[t][j]] / T - lse[t]          tokens device int32 [rows x n_tokens], n_tokens 0..256
- *   entropy[t]    = -sum_v p log p, p = exp(z[t][v] / T - lse[t])   (absolute error about 1e-6)
+ *   entropy[t]    = -sum_v p log p, p = exp(z[t][v] / T - lse[t])
  *   top_index[t], top_logprob[t]: the top_k words with the largest logits, in order, ties to the lower index
  *                                  (int32 and fp32 [rows x top_k], top_k 0..64 and at most vocab)
- * all fp32 but the indices, lists without gaps between rows. A place without a token holds -1 and has logprob 0; so has one
+ * all fp32 but the indices, lists without gaps between rows. The entropy of exact logits is off by about 1e-6 (1 + entropy); the
+ * logits' own errors (sums of d products in fp32) count 1 / T times in lse and logprob, up to 2 entropy / T times in it. A place without a token holds -1 and has logprob 0; so has one
  * that lies outside the vocabulary otherwise, which also sets bit 0 of ds4moe_ops_status. lse and entropy may be NULL, the
  * lists where they have no places. A logit of -inf has probability 0; a row with no other has lse -inf, its entropy and
  * log probabilities are NaN. A logit that is NaN makes lse, entropy and the log probabilities of its row NaN and is listed

@@ -8,7 +8,7 @@ import torch
 
 from quantized_moe_gb300 import ds4moe as api
 from test_gpu_block_head import grid, score, score_check
-from test_gpu_mm16 import NAN, gen
+from test_gpu_mm16 import NAN, gen, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,22 @@ def test_best_words_among_words_that_are_not_numbers(rows, top):
     assert torch.equal(got["top_index"].long(), torch.sort(z, dim=1, descending=True, stable=True).indices[:, :top])
     assert all(bool(got[name].isnan().all()) for name in ("lse", "entropy", "logprob", "top_logprob"))
     assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,vocab", [(12, 900), (300, 9001), (20, 140000)])
+@pytest.mark.parametrize("t", [1.0, 1e-3, 1e3, 0.3])
+def test_entropy_of_exact_logits(rows, vocab, t):
+    """The logits are exact (whole numbers below 2^24), so that what is left is the sums' and the exponentials' rounding: at
+    most 73 roundings one after the other in each of two sums (chunks of 32 words in four accumulators, the joins), as a
+    random walk of sqrt(146) steps of 2^-24, below 2^-20, twice that allowed for; and the factor 1 / T, whose rounding of up
+    to 2^-23 moves the entropy by the variance of log p as much."""
+    d = 64
+    x, w = grid((rows, d), "bf16", 1, 16, 1.0), grid((vocab, d), "bf16", 2, 20, 1.0)
+    x[rows // 2:] = (x[rows // 2:].float() * 0.01).round().to(x.dtype)  # rows of small logits, with a large entropy
+    tokens = torch.zeros((rows, 1), dtype=torch.int32, device="cuda")
+    got = score(x, w, tokens, 0, temperature=t)["entropy"].double()
+    logp = torch.log_softmax(x.double() @ w.double().T / t, 1)
+    p = logp.exp()
+    want = -torch.where(p > 0, p * logp, 0.0).sum(1)
+    var = torch.where(p > 0, p * (logp + want[:, None]) ** 2, 0.0).sum(1)
+    assert bool(((got - want).abs() <= 2.0 ** -19 * (1 + want) + 2.0 ** -23 * var).all())
