@@ -7,8 +7,8 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_block_head import grid, score, score_check
-from test_gpu_mm16 import NAN, gen, whole
+from test_gpu_block_head import distill_check, distilled, grid, lists, score, score_check
+from test_gpu_mm16 import NAN, gen, normal, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,24 @@ def test_entropy_of_exact_logits(rows, vocab, t):
     want = -torch.where(p > 0, p * logp, 0.0).sum(1)
     var = torch.where(p > 0, p * (logp + want[:, None]) ** 2, 0.0).sum(1)
     assert bool(((got - want).abs() <= 2.0 ** -19 * (1 + want) + 2.0 ** -23 * var).all())
+
+
+@pytest.mark.parametrize("dtype,rows,vocab,d,k,temperature", [
+    ("bf16", 1, 40000, 64, 8, 1.0), ("fp16", 16, 40007, 72, 32, 2.0), ("bf16", 128, 40000, 200, 16, 1.0), ("bf16", 512, 33000, 64, 8, 1.0),
+    ("bf16", 513, 33000, 64, 8, 1.0), ("fp16", 700, 33001, 72, 5, 1.0), ("bf16", 64, 40000, 1024, 8, 1.0), ("bf16", 512, 140000, 64, 8, 0.8),
+    ("bf16", 64, 16000, 1024, 8, 1.0), ("fp16", 512, 16128, 1024, 8, 1.0), ("bf16", 200, 9000, 712, 8, 1.0), ("bf16", 40, 140001, 77, 8, 1.0)])
+def test_distillation_over_long_vocabularies(dtype, rows, vocab, d, k, temperature):
+    """Pieces above 16384 words, several of them, the step from 512 to 513 rows, sums of dx in several accumulators, and over
+    clusters; listed words on both sides of where pieces may end."""
+    x, w = normal((rows, d), dtype, 1), normal((vocab, d), dtype, 2, 2.0 * d ** -0.5)
+    ids, teacher = lists(rows, vocab, k)
+    ends = [e + o for e in (256, 8192, 14592, 16128, 16384, 20224, 32768, 65536) for o in (-1, 0, 1) if e + o < vocab] + [0, vocab - 1]
+    for i, word in enumerate(ends):
+        ids[i % rows, i // rows % k] = word
+    dloss = torch.rand(rows, generator=gen(8), device="cuda") / rows
+    got = distilled(x, w, ids, teacher, dloss, dtype, temperature)
+    distill_check(x, w, ids, teacher, dloss, dtype, temperature, got)
+    # a workspace made for more rows changes nothing
+    again = distilled(x, w, ids, teacher, dloss, dtype, temperature)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert api.ds4moe_ops_status() == 0
