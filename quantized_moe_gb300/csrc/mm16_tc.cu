@@ -1049,8 +1049,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     // cleared in both operands before the MMA reads them (0 * NaN would not vanish). A row is 128 bytes of a box.
     // The warp passes every stage in turn and arrives on its empty barrier too, so that the ring cannot lap it. In a pair
     // the other CTA's full barriers see ragged ends alone, and its cleaner waits for nothing else: neither can lap the other.
-    // The MMA waits for both cleaners (64 groups around 256 rows, 4096 x 4096: 642 us on single CTAs, 566 on pairs; 256 rows
-    // each 499, 455). Their arrival releases nothing: a cleared end is in shared memory once the proxy fence is passed
+    // The MMA waits for both cleaners (64 groups around 256 rows, 4096 x 4096: 642 us on single CTAs, 566 on pairs). Their arrival releases nothing: a cleared end is in shared memory once the proxy fence is passed
     // (with a release at cluster scope 615).
     int s = 0;
     uint32_t ph = 0, cleaned = 0;
@@ -1772,6 +1771,20 @@ Schedule schedule(int64_t lane_tiles, int cols, bool b_red, int groups, int cg, 
   return best;
 }
 
+// Whether a ragged reduction runs on pairs. They halve the operands' way into the SMs, but start 0.8 us later, waste half a
+// pair where the tiles of 128 lanes are odd, and leave half as many units to share few tiles out to. Measured over 759 shapes of 1
+// to 256 groups of 7 to 16384 rows (single CTAs first): 64 groups of 256 rows, 4096 x 4096 510 us, 459, but 256 x 512 8.8, 9.5;
+// 64 of 128 rows, 1000 x 1024 33.8, 31.8, but 512 x 4096 58.0, 61.5; 24 of 64 rows, 2048 x 1024 22.9, 23.8; 64 of 256 rows,
+// 2048 x 264 (three tiles of lanes) 33.4, 35.4; one of 16384 rows, 2048 x 2048 90, 79, 512 x 512 (four tiles) 62.8, 70.3, and
+// 4096 x 1152 (nine) 95, 147. Of the 113 with an even number of tiles that this takes none is slower on pairs.
+bool rag_pairs(const MmProblem& p, int pairs) {
+  const int64_t lanes128 = (p.lanes + BM - 1) / BM, average = p.red / p.groups;
+  const int64_t tiles = (lanes128 + 1) / 2 * ((p.cols + 255) / 256) * p.groups;
+  if (lanes128 % 2 && lanes128 <= 16) return false;
+  if (average >= 192 ? p.lanes <= 256 || p.cols <= 256 : average < 128 || p.lanes <= 512 || p.cols <= 512) return false;
+  return 5 * tiles >= 4 * pairs && tiles * (average + 4 * BK) >= (int64_t)33 * BK * pairs;  // (33 steps of 64 for each pair, with what a tile costs)
+}
+
 }  // namespace
 
 int mm_few_parts(int vocab) {
@@ -1899,9 +1912,9 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
                by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   a.plain = a.rows_out && p.epi == MM_EPI_STORE && (!ep.scale || p.rag == MM_DENSE) && !ep.bias && !ep.z && !ep.residual && !ep.accumulate && ep.act == MM_ACT_NONE;
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
-  // narrow product); of ragged reductions those whose results leave by rows.
+  // narrow product); of ragged reductions those whose results leave by rows and that rag_pairs takes.
   const bool few_tokens = p.epi == MM_EPI_SCORE_FEW;
-  const int cg = !gen && !few_tokens && (p.rag != MM_RAG_RED || a.plain) && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
+  const int cg = !gen && !few_tokens && (p.rag != MM_RAG_RED || (a.plain && rag_pairs(p, pairs))) && lanes > BM && pairs > 0 && a.split == 1 ? 2 : 1;
   const int units = cg == 2 ? pairs : few_tokens ? std::min(sms, kMmFewParts / 4) : sms;
   a.lane_tiles = (lanes + BM * cg - 1) / (BM * cg);
   a.bn = 256;

@@ -8,7 +8,7 @@ import torch
 
 from quantized_moe_gb300 import ds4moe as api
 from test_gpu_block_head import distill_check, distilled, grid, lists, score, score_check
-from test_gpu_mm16 import NAN, gen, normal, whole
+from test_gpu_mm16 import NAN, gen, groups_of, normal, offsets, stream, whole
 
 pytestmark = pytest.mark.gpu
 
@@ -100,4 +100,31 @@ def test_distillation_over_long_vocabularies(dtype, rows, vocab, d, k, temperatu
     # a workspace made for more rows changes nothing
     again = distilled(x, w, ids, teacher, dloss, dtype, temperature)
     assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert api.ds4moe_ops_status() == 0
+
+
+def ragged(groups, average, spread, seed=5):
+    g = torch.Generator().manual_seed(seed)
+    return [max(0, average + int(v)) for v in (torch.randn(groups, generator=g) * spread).round().tolist()]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("counts,n,k", [
+    (ragged(16, 200, 60), 1040, 1024), ([128] * 40, 600, 1000), ([0, 500, 1, 700, 15, 17, 900, 33] * 4, 520, 1280), ([20005, 17, 0, 300], 1040, 1024),
+    ([1, 16384, 16385], 1288, 1024), (ragged(64, 256, 40), 776, 712), (ragged(30, 150, 100), 1024, 2200), ([3000], 4104, 1024)])
+def test_ragged_weight_gradients_on_pairs(dtype, counts, n, k):
+    """Groups with ends that are no multiple of 16, empty and long ones, next to rows that are not finite."""
+    rows, g = sum(counts) + 9, len(counts)
+    dy, x = whole((rows, n), dtype, 1), whole((rows, k), dtype, 2)
+    dy[sum(counts):], x[sum(counts):] = NAN, NAN
+    dw = torch.full((g, n, k), 7.0, dtype=x.dtype, device="cuda")
+    api.ds4moe_grouped_mm_dw(dy, x, offsets(counts), dw, rows, n, k, g, dtype, stream=stream())
+    for e, lo, hi in groups_of(counts):
+        assert torch.equal(dw[e], (dy[lo:hi].double().T @ x[lo:hi].double()).to(dw.dtype)), (e, lo, hi)
+    last = max(e for e, c in enumerate(counts) if c)  # a group's rows stay out of its neighbours'
+    x[sum(counts[:last]) + counts[last] // 2, 3] = math.inf
+    api.ds4moe_grouped_mm_dw(dy, x, offsets(counts), dw, rows, n, k, g, dtype, stream=stream())
+    for e, lo, hi in groups_of(counts):
+        if e != last:
+            assert torch.equal(dw[e], (dy[lo:hi].double().T @ x[lo:hi].double()).to(dw.dtype)), (e, lo, hi)
     assert api.ds4moe_ops_status() == 0
