@@ -64,6 +64,7 @@ __host__ __device__ constexpr bool is_glu(int epi) { return epi == MM_EPI_GLU ||
 __host__ __device__ constexpr bool is_wide(int epi) { return epi == kEpiPlainWide || epi == kEpiGluWide; }
 constexpr int kAccCols = 256;             // columns of one accumulator, the widest MMA
 constexpr int kMaxSpread = 8;             // CTAs of a cluster that share out a tile's reduction and its columns
+constexpr int kRagBox = 32;               // rows of a box where the columns are ragged
 constexpr int kPanel = 8;                 // column tiles that a raster panel spans
 constexpr int kEpiWarps = 8;              // epilogue warps: two per quadrant of tensor-memory lanes
 constexpr int kFirstLoader = 4 + kEpiWarps;
@@ -93,6 +94,7 @@ struct TcArgs {
   int bn, stages, b_box;      // column tile (above kAccCols: tiles that need it take both accumulators), pipeline depth, rows of a column-operand box
   int a_blocks, b_blocks;     // boxes of 64 x 64 that one copy of an MN-major operand brings
   int glu_whole;              // one copy brings a gated block's 64 gate and 64 up rows (else 16 rows each)
+  int ring;                   // bytes of all stages
   int lane_tiles, col_tiles;  // of BM * CG lanes; of bn columns (without ragged columns)
   int rows_out;               // the 16-bit output (and residual, z) can be moved 8 lanes at a time
   int plain;                  // and nothing is to be added (a dense one may be scaled)
@@ -243,6 +245,47 @@ __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[1
       : "memory");
 }
 
+// The columns of the widest tile where tiles may take both accumulators, from the sizes that the groups have: a multiple of 64
+// above kAccCols, up to a.bn, if one tile for each group of so many rows takes less time than tiles of kAccCols, else
+// kAccCols. A wide tile passes over its group's weights once, but nothing overlaps the storing of its results. Time is estimated
+// as the rounds of an average tile and what the largest takes longer, in cycles fitted to 465 shapes of 16 to 128 groups of 171 to
+// 448 rows on average: a step of 64 loads 256 lanes and n columns in 1.1 cycles each, or multiplies them in 2 n (tiles of kAccCols
+// first: 64 groups of 264, 2048 x 4096 346 us, 223; 64 of 0 to 600, 2048 x 768 63, 76). The choice costs 0.2 % on average, wide
+// tiles throughout 2 % for products and 4 % for blocks, none 6 % and 5 %. Both CTAs of a pair come to the same.
+template <bool GLU>
+__device__ __forceinline__ int widest_tile(const TcArgs& a, const int* lo_of, int units, int lane) {
+  int most = 0;
+#pragma unroll 1
+  for (int g = lane; g < a.p.groups; g += 32) {
+    const int n = lo_of[g + 1] - lo_of[g];
+    if (n <= a.bn) most = max(most, n);
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (most <= kAccCols) return kAccCols;
+  const float blocks = (float)((a.p.red + BK - 1) / BK), store = GLU ? 18.f : 6.f;  // (cycles of a column's results)
+  const auto main_loop = [&](float n) { return blocks * fmaxf(1.1f * (2 * BM + n), 2.f * n); };
+  const auto cost = [&](int n) -> unsigned { return n ? (unsigned)(fmaxf(main_loop((float)n), store * (float)n) + 3000.f) : 0u; };
+  const unsigned of_full = cost(kAccCols);
+  unsigned sum[2] = {}, largest[2] = {}, tiles[2] = {};
+#pragma unroll 1
+  for (int g = lane; g < a.p.groups; g += 32) {
+    const unsigned n = (unsigned)max(lo_of[g + 1] - lo_of[g], 0), full = n / kAccCols, rest = n % kAccCols;
+    const unsigned of_rest = cost((int)rest), narrow = full * of_full + of_rest, top = full ? of_full : of_rest, count = full + (rest > 0);
+    const bool one = n > kAccCols && n <= a.bn;
+    const unsigned wide = (unsigned)(main_loop((float)n) + store * (float)n + (GLU ? 3000.f : 4500.f));
+    sum[0] += narrow, tiles[0] += count, largest[0] = max(largest[0], top);
+    sum[1] += one ? wide : narrow, tiles[1] += one ? 1 : count, largest[1] = max(largest[1], one ? wide : top);
+  }
+  float time[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float count = (float)__reduce_add_sync(0xffffffffu, tiles[i]), mean = __fdividef((float)__reduce_add_sync(0xffffffffu, sum[i]), count);
+    const float rounds = ceilf(__fdividef((float)a.lane_tiles * count, (float)units) - 1e-3f);
+    time[i] = (rounds - 1.f) * mean + (float)__reduce_max_sync(0xffffffffu, largest[i]);
+  }
+  return (GLU ? 1.03f : 1.06f) * time[1] < time[0] ? (most + 63) / 64 * 64 : kAccCols;
+}
+
 // One output tile.
 struct Tile {
   int g, l0, c0, n, r0, red;  // group, first lane of the CTA (pair), first column, columns, first of the reduction, its length
@@ -251,11 +294,14 @@ struct Tile {
 // Tables in shared memory: lo[g], g = 0..groups, the first row of each group, clamped to the matrix (a group
 // ends where the next one begins, or is empty if that lies before it); for ragged columns pref[g], the running
 // count of the groups' column tiles.
-template <int CG>
-__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int t, int share) {
+// WIDE: a group of at most `widest` rows has one tile, which beyond kAccCols takes both accumulators; a larger one has tiles of
+// kAccCols, whose accumulators take turns (64 groups of 20 and 400 rows in turn, 2048 x 4096: 222 us, in tiles of 320 and 80
+// columns 300).
+template <int CG, bool WIDE>
+__device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int widest, int t, int share) {
   const MmProblem& p = a.p;
   Tile o;
-  int col_tiles = a.col_tiles, c_lo = 0, c_n = p.cols, part = 0, width = a.bn;
+  int col_tiles = a.col_tiles, c_lo = 0, c_n = p.cols, part = 0, pitch = a.bn, width = a.bn;
   o.g = 0, o.r0 = 0, o.red = p.red;
   if (p.rag == MM_RAG_COLS) {
     const int ct = a.by_lanes.div(t);  // a group takes lane_tiles * its column tiles consecutive tiles
@@ -268,6 +314,7 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
     col_tiles = pref[lo + 1] - pref[lo];
     t -= pref[lo] * a.lane_tiles;
     c_lo = lo_of[lo], c_n = max(lo_of[lo + 1] - c_lo, 0);
+    if (WIDE && c_n > widest) pitch = width = kAccCols;
   } else if (p.rag == MM_RAG_RED) {
     o.g = a.by_matrix.div(t);
     t -= o.g * a.lane_tiles * col_tiles;
@@ -286,8 +333,8 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
   const int w = min(kPanel, col_tiles - panel * kPanel);
   const int lt = w == 1 ? t : w == kPanel ? t / kPanel : t / w, ct = panel * kPanel + t - lt * w;
   o.l0 = lt * BM * CG;
-  o.c0 = c_lo + ct * a.bn + part * width;
-  o.n = min(width, c_n - ct * a.bn - part * width);  // (a part past the last column has none)
+  o.c0 = c_lo + ct * pitch + part * width;
+  o.n = min(width, c_n - ct * pitch - part * width);  // (a part past the last column has none)
   if (CG == 1 && a.split > 1) {  // this CTA's share of the reduction, whole stages
     const int blocks = (o.red + BK - 1) / BK;
     const int b0 = blocks * share / a.split * BK, b1 = blocks * (share + 1) / a.split * BK;
@@ -300,14 +347,14 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
 // The tiles of a warp in turn, every `step`-th one from `first`: tile_of takes a few hundred cycles of dependent
 // arithmetic, so the lanes work out 32 tiles at once and hand them round (weight gradients of 256 experts, 128 rows
 // each, where a tile has two or three stages: 910 -> 857 us with this and the cleaner's stores unrolled).
-template <int CG>
+template <int CG, bool WIDE>
 struct Walk {
   Tile mine;
   int i = 31;
-  __device__ __forceinline__ Tile next(const TcArgs& a, const int* lo_of, const int* pref, int t, int step, int tiles, int share, int lane) {
+  __device__ __forceinline__ Tile next(const TcArgs& a, const int* lo_of, const int* pref, int widest, int t, int step, int tiles, int share, int lane) {
     if (++i == 32) {
       i = 0;
-      mine = tile_of<CG>(a, lo_of, pref, min(t + lane * step, tiles - 1), share);
+      mine = tile_of<CG, WIDE>(a, lo_of, pref, widest, min(t + lane * step, tiles - 1), share);
     }
     Tile o;
     o.g = __shfl_sync(0xffffffffu, mine.g, i);
@@ -791,8 +838,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   const MmProblem& p = a.p;
   // the stages start on a 1024-byte boundary (the swizzle's period); in a pair both CTAs have the same layout
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  const int stage_bytes = A_BYTES + a.bn / CG * BK * 2;
-  uint8_t* out_stage = smem + a.stages * stage_bytes;  // [2][kOutBytes]
+  int stages = a.stages, stage_bytes = A_BYTES + a.bn / CG * BK * 2;
+  uint8_t* out_stage = smem + a.ring;  // [2][kOutBytes]
   float* parts = reinterpret_cast<float*>(out_stage + 2 * kOutBytes);  // [split - 1][bn][kPartLd], in the cluster's first CTA
   uint8_t* ctrl = out_stage + 2 * kOutBytes + (a.spread ? 0 : (a.split - 1) * a.bn * kPartLd * 4);
   uint64_t* full = reinterpret_cast<uint64_t*>(ctrl);
@@ -802,6 +849,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   uint64_t* clean = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(clean + kMaxStages);
   volatile int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  int* widest_slot = reinterpret_cast<int*>(tmem_slot + 2);
   int* lo_of = reinterpret_cast<int*>(tmem_slot + 4);
   int* pref = lo_of + p.groups + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -813,7 +861,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   while (tmem_cols < 2u * acc_stride) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < a.stages; ++i) {
+    for (int i = 0; i < (kWide ? kMaxStages : a.stages); ++i) {
       mbar_init(full + i, GEN ? kLoaders : 1);
       mbar_init(empty + i, !GEN && p.rag == MM_RAG_RED && rank == 0 ? 2 : 1);  // the MMAs' commit, and the cleaner
       mbar_init(clean + i, CG);
@@ -839,10 +887,15 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     for (int g = threadIdx.x; g <= p.groups; g += blockDim.x) lo_of[g] = min(max(*(p.offsets + g), 0), total);
     __syncthreads();
     if (p.rag == MM_RAG_COLS && warp == 2) {
-      int run = 0;
+      int run = 0, most = a.bn;
+      if (kWide) {
+        most = widest_tile<is_glu(EPI)>(a, lo_of, gridDim.x / CG, lane);
+        if (lane == 0) *widest_slot = most;
+      }
       for (int g0 = 0; g0 <= p.groups; g0 += 32) {
         const int g = g0 + lane;
-        const int n = g < p.groups ? (max(lo_of[g + 1] - lo_of[g], 0) + a.bn - 1) / a.bn : 0;
+        const int rows = g < p.groups ? max(lo_of[g + 1] - lo_of[g], 0) : 0;
+        const int n = kWide ? rows > most ? (rows + kAccCols - 1) / kAccCols : rows > 0 : (rows + a.bn - 1) / a.bn;
         int inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -859,6 +912,11 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const int widest = kWide ? *widest_slot : a.bn;
+  if (kWide) {  // the ring has as many stages as these tiles leave room for
+    stage_bytes = A_BYTES + widest / CG * BK * 2;
+    stages = min(kMaxStages, a.ring / stage_bytes);
+  }
   int tiles = a.lane_tiles * (p.rag == MM_RAG_COLS ? pref[p.groups] : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
   if (p.rag == MM_DENSE) tiles += (tiles - a.tail_from) * ((1 << a.tail_lg) - 1);
   const int share = CG == 2 ? 2 : a.split;  // CTAs that work on the same tile
@@ -875,16 +933,21 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     const int a_boxes = is_glu(EPI) ? (a.glu_whole ? 1 : BM / 16) : a_red ? 1 : 2 / a.a_blocks;
-    Walk<CG> walk;
+    Walk<CG, kWide> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
+      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const bool wide = kWide && o.n > kAccCols;
       const int nb = mma_n<CG>(p, wide ? o.n - kAccCols : o.n) / CG;  // columns that this CTA stages (of the second part)
-      const int b_boxes = kWide && wide ? kAccCols / CG / a.b_box + (nb + a.b_box - 1) / a.b_box : b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
-      const int b_box_bytes = b_red ? a.b_box * 128 : a.b_blocks * 8192;
+      const int b_boxes = kWide ? (wide ? kAccCols / CG / kRagBox : 0) + (nb + kRagBox - 1) / kRagBox :
+                          b_red ? (nb + a.b_box - 1) / a.b_box : (nb / 64 + a.b_blocks - 1) / a.b_blocks;
+      const int b_box_bytes = kWide ? kRagBox * 128 : b_red ? a.b_box * 128 : a.b_blocks * 8192;
       const uint32_t bytes = A_BYTES + b_boxes * b_box_bytes;
       const int la = o.l0 + BM * rank, cb = o.c0 + nb * rank;
+      // The lane's box: of a wide tile the first part's columns, split between the CTAs, and then the second's. (Worked out for
+      // every stage it slowed narrow tiles too: 16 groups of 200 rows, 2048 x 768 15.4 us, 14.1.)
+      int y_wide = cb + lane * kRagBox;
+      if (kWide && wide) y_wide += lane < kAccCols / CG / kRagBox ? (kAccCols / CG - nb) * (int)rank : kAccCols - kAccCols / CG;
       const int ga = p.rag == MM_RAG_COLS ? o.g : 0;
       for (int k = 0; k < o.red; k += BK) {
         ok = __all_sync(0xffffffffu, mbar_wait(empty + s, ph ^ 1, abort_flag, p.err, 1));
@@ -914,17 +977,16 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           }
         } else if (lane < b_boxes) {
           const uint32_t to = st + A_BYTES + lane * b_box_bytes;
-          if (kWide && wide) {
-            const int c = lane * a.b_box, first_part = kAccCols / CG;  // of the CTA's columns
-            tma_load<CG>(to, &tb, r, c < first_part ? o.c0 + first_part * rank + c : cb + kAccCols - first_part + c, 0, 0, bar);
-          } else if (b_red)
+          if (kWide)
+            tma_load<CG>(to, &tb, r, y_wide, 0, 0, bar);
+          else if (b_red)
             tma_load<CG>(to, &tb, r, cb + lane * a.b_box, 0, 0, bar);
           else if (a.b_blocks > 1)
             load(to, &tb, 0, r, cb / 64 + lane * a.b_blocks, 0, bar);
           else
             load(to, &tb, cb + 64 * lane, r, 0, 0, bar);
         }
-        if (++s == a.stages) s = 0, ph ^= 1;
+        if (++s == stages) s = 0, ph ^= 1;
       }
     }
   } else if (GEN && warp >= kFirstLoader) {
@@ -933,9 +995,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     const int tid = threadIdx.x - kThreads;
-    Walk<CG> walk;
+    Walk<CG, kWide> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
+      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const int nb = mma_n<CG>(p, o.n);
@@ -964,7 +1026,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(full + s);
-        if (++s == a.stages) s = 0, ph ^= 1;
+        if (++s == stages) s = 0, ph ^= 1;
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -977,7 +1039,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const uint64_t a_desc = op_desc(su32(smem), p.a.red_major), b_desc = op_desc(su32(smem + A_BYTES), p.b.red_major);
       const uint32_t type = p.f16 ? 0u : 1u;
       for (int t = first; t < tiles && ok; t += step) {
-        const Tile o = tile_of<CG>(a, lo_of, pref, t, part);
+        const Tile o = tile_of<CG, kWide>(a, lo_of, pref, widest, t, part);
         if (o.red <= 0 || o.n <= 0) continue;  // an empty sum: the epilogue writes zeros without an accumulator
         const bool wide = kWide && o.n > kAccCols;
         const int n = wide ? kAccCols : mma_n<CG>(p, o.n);
@@ -1023,7 +1085,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             for (int i = 0; 16 * i < left; ++i) mma<CG>(d, da + i * a_step, db + i * b_step, idesc, in_seg | i);
           }
           commit<CG>(empty + s);
-          if (++s == a.stages) s = 0, ph ^= 1;
+          if (++s == stages) s = 0, ph ^= 1;
           in_seg += BK;
           if (in_seg == a.seg || k + BK >= o.red) {
             if (kWide && wide) {  // (its reduction fits one accumulator: mm_launch)
@@ -1054,13 +1116,13 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int s = 0;
     uint32_t ph = 0, cleaned = 0;
     bool ok = true;
-    Walk<CG> walk;
+    Walk<CG, kWide> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
+      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       for (int k = 0; k < o.red; k += BK) {
         const int left = min(BK, o.red - k);
         if (CG == 2 && rank && !(left & 15)) {
-          if (++s == a.stages) s = 0;
+          if (++s == stages) s = 0;
           continue;
         }
         ok = __all_sync(0xffffffffu, mbar_wait(full + s, CG == 2 && rank ? cleaned >> s & 1 : ph, abort_flag, p.err, 2));
@@ -1086,7 +1148,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             mbar_arrive(empty + s);
           }
         }
-        if (++s == a.stages) s = 0, ph ^= 1;
+        if (++s == stages) s = 0, ph ^= 1;
       }
     }
   } else if (is_plain(EPI) && warp >= 4 && warp < kFirstLoader) {
@@ -1096,9 +1158,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     const int64_t ld = p.e.ld;
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
-    Walk<CG> walk;
+    Walk<CG, kWide> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
+      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const bool sum = o.red > 0;
       const int l = o.l0 + BM * rank + 8 * piece;
@@ -1224,9 +1286,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     int buf = 0;
     uint32_t used = 0;  // as the MMA counts them
     float few_m = NAN, few_s = 0.f, few_u = 0.f;  // few tokens: of all the warp's words
-    Walk<CG> walk;
+    Walk<CG, kWide> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, t, step, tiles, part, lane);
+      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
@@ -1694,7 +1756,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const TcArgs& a
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(GEN ? kThreads + 32 * kLoaders : kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, a.stages, a.spread ? 1 : a.split, a.p);
+  cfg.dynamicSmemBytes = smem_bytes(CG, a.bn, 0, a.spread ? 1 : a.split, a.p) + a.ring;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1932,7 +1994,7 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
     const int64_t average = ((int64_t)p.cols + p.groups - 1) / p.groups, typical = std::min<int64_t>(2 * average, p.cols);
     while (a.bn > 64 && a.bn / 2 >= typical) a.bn /= 2;
     // Groups around 256 rows: those above would pass over their weights once more for a few rows (64 groups of 264, 4096 x
-    // 4096: 677 us, 462 in one pass). Where there are tiles for every pair of SMs, the tile holds half as much again as the average.
+    // 4096: 677 us, 462 in one pass). Where there are tiles for every pair of SMs, the tile may hold half as much again as the average (widest_tile).
     if (cg == 2 && p.red <= kSegFold && p.b.red_major && (a.plain || p.epi == MM_EPI_GLU) && 3 * average > 2 * kAccCols &&
         average <= 448 && a.lane_tiles * (int64_t)std::min(p.groups, p.cols) >= units)
       a.bn = (int)std::min<int64_t>(2 * kAccCols, (3 * average / 2 + 63) / 64 * 64);
@@ -1944,13 +2006,15 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   }
   a.stages = 1;
   while (a.stages < kMaxStages && smem_bytes(cg, a.bn, a.stages + 1, a.spread ? 1 : a.split, p) <= kSmemMax) ++a.stages;
+  const int room = kSmemMax - smem_bytes(cg, a.bn, 0, a.spread ? 1 : a.split, p);
+  a.ring = a.bn > kAccCols ? room / 1024 * 1024 : a.stages * (A_BYTES + a.bn / cg * BK * 2);
   // the rows of a copy divide what a CTA stages; large copies where the columns are not ragged (4096^3 with copies of
   // 128 rows 81.7 us, of 64 rows 83.8)
   const int staged = a.bn / cg;
-  a.b_box = p.rag == MM_RAG_COLS || staged % 64 ? 32 : staged % 128 ? 64 : 128;
+  a.b_box = p.rag == MM_RAG_COLS || staged % 64 ? kRagBox : staged % 128 ? 64 : 128;
   a.a_blocks = !p.a.red_major && p.lanes % 64 == 0 ? 2 : 1;
   a.b_blocks = !p.b.red_major && p.cols % 64 == 0 && (staged == 256 || staged == 128) ? staged / 64 : 1;
-  a.col_tiles = (p.cols + a.bn - 1) / a.bn;
+  a.col_tiles = (p.cols + std::min(a.bn, kAccCols) - 1) / std::min(a.bn, kAccCols);
   const int64_t tiles = a.lane_tiles * (int64_t)(p.rag == MM_RAG_COLS ? a.col_tiles + p.groups : a.col_tiles) * (p.rag == MM_RAG_RED ? p.groups : 1);
   if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
   if (a.tail_lg == 0) a.tail_from = (int)tiles;

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from quantized_moe_gb300 import ds4moe as api
-from test_gpu_block_head import distill_check, distilled, grid, lists, score, score_check
+from test_gpu_block_head import block, distill_check, distilled, grid, lists, score, score_check
 from test_gpu_mm16 import NAN, gen, groups_of, normal, offsets, stream, whole
 
 pytestmark = pytest.mark.gpu
@@ -127,4 +127,25 @@ def test_ragged_weight_gradients_on_pairs(dtype, counts, n, k):
     for e, lo, hi in groups_of(counts):
         if e != last:
             assert torch.equal(dw[e], (dy[lo:hi].double().T @ x[lo:hi].double()).to(dw.dtype)), (e, lo, hi)
+    assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("counts", [[20, 400] * 8, [10, 0, 30, 900, 5, 1500, 300, 256], [257] * 8, [256] * 8, [200] * 8, [320, 321, 384, 385, 0, 448, 1, 255],
+                                    [2000] + [30] * 9, [448, 449, 512, 447, 500, 433, 434, 441], [700, 1, 1, 1]])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_groups_beside_wide_tiles(dtype, counts):
+    """Groups that fit a tile of both accumulators, and that do not, in every mixture: blocks and both products."""
+    rows, g, n, k = sum(counts) + 3, len(counts), 2568, 264
+    x, w = whole((rows, k), dtype, 1), whole((g, 2 * n, k), dtype, 2)
+    x[sum(counts):] = NAN
+    off = offsets(counts)
+    h, z, clean = block(x, w, off, n, "relu", dtype)
+    y, dx = (torch.full((rows, 2 * n), 7.0, dtype=x.dtype, device="cuda") for _ in range(2))
+    api.ds4moe_grouped_mm(x, w, off, y, rows, 2 * n, k, g, dtype, stream=stream())
+    api.ds4moe_grouped_mm_dx(x, w.transpose(1, 2).contiguous(), off, dx, rows, k, 2 * n, g, dtype, stream=stream())
+    assert clean and torch.equal(z, y) and torch.equal(z, dx) and bool((y[sum(counts):] == 7.0).all()) and bool((h[sum(counts):] == 7.0).all())
+    for e, lo, hi in groups_of(counts):
+        ref = x[lo:hi].double() @ w[e].double().T
+        assert torch.equal(z[lo:hi], ref.to(z.dtype)), e
+        assert torch.equal(h[lo:hi], (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype)), e
     assert api.ds4moe_ops_status() == 0
