@@ -31,7 +31,8 @@ enum MmRag : int {
 enum MmEpi : int {
   MM_EPI_STORE = 0,     // out = act(v + bias) + residual, or v * scale + what is there
   MM_EPI_STATS = 1,     // per lane: max and sum of exponentials over the tile's columns; the label's value
-  MM_EPI_SOFTGRAD = 2,  // out = (exp(v / T - lse) - [column is the label]) * g
+  MM_EPI_SOFTGRAD = 2,  // out = (exp(v / T - lse) - [column is the label]) * g; its rows have room for whole, aligned pieces of
+                        // eight, and the lanes behind the last token get zeros
   MM_EPI_GLU = 3,       // out = act(gate) * up; lanes are the features of out, A has twice as many rows
   MM_EPI_SCORE = 4,     // per lane: as STATS of v / T, and the entropy's sum; the logits of listed words; the logits
   MM_EPI_SCORE_FEW = 5  // the same of few tokens: lanes are words, columns (up to kMmFewRows) tokens, a tile 32 words

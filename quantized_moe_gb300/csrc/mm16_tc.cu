@@ -1293,7 +1293,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
       // what the tile needs besides its sums is fetched before they are waited for
-      const bool by_rows = !kStats && EPI != MM_EPI_SCORE_FEW && a.rows_out;
+      const bool by_rows = EPI == MM_EPI_SOFTGRAD || (!kStats && EPI != MM_EPI_SCORE_FEW && a.rows_out);
       const int64_t group_out = p.rag == MM_RAG_RED ? o.g * e.group_stride : 0;
       const void* add = e.accumulate ? e.out : e.residual;
       const int64_t add_ld = e.accumulate ? e.ld : e.ldr;
@@ -1634,14 +1634,9 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             const int nv = min(32, o.n - c);
             if (is_glu(EPI)) {
               glu_out(p, l, o.c0 + c, nv, v);
-            } else if (is_store(EPI)) {
+            } else {
               epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
               put(p, o.g, l, o.c0 + c, nv, v);
-            } else {
-              const int at = lab[0] - (o.c0 + c);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = gw[0] == 0.f ? 0.f : (__expf(v[j] * e.inv_t - lse[0]) - (j == at ? 1.f : 0.f)) * gw[0];
-              put(p, 0, l, o.c0 + c, nv, v);
             }
           }
         }
@@ -1775,7 +1770,7 @@ cudaError_t launch_epi(const CUtensorMap& ta, const CUtensorMap& tb, const TcArg
   switch (a.p.epi) {
     case MM_EPI_STATS: return launch<CG, MM_EPI_STATS, GEN>(ta, tb, a, grid, s);
     case MM_EPI_SOFTGRAD:
-      if (!GEN && a.rows_out && !a.p.e.labels) return launch<CG, kEpiPlainSoft, false>(ta, tb, a, grid, s);
+      if (!GEN && !a.p.e.labels) return launch<CG, kEpiPlainSoft, false>(ta, tb, a, grid, s);
       return launch<CG, MM_EPI_SOFTGRAD, GEN>(ta, tb, a, grid, s);
     case MM_EPI_GLU:
       if (a.bn > kAccCols) return CG == 2 && !GEN ? launch<2, kEpiGluWide, false>(ta, tb, a, grid, s) : cudaErrorInvalidValue;
@@ -1968,9 +1963,8 @@ cudaError_t mm_launch(const MmProblem& p, cudaStream_t s) {
   }
   const MmEpiArgs& ep = p.e;
   const auto by_rows = [](const void* base, int64_t ld) { return !base || ((uintptr_t)base % 16 == 0 && ld % 8 == 0); };
-  // (dz of a softmax loss has room for whole pieces: the lanes behind the last token get zeros)
-  const bool pieces = p.lanes % 8 == 0 || (p.epi == MM_EPI_SOFTGRAD && ep.ld >= (p.lanes + 7) / 8 * 8);
-  a.rows_out = !ep.out_f32 && !ep.acc_in && pieces && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
+  // (dz of a softmax loss always leaves by rows, see MM_EPI_SOFTGRAD)
+  a.rows_out = !ep.out_f32 && !ep.acc_in && p.lanes % 8 == 0 && ep.group_stride % 8 == 0 && by_rows(ep.out, ep.ld) &&
                by_rows(ep.residual, ep.ldr) && by_rows(ep.z, ep.ldz);
   a.plain = a.rows_out && p.epi == MM_EPI_STORE && (!ep.scale || p.rag == MM_DENSE) && !ep.bias && !ep.z && !ep.residual && !ep.accumulate && ep.act == MM_ACT_NONE;
   // Pairs where there are at least two 128-lane tiles (a half-empty pair would double the work of a
