@@ -237,6 +237,13 @@ __device__ __forceinline__ void tmem_get16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[32]) { tmem_ld32(taddr, v); }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  tmem_get16(taddr, r);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
@@ -346,7 +353,8 @@ __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const
 
 // The tiles of a warp in turn, every `step`-th one from `first`: tile_of takes a few hundred cycles of dependent
 // arithmetic, so the lanes work out 32 tiles at once and hand them round (weight gradients of 256 experts, 128 rows
-// each, where a tile has two or three stages: 910 -> 857 us with this and the cleaner's stores unrolled).
+// each, where a tile has two or three stages: 910 -> 857 us with this and the cleaner's stores unrolled). The unaligned form
+// does without: its threads have 72 registers, and the seven that a Walk holds spilled (2048 x 4096 x 513: 48 us, 46).
 template <int CG, bool WIDE>
 struct Walk {
   Tile mine;
@@ -471,10 +479,11 @@ __device__ __forceinline__ void fold_acc(uint32_t acc, uint32_t sum, bool first,
   tmem_st_wait();
 }
 
-// 32 elements of one lane, nv of them there, `ld` apart: the type is chosen once for all of them.
-__device__ __forceinline__ void to16(const float (&v)[32], uint16_t (&h)[32], int f16) {
+// N elements of one lane, nv of them there, `ld` apart: the type is chosen once for all of them.
+template <int N>
+__device__ __forceinline__ void to16(const float (&v)[N], uint16_t (&h)[N], int f16) {
 #pragma unroll
-  for (int j = 0; j < 32; j += 2) {
+  for (int j = 0; j < N; j += 2) {
     uint32_t u;
     if (f16) {
       const __half2 t = __floats2half2_rn(v[j], v[j + 1]);
@@ -486,88 +495,108 @@ __device__ __forceinline__ void to16(const float (&v)[32], uint16_t (&h)[32], in
     h[j] = (uint16_t)u, h[j + 1] = (uint16_t)(u >> 16);
   }
 }
-template <class T>
-__device__ __forceinline__ void store_col(T* q, int64_t ld, int nv, const T (&h)[32]) {
-  if (nv >= 32) {
+template <class T, int N>
+__device__ __forceinline__ void store_col(T* q, int64_t ld, int nv, const T (&h)[N]) {
+  if (nv >= N) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j, q += ld) *q = h[j];
+    for (int j = 0; j < N; ++j, q += ld) *q = h[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j, q += ld)
+    for (int j = 0; j < N; ++j, q += ld)
       if (j < nv) *q = h[j];
   }
 }
-template <class T>
-__device__ __forceinline__ void load_col(const T* q, int64_t ld, int nv, T (&h)[32]) {
-  if (nv >= 32) {
+template <class T, int N>
+__device__ __forceinline__ void load_col(const T* q, int64_t ld, int nv, T (&h)[N]) {
+  if (nv >= N) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j, q += ld) h[j] = *q;
+    for (int j = 0; j < N; ++j, q += ld) h[j] = *q;
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j, q += ld) h[j] = j < nv ? *q : T(0);
+    for (int j = 0; j < N; ++j, q += ld) h[j] = j < nv ? *q : T(0);
   }
 }
-__device__ __forceinline__ void add16(float (&v)[32], const void* base, int64_t at, int64_t ld, int nv, int f16) {
-  uint16_t h[32];
+template <int N>
+__device__ __forceinline__ void add16(float (&v)[N], const void* base, int64_t at, int64_t ld, int nv, int f16) {
+  uint16_t h[N];
   load_col(static_cast<const uint16_t*>(base) + at, ld, nv, h);
   if (f16) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += __half2float(__ushort_as_half(h[j]));
+    for (int j = 0; j < N; ++j) v[j] += __half2float(__ushort_as_half(h[j]));
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += __uint_as_float((uint32_t)h[j] << 16);
+    for (int j = 0; j < N; ++j) v[j] += __uint_as_float((uint32_t)h[j] << 16);
   }
 }
-__device__ __forceinline__ void add32(float (&v)[32], const float* q, int64_t ld, int nv) {
-  float h[32];
+template <int N>
+__device__ __forceinline__ void add32(float (&v)[N], const float* q, int64_t ld, int nv) {
+  float h[N];
   load_col(q, ld, nv, h);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] += h[j];
+  for (int j = 0; j < N; ++j) v[j] += h[j];
 }
 
-// Writes 32 columns (nv exist for this lane) of lane l.
-__device__ __forceinline__ void put(const MmProblem& p, int g, int l, int c, int nv, const float (&v)[32]) {
+// Writes N columns (nv exist for this lane) of lane l.
+template <int N>
+__device__ __forceinline__ void put(const MmProblem& p, int g, int l, int c, int nv, const float (&v)[N]) {
   const MmEpiArgs& e = p.e;
   if (l >= p.lanes) return;
   const int64_t o = (p.rag == MM_RAG_RED ? g * e.group_stride : 0) + (int64_t)c * e.ld + l;
   if (e.out_f32) {
     store_col(static_cast<float*>(e.out) + o, e.ld, nv, v);
   } else {
-    uint16_t h[32];
+    uint16_t h[N];
     to16(v, h, p.f16);
     store_col(static_cast<uint16_t*>(e.out) + o, e.ld, nv, h);
   }
 }
 
-// The arithmetic of a stored result: 32 columns (nv exist for this lane) of lane l.
-__device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int c, int nv, bool accumulate, float (&v)[32]) {
+// What `out` holds of N columns (nv exist) of lane l.
+template <int N>
+__device__ __forceinline__ void epi_fetch(const MmProblem& p, int g, int l, int c, int nv, uint32_t (&w)[N]) {
+  const MmEpiArgs& e = p.e;
+  if (l >= p.lanes) nv = 0;
+  const int64_t at = (p.rag == MM_RAG_RED ? g * e.group_stride : 0) + (int64_t)c * e.ld + l;
+  if (e.out_f32) {
+    load_col(static_cast<const uint32_t*>(e.out) + at, e.ld, nv, w);
+  } else {
+    uint16_t h[N];
+    load_col(static_cast<const uint16_t*>(e.out) + at, e.ld, nv, h);
+#pragma unroll
+    for (int j = 0; j < N; ++j) w[j] = h[j];
+  }
+}
+
+// The arithmetic of a stored result: N columns (nv exist for this lane) of lane l.
+template <int N>
+__device__ __forceinline__ void epi_store(const MmProblem& p, int g, int l, int c, int nv, bool accumulate, float (&v)[N]) {
   const MmEpiArgs& e = p.e;
   if (l >= p.lanes) nv = 0;
   if (e.acc_in) add32(v, e.acc_in + (int64_t)c * e.acc_ld + l, e.acc_ld, nv);
   if (e.scale) {
     const float s = *e.scale;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] *= s;
+    for (int j = 0; j < N; ++j) v[j] *= s;
   }
   if (e.bias) {
     const float b = nv ? ld16(e.bias, l, p.f16) : 0.f;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] += b;
+    for (int j = 0; j < N; ++j) v[j] += b;
   }
   if (e.z) {
-    uint16_t h[32];
+    uint16_t h[N];
     to16(v, h, p.f16);
     store_col(static_cast<uint16_t*>(e.z) + (int64_t)c * e.ldz + l, e.ldz, nv, h);
   }
   if (e.act == MM_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_silu(v[j]);
+    for (int j = 0; j < N; ++j) v[j] = mm_silu(v[j]);
   } else if (e.act == MM_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_gelu(v[j]);
+    for (int j = 0; j < N; ++j) v[j] = mm_gelu(v[j]);
   } else if (e.act == MM_ACT_RELU) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = mm_relu(v[j]);
+    for (int j = 0; j < N; ++j) v[j] = mm_relu(v[j]);
   }
   if (e.residual) add16(v, e.residual, (int64_t)c * e.ldr + l, e.ldr, nv, p.f16);
   if (accumulate) {
@@ -598,9 +627,24 @@ __device__ __forceinline__ void glu_out(const MmProblem& p, int l, int c, int nv
 // ---- 16-bit results by rows: the warps hold 32 lanes x 32 columns as fragments (a thread: lanes i/4 + 8 r, columns
 // 8 j + 2 (i % 4) and the next), which stmatrix writes transposed into shared memory, from where whole rows of 128
 // lanes leave as 16-byte stores.
-struct Frag {
-  float v[4][4][2];  // [block of 8 columns][block of 8 lanes][column parity]
+template <int J>
+struct FragOf {
+  float v[J][4][2];  // [block of 8 columns][block of 8 lanes][column parity]
 };
+using Frag = FragOf<4>;
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, FragOf<2>& f) {  // (16 columns)
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%16];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%8, %9, %10, %11, %12, %13, %14, %15}, [%17];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr), "r"(taddr + (16u << 16))
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) f.v[(i >> 2) & 1][2 * (i >> 3) + ((i >> 1) & 1)][i & 1] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, Frag& f) {
   uint32_t r[32];
   asm volatile(
@@ -628,10 +672,11 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, int f16) {
 __device__ __forceinline__ uint32_t frag_addr(uint32_t stage, int quad, int j, int lane) {
   return stage + (uint32_t)((8 * j + (lane & 7)) * kRowBytes + quad * 64 + (lane >> 3) * 16);
 }
-__device__ __forceinline__ void frag_out(uint32_t stage, int quad, int lane, const Frag& f, int f16) {
+template <int J>
+__device__ __forceinline__ void frag_out(uint32_t stage, int quad, int lane, const FragOf<J>& f, int f16, int j0 = 0) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(frag_addr(stage, quad, j, lane)),
+  for (int j = 0; j < J; ++j)
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(frag_addr(stage, quad, j0 + j, lane)),
                  "r"(pack16(f.v[j][0][0], f.v[j][0][1], f16)), "r"(pack16(f.v[j][1][0], f.v[j][1][1], f16)),
                  "r"(pack16(f.v[j][2][0], f.v[j][2][1], f16)), "r"(pack16(f.v[j][3][0], f.v[j][3][1], f16))
                  : "memory");
@@ -674,13 +719,14 @@ __device__ __forceinline__ void glu_frag_out_h(uint32_t stage, int quad, int lan
                  "r"(pack16(f.v[j + 1][0][0], f.v[j + 1][0][1], f16)), "r"(pack16(f.v[j + 1][1][0], f.v[j + 1][1][1], f16))
                  : "memory");
 }
-__device__ __forceinline__ void frag_add(uint32_t stage, int quad, int lane, Frag& f, int f16) {
+template <int J>
+__device__ __forceinline__ void frag_add(uint32_t stage, int quad, int lane, FragOf<J>& f, int f16, int j0) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < J; ++j) {
     uint32_t r[4];
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(frag_addr(stage, quad, j, lane))
+                 : "r"(frag_addr(stage, quad, j0 + j, lane))
                  : "memory");
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -995,9 +1041,8 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t ph = 0;
     bool ok = true;
     const int tid = threadIdx.x - kThreads;
-    Walk<CG, kWide> walk;
     for (int t = first; t < tiles && ok; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
+      const Tile o = tile_of<CG, kWide>(a, lo_of, pref, widest, t, part);
       if (o.n <= 0) continue;
       const uint16_t* pa = static_cast<const uint16_t*>(p.a.p) + (p.rag == MM_RAG_COLS ? o.g * p.a.group_stride : 0);
       const int nb = mma_n<CG>(p, o.n);
@@ -1160,7 +1205,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     uint32_t used = 0;  // as the MMA counts them
     Walk<CG, kWide> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
+      const Tile o = GEN ? tile_of<CG, kWide>(a, lo_of, pref, widest, t, part) : walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const bool sum = o.red > 0;
       const int l = o.l0 + BM * rank + 8 * piece;
@@ -1278,6 +1323,10 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     }
     const int c_first = 32 * half, c_step = 64;
     constexpr bool kSpread = EPI == kEpiSpread;
+    // Columns that a thread holds of a stored result. In the unaligned form it has 72 registers: with 32 columns, what is added
+    // and the bias fetched ahead and a Walk it spilled 648 bytes (2048 x 4096 x 101 with bias, gelu and kept z 48 us, now 36; dW of
+    // 24 groups, 8 rows, n 2000, k 711, added to an older one in fp32 137, now 90).
+    constexpr int kPieces = GEN && is_store(EPI) ? 16 : 32;
     const auto part_of = [&](int k, int c) -> const float* {  // the k-th other CTA's sums of columns c to c + 31
       if (kSpread) return reinterpret_cast<const float*>(smem) + ((k - 1) * a.spread + (c >> 5) / a.split * 32) * kPartLd;
       return parts + ((k - 1) * a.bn + c) * kPartLd;
@@ -1288,7 +1337,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     float few_m = NAN, few_s = 0.f, few_u = 0.f;  // few tokens: of all the warp's words
     Walk<CG, kWide> walk;
     for (int t = first; t < tiles; t += step) {
-      const Tile o = walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
+      const Tile o = GEN ? tile_of<CG, kWide>(a, lo_of, pref, widest, t, part) : walk.next(a, lo_of, pref, widest, t, step, tiles, part, lane);
       if (o.n <= 0) continue;
       const int l0 = o.l0 + BM * rank;
       const bool sum = o.red > 0;
@@ -1302,7 +1351,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
       int64_t add_at = (e.accumulate ? group_out : 0) + first_row * add_ld + piece;
       uint4 next[4];
       rows.live = piece < p.lanes;
-      if (by_rows && add && part == 0) rows.load(add, add_at, add_ld, o.n - c_first, next);
+      if (!GEN && by_rows && add && part == 0) rows.load(add, add_at, add_ld, o.n - c_first, next);
       // lanes of the fragments (four per thread) or the thread's own lane
       float lse[4], gw[4], bias[4];
       int lab[4];
@@ -1527,34 +1576,55 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             named_bar(2 + half, 128);
           }
         } else if (by_rows) {
+          constexpr int kJ = kPieces / 8;
           for (int c = c_first; c < o.n; c += c_step) {
             if (kSpread && (c >> 5) % a.split != part) continue;
-            Frag f;
-            if (sum) {
-              tmem_ld_frag(taddr + c, f);
-            } else {
+            FragOf<kJ> f;
+            const auto each = [&](auto fn) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) f.v[j][r][0] = f.v[j][r][1] = 0.f;
-            }
-            if (CG == 1) {
-              for (int k = 1; k < a.split; ++k) {
-                const float* q = part_of(k, c) + 2 * (lane & 3) * kPartLd + 32 * quad + (lane >> 2);
+                for (int r = 0; r < 4; ++r) f.v[j][r][0] = fn(f.v[j][r][0], r), f.v[j][r][1] = fn(f.v[j][r][1], r);
+            };
+            const auto sums = [&](int j0) {  // of 8 kJ columns from 8 j0 on
+              if (sum)
+                tmem_ld_frag(taddr + c + 8 * j0, f);
+              else
+                each([](float, int) { return 0.f; });
+              if (CG == 1) {
+                for (int k = 1; k < a.split; ++k) {
+                  const float* q = part_of(k, c) + (8 * j0 + 2 * (lane & 3)) * kPartLd + 32 * quad + (lane >> 2);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                  for (int j = 0; j < kJ; ++j)
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) {
-                    f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
-                    f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
-                  }
+                    for (int r = 0; r < 4; ++r) {
+                      f.v[j][r][0] += q[8 * j * kPartLd + 8 * r];
+                      f.v[j][r][1] += q[(8 * j + 1) * kPartLd + 8 * r];
+                    }
+                }
               }
-            }
+              if (is_store(EPI)) {
+                if (e.scale) {
+                  const float sc = *e.scale;
+                  each([&](float v, int) { return v * sc; });
+                }
+                if (e.bias) each([&](float v, int r) { return v + bias[r]; });
+              }
+            };
+            const auto act = [&] {
+              if (e.act == MM_ACT_SILU)
+                each([](float v, int) { return mm_silu(v); });
+              else if (e.act == MM_ACT_GELU)
+                each([](float v, int) { return mm_gelu(v); });
+              else if (e.act == MM_ACT_RELU)
+                each([](float v, int) { return mm_relu(v); });
+            };
             const int64_t row_at = first_row + (c - c_first);
+            if (kJ == 4) sums(0);
             if (EPI == MM_EPI_SOFTGRAD) {
               const int word = o.c0 + c + 2 * (lane & 3);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
+              for (int j = 0; j < kJ; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -1563,52 +1633,36 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
                     const float d = (__expf(f.v[j][r][q] * e.inv_t - lse[r]) - (word + 8 * j + q == lab[r] ? 1.f : 0.f)) * gw[r];
                     f.v[j][r][q] = gw[r] == 0.f ? 0.f : d;
                   }
+              frag_out(stage, quad, lane, f, p.f16);
             } else {
-              if (e.scale) {
-                const float sc = *e.scale;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] *= sc, f.v[j][r][1] *= sc;
-              }
-              if (e.bias) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] += bias[r], f.v[j][r][1] += bias[r];
-              }
               if (e.z) {
-                frag_out(stage, quad, lane, f, p.f16);
+#pragma unroll 1
+                for (int j0 = 0; j0 < 4; j0 += kJ) {
+                  if (kJ < 4) sums(j0);
+                  frag_out(stage, quad, lane, f, p.f16, j0);
+                }
                 named_bar(2 + half, 128);
                 rows.store(e.z, row_at * e.ldz + piece, e.ldz, o.n - c);
                 named_bar(2 + half, 128);
               }
-              if (e.act == MM_ACT_SILU) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_silu(f.v[j][r][0]), f.v[j][r][1] = mm_silu(f.v[j][r][1]);
-              } else if (e.act == MM_ACT_GELU) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_gelu(f.v[j][r][0]), f.v[j][r][1] = mm_gelu(f.v[j][r][1]);
-              } else if (e.act == MM_ACT_RELU) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                  for (int r = 0; r < 4; ++r) f.v[j][r][0] = mm_relu(f.v[j][r][0]), f.v[j][r][1] = mm_relu(f.v[j][r][1]);
-              }
+              if (kJ == 4) act();
               if (add) {
+                if (GEN) rows.load(add, add_at, add_ld, o.n - c, next);
                 rows.stage(next);
                 named_bar(2 + half, 128);
                 add_at += c_step * add_ld;
-                if (c + c_step < o.n) rows.load(add, add_at, add_ld, o.n - c - c_step, next);
-                frag_add(stage, quad, lane, f, p.f16);  // (each warp rereads and overwrites its own quarter only)
-                __syncwarp();
+                if (!GEN && c + c_step < o.n) rows.load(add, add_at, add_ld, o.n - c - c_step, next);
+              }
+#pragma unroll 1
+              for (int j0 = 0; j0 < 4; j0 += kJ) {
+                if (kJ < 4) sums(j0), act();
+                if (add) {
+                  frag_add(stage, quad, lane, f, p.f16, j0);  // (each warp rereads and overwrites its own quarter only)
+                  __syncwarp();
+                }
+                frag_out(stage, quad, lane, f, p.f16, j0);
               }
             }
-            frag_out(stage, quad, lane, f, p.f16);
             named_bar(2 + half, 128);
             rows.store(e.out, group_out + row_at * e.ld + piece, e.ld, o.n - c);
             named_bar(2 + half, 128);
@@ -1617,26 +1671,56 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
           const int l = l0 + 32 * quad + lane;
           for (int c = c_first; c < o.n; c += c_step) {
             if (kSpread && (c >> 5) % a.split != part) continue;
-            float v[32];
-            if (sum) {
-              tmem_ld32(taddr + c, v);
-            } else {
+            const bool accumulate = e.accumulate || (k && !folds);
+            if constexpr (GEN && is_store(EPI)) {
+              // What a weight gradient (to which nothing else is done) is added to comes 32 columns at a time, as in the aligned
+              // form: with 16 loads in flight 64 groups of 128 rows, n 2000, k 711 took 296 us, so 228.
+              if (accumulate) {
+                uint32_t old[32];
+                epi_fetch(p, o.g, l, o.c0 + c, min(32, o.n - c), old);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
-            }
-            if (CG == 1) {
-              for (int k = 1; k < a.split; ++k) {
-                const float* q = part_of(k, c) + 32 * quad + lane;
+                for (int h = 0; h < 32; h += kPieces) {
+                  float v[kPieces];
+                  if (sum) {
+                    tmem_ld(taddr + c + h, v);
+                  } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += q[j * kPartLd];
+                    for (int j = 0; j < kPieces; ++j) v[j] = 0.f;
+                  }
+#pragma unroll
+                  for (int j = 0; j < kPieces; ++j) {
+                    const uint32_t w = old[h + j];
+                    v[j] += e.out_f32 ? __uint_as_float(w) : p.f16 ? __half2float(__ushort_as_half((uint16_t)w)) : __uint_as_float(w << 16);
+                  }
+                  put(p, o.g, l, o.c0 + c + h, min(kPieces, o.n - c - h), v);
+                }
+                continue;
               }
             }
-            const int nv = min(32, o.n - c);
-            if (is_glu(EPI)) {
-              glu_out(p, l, o.c0 + c, nv, v);
-            } else {
-              epi_store(p, o.g, l, o.c0 + c, nv, e.accumulate || (k && !folds), v);
-              put(p, o.g, l, o.c0 + c, nv, v);
+#pragma unroll 1
+            for (int h = 0; h < 32; h += kPieces) {
+              const int nv = min(kPieces, o.n - c - h);
+              if (nv <= 0) break;
+              float v[kPieces];
+              if (sum) {
+                tmem_ld(taddr + c + h, v);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kPieces; ++j) v[j] = 0.f;
+              }
+              if (CG == 1) {
+                for (int k = 1; k < a.split; ++k) {
+                  const float* q = part_of(k, c) + h * kPartLd + 32 * quad + lane;
+#pragma unroll
+                  for (int j = 0; j < kPieces; ++j) v[j] += q[j * kPartLd];
+                }
+              }
+              if constexpr (is_glu(EPI)) {
+                glu_out(p, l, o.c0 + c, nv, v);
+              } else {
+                epi_store(p, o.g, l, o.c0 + c + h, nv, !GEN && accumulate, v);
+                put(p, o.g, l, o.c0 + c + h, nv, v);
+              }
             }
           }
         }
