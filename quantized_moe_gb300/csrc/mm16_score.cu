@@ -1,7 +1,8 @@
 // The small kernels around the head's scores: the lists of wanted words before the product, what its partials
 // say of each row after it (log probabilities, entropy, best words; the distillation's loss), and the places that the
-// distillation's gradient has at the listed words. One block of 256 threads for each row throughout: a row has up to 256
-// listed words, and 505 to 1010 partials of a vocabulary of 129280.
+// distillation's gradient has at the listed words. A block of 256 threads for each row (a row has up to 256 listed words, and
+// 505 to 1010 partials of a vocabulary of 129280), a warp for each of many rows in the search for the best words, a thread
+// for each listed word where the gradient's places are written.
 #include <type_traits>
 
 #include "mm16_small.cuh"
@@ -154,8 +155,8 @@ struct Picks {
 
 // Leaves the k largest keys of item(0..n-1) (all, if there are fewer) in `list` in their order, and returns their number.
 // The k-th largest of the threads' largest values, found bit by bit from the top, is reached by at least k items and as a
-// rule by few more: those are ranked by counting. Where more than kCandidates reach it (equal values, or k above the number
-// of threads) the k-th largest key itself is found, bit by bit over all items (for all rows and sizes at first: 2048 rows,
+// rule by few more: those are ranked by counting. Where more than kCandidates reach it (equal values) the k-th largest key
+// itself is found, bit by bit over all items (for all rows and sizes at first: 2048 rows,
 // 20 best, 68 us instead of 64). What item() reads may not be `list`.
 // A warp's threads hold up to HELD items each in registers, unrolled. A block (HELD 0) keeps them in shared memory under
 // rolled loops: with few rows it runs its code once, and the product has driven that out of the caches (one row, 8 best of
@@ -376,10 +377,14 @@ cudaError_t mm_sort_words(const int* words, int n, int vocab, int rows, int tile
   return launch(sort_words_kernel, dim3(rows), kThreads, s, words, n, vocab, tile, (vocab + tile - 1) / tile, want, first);
 }
 
-// A warp for each row where there are best words to find and rows enough to fill the SMs with warps: it needs no barriers (2048
-// rows of 129280 words, 20 best: 64 us, a block for each 83; but 512 rows of 32000 words, 8 best: 28 us, 20 by blocks).
+// A warp for each row where there are best words to find and rows enough to fill the SMs with warps: it needs no barriers (a call
+// of 2048 rows of 129280 words, d 64, 20 best: 281 us, with a block for each 307; 1024 rows, 8 best: 149 both; but the join of 512
+// rows of 32000 words, 8 best: 28 us, 20 by blocks). Up to 28 best words: the k-th largest of a warp's 32 values is then passed by
+// 32 log(32 / (32 - k)) = 67 items on average, at 31 by 111 and from 32 on by more than the candidates hold in most rows, and above
+// 32 there is no k-th (2048 rows of 129280 words, 33 best: 972 us, by blocks 335; 64 best 1902, 386; 151936 words, 32 best 494, 372).
+constexpr int kWarpTop = 28;
 cudaError_t mm_score_join(const MmScores& a, cudaStream_t s) {
-  if (a.top_k && a.rows >= 1024) return launch(score_join_warp_kernel, dim3((a.rows + kWarps - 1) / kWarps), kThreads, s, a);
+  if (a.top_k && a.top_k <= kWarpTop && a.rows >= 1024) return launch(score_join_warp_kernel, dim3((a.rows + kWarps - 1) / kWarps), kThreads, s, a);
   return launch(score_join_block_kernel, dim3(a.rows), kThreads, s, a);
 }
 

@@ -149,3 +149,13 @@ def test_groups_beside_wide_tiles(dtype, counts):
         assert torch.equal(z[lo:hi], ref.to(z.dtype)), e
         assert torch.equal(h[lo:hi], (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype)), e
     assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(1023, 3001, 28), (1024, 3001, 28), (1024, 3001, 29), (1031, 140001, 28), (2050, 999, 31), (1024, 40, 28)])
+def test_best_words_of_many_rows(rows, vocab, top):
+    """On both sides of where a warp instead of a block searches for a row's best words; equal logits in some rows."""
+    x, w = grid((rows, 64), "bf16", 1, 16, 2.0 ** -4), grid((vocab, 64), "bf16", 2, 20, 2.0 ** -6)
+    x[::7] = 0
+    tokens = torch.randint(-1, vocab, (rows, 2), generator=gen(3), device="cuda", dtype=torch.int32)
+    score_check(x, w, tokens, top, "bf16", 1.0, score(x, w, tokens, top))
+    assert api.ds4moe_ops_status() == 0
