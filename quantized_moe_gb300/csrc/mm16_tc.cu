@@ -117,10 +117,23 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// An arrival at a pair's leader. Without a release at cluster scope, which would wait for the warp's stores to global memory: what
-// it stands for is complete when it is issued (tensor memory read, tcgen05.wait::ld; a cleared end written, the proxy fence).
+// An arrival at a pair's leader that hands tensor memory back: no memory is passed on with it (tcgen05.wait::ld and the fence
+// before it order the reads), and a release at cluster scope would wait for the warp's stores to global memory.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+
+// One that passes on what the warp has written, or seen arrive, in its own CTA's shared memory, and the other side of it, of a phase
+// that is known to be complete: ordered at cluster scope, since MMAs that the leader issues read that memory, but for shared memory
+// alone (a release of everything waits for the epilogue's stores: 64 groups around 256 rows, 4096 x 4096 480 us so, 531).
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t addr) {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ void mbar_acquire_pair(uint64_t* b, uint32_t parity) {
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%0], %1;\n}\n"
+      "fence.acquire.sync_restrict::shared::cluster.cluster;\n" ::"r"(su32(b)), "r"(parity)
+      : "memory");
 }
 
 // Programmatic dependent launch: the next launch of the stream may set itself up while this one runs; nothing of
@@ -1114,6 +1127,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
             ok = false;
             break;
           }
+          if (CG == 2 && p.rag == MM_RAG_RED && (left & 15)) mbar_acquire_pair(clean + s, cleaned >> s & 1);
           if (left & 15) cleaned ^= 1u << s;
           tc_fence_after();
           const uint64_t da = a_desc + (uint32_t)(s * stage_bytes >> 4), db = b_desc + (uint32_t)(s * stage_bytes >> 4);
@@ -1156,8 +1170,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
     // cleared in both operands before the MMA reads them (0 * NaN would not vanish). A row is 128 bytes of a box.
     // The warp passes every stage in turn and arrives on its empty barrier too, so that the ring cannot lap it. In a pair
     // the other CTA's full barriers see ragged ends alone, and its cleaner waits for nothing else: neither can lap the other.
-    // The MMA waits for both cleaners (64 groups around 256 rows, 4096 x 4096: 642 us on single CTAs, 566 on pairs). Their arrival releases nothing: a cleared end is in shared memory once the proxy fence is passed
-    // (with a release at cluster scope 615).
+    // The MMA waits for both cleaners (64 groups around 256 rows, 4096 x 4096: 564 us on single CTAs, 480 on pairs).
     int s = 0;
     uint32_t ph = 0, cleaned = 0;
     bool ok = true;
@@ -1187,7 +1200,7 @@ __global__ void __launch_bounds__(GEN ? kThreads + 32 * kLoaders : kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (CG == 2 && rank) {
-            mbar_arrive_cluster(mapa(su32(clean + s), 0));
+            mbar_arrive_leader(mapa(su32(clean + s), 0));
           } else {
             if (left & 15) mbar_arrive(clean + s);
             mbar_arrive(empty + s);
