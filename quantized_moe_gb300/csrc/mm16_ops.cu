@@ -552,9 +552,10 @@ struct DistillSpace {
   }
   int64_t total(int64_t rows, int64_t piece) const { return dz + 2 * up(rows, 8) * piece; }
 };
-// Its pieces of the vocabulary: of up to 512 rows as many words as make 64 MB of dz, which still come from L2 (128 rows, 129280 words,
-// d 2048: 605 us in pieces of 16384, 383 in one; 512 rows, d 1024: 623, 497 in pieces of 32768 to 65536). Beyond, the longer sums of
-// dx, in several accumulators, cost more than fewer launches save (1024 rows, 64000 words, d 1024: 431 us, 505 in halves).
+// Its pieces of the vocabulary: of up to 512 rows as many words as make 64 MB of dz, which still come from L2 (inputs in turns: 128 rows,
+// 129280 words, d 2048 604 us in pieces of 16384, 383 in one; 512 rows, d 512 496, 335; 16 rows, 32000 words, d 1024 121, 91; but 256
+// rows, 32000 words, d 4096 261, 292, and 512 rows, 129280 words, d 2048 940, 962). Beyond, the longer sums of dx, in several
+// accumulators, cost more than fewer launches save (1024 rows, 64000 words, d 1024: 431 us, 505 in halves).
 constexpr int64_t kDistillRows = 512, kDistillDz = (int64_t)1 << 26;
 int64_t distill_piece(int64_t rows) {
   return rows > kDistillRows ? kPieceMax : std::max<int64_t>(kPieceMax, kDistillDz / 2 / up(rows, 8) / kPieceMin * kPieceMin);

@@ -16,7 +16,7 @@
 // stage in parallel); one thread of warp 1 issues the MMAs (the leader's, in a pair); warp 2 clears what a
 // ragged end of the reduction leaves in a stage; warps 4-11 run the epilogue of one tile while the next one's main loop
 // fills the other accumulator. Where an operand's address or row distance is not a multiple of 16
-// bytes, eight loader warps (12-19) read it with ordinary loads and write the same swizzled layout.
+// bytes, 16 loader warps (12-27) read it with ordinary loads and write the same swizzled layout.
 // Few tiles share their reduction out over a cluster of CTAs, which join their sums in shared memory.
 //
 // The gated block is a product whose lanes are 16 gate features, the same 16 up features, and so on, so that a thread of the
@@ -1812,9 +1812,6 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 int g_sms[64] = {}, g_pairs[64] = {};  // per device: SMs, and pairs that can be resident at once
 int g_clusters[64][kMaxSpread + 1] = {};  // and clusters of so many CTAs
 
-// 4D map with boxes of 64 contiguous elements, 128-byte swizzle: (contiguous index, row, -, group) with box_rows rows;
-// or, for an MN-major operand whose width is a multiple of 64, (index in a block of 64, row, block, group) with
-// `blocks` blocks of BK rows, which one copy lays one after the other.
 // A gated block's weights, n a multiple of 16: (reduction, row of 16, gate or up, 16 rows, group); one copy brings four times 16
 // gate rows and the same 16 up rows.
 bool make_glu_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t red, uint64_t n, uint64_t groups) {
@@ -1828,6 +1825,9 @@ bool make_glu_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t red, uin
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 4D map with boxes of 64 contiguous elements, 128-byte swizzle: (contiguous index, row, -, group) with box_rows rows;
+// or, for an MN-major operand whose width is a multiple of 64, (index in a block of 64, row, block, group) with
+// `blocks` blocks of BK rows, which one copy lays one after the other.
 bool make_map(CUtensorMap* m, const MmOperand& o, int f16, uint64_t inner, uint64_t rows, uint64_t groups, uint32_t box_rows, int blocks) {
   const cuuint64_t row = (cuuint64_t)o.ld * 2;
   const cuuint64_t dims[4] = {blocks > 1 ? 64 : inner, rows, blocks > 1 ? inner / 64 : 1, groups};
