@@ -24,7 +24,7 @@
 //
 // What bounds it (GB300, measured): the experts' products stream their weights (256 experts, 32768
 // rows, n 2048, k 4096: 0.70-0.72 ms = 6.5-6.8 TB/s, 96-99 % of the copy bandwidth, for y and dx; the
-// weight gradients, 4.3 GB of results, 0.80 ms = 5.9 TB/s: their way through shared memory beside the MMAs' operands);
+// weight gradients, 4.3 GB of results, 0.79 ms = 5.9 TB/s: their busiest unit is shared memory, for operands and results, 72 %);
 // large dense products the tensor pipe and the SMs' L2 reads (2048 x 129280 x 4096: 1.12 ms = 1.94
 // PFLOP/s, the rate of a large library product; 4096^3 with its epilogue 94 us = 1.46 PFLOP/s, of
 // which a seventh is the last, partial round and the launch); single tokens the launch and one pass of
@@ -315,7 +315,7 @@ struct Tile {
 // ends where the next one begins, or is empty if that lies before it); for ragged columns pref[g], the running
 // count of the groups' column tiles.
 // WIDE: a group of at most `widest` rows has one tile, which beyond kAccCols takes both accumulators; a larger one has tiles of
-// kAccCols, whose accumulators take turns (64 groups of 20 and 400 rows in turn, 2048 x 4096: 222 us, in tiles of 320 and 80
+// kAccCols, whose accumulators take turns (64 groups of 20 and 400 rows in turn, 2048 x 4096: 231 us, in tiles of 320 and 80
 // columns 300).
 template <int CG, bool WIDE>
 __device__ __forceinline__ Tile tile_of(const TcArgs& a, const int* lo_of, const int* pref, int widest, int t, int share) {
