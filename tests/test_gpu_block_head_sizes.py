@@ -159,3 +159,17 @@ def test_best_words_of_many_rows(rows, vocab, top):
     tokens = torch.randint(-1, vocab, (rows, 2), generator=gen(3), device="cuda", dtype=torch.int32)
     score_check(x, w, tokens, top, "bf16", 1.0, score(x, w, tokens, top))
     assert api.ds4moe_ops_status() == 0
+
+
+@pytest.mark.parametrize("average,spread", [(190, 120), (300, 30), (256, 5), (400, 200)])
+def test_a_thousand_groups_beside_wide_tiles(average, spread):
+    counts, n, k = ragged(1024, average, spread), 72, 64
+    rows, g = sum(counts), len(counts)
+    x, w, off = whole((rows, k), "bf16", 1), whole((g, 2 * n, k), "bf16", 2), offsets(counts)
+    h, z, clean = block(x, w, off, n, "relu", "bf16")
+    y = torch.full((rows, 2 * n), 7.0, dtype=x.dtype, device="cuda")
+    api.ds4moe_grouped_mm(x, w, off, y, rows, 2 * n, k, g, "bf16", stream=stream())
+    ref = torch.cat([x[lo:hi].double() @ w[e].double().T for e, lo, hi in groups_of(counts)])
+    assert clean and torch.equal(z, ref.to(z.dtype)) and torch.equal(y, z)
+    assert torch.equal(h, (ref[:, :n].clamp(min=0) * ref[:, n:]).to(h.dtype))
+    assert api.ds4moe_ops_status() == 0
